@@ -26,15 +26,17 @@ STATUS_NAMES = {
     4: "FA_ERR_DTYPE", 5: "FA_ERR_ALIGN", 6: "FA_ERR_SCALE", 7: "FA_ERR_ARCH",
     8: "FA_ERR_WORKSPACE", 9: "FA_ERR_CUDA", 10: "FA_ERR_WATCHDOG",
     11: "FA_ERR_SEQ_LEN", 12: "FA_ERR_ALIAS", 13: "FA_ERR_SPLITS",
+    14: "FA_ERR_PAGE",
 }
 (FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEAD_DIM, FA_ERR_DTYPE, FA_ERR_ALIGN, FA_ERR_SCALE, FA_ERR_ARCH,
  FA_ERR_WORKSPACE, FA_ERR_CUDA, FA_ERR_WATCHDOG, FA_ERR_SEQ_LEN, FA_ERR_ALIAS,
- FA_ERR_SPLITS) = range(1, 14)
+ FA_ERR_SPLITS, FA_ERR_PAGE) = range(1, 15)
 
 _lock = threading.Lock()
 _lib = None
 
 _vp, _i, _f, _u, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint, ctypes.c_size_t
+_ll = ctypes.c_longlong
 _SIGNATURES = {
     "fa_prefill": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
     "fa_prefill_ex": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _i, _vp]),
@@ -60,6 +62,15 @@ _SIGNATURES = {
     "fa_decode_choose_splits": (_i, [_i, _i, _i, _i]),
     "fa_decode_chunk_len": (_i, [_i, _i]),
     "fa_decode_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_cache_append": (_i, [_vp, _vp, _vp, _vp, _vp, _ll, _ll, _ll, _ll, _vp, _i, _vp, _vp, _vp,
+                             _i, _i, _i, _vp, _i, _i, _i, _vp]),
+    "fa_decode_paged": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "fa_prefill_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _f, _i,
+                              _vp, _sz, _vp]),
+    "fa_decode_shared": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _f, _i, _vp, _sz,
+                              _vp]),
+    "fa_paged_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_shared_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "fa_status_string": (ctypes.c_char_p, [_i]),
     "fa_last_cuda_error": (_i, []),
     "fa_device_status": (_i, [_i]),
@@ -68,6 +79,13 @@ _SIGNATURES = {
     "fa_read_probe": (_i, [_vp, _sz, _vp, _vp]),
     "fa_version": (_i, []),
 }
+
+
+class PagedCacheArg(ctypes.Structure):
+    """fa_paged_cache of include/fa.h."""
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("page_stride", _ll), ("head_stride", _ll),
+                ("slot_stride", _ll), ("num_pages", _i), ("num_heads", _i), ("page_size", _i),
+                ("head_dim", _i), ("dtype", _i)]
 
 
 class FaError(RuntimeError):
@@ -210,6 +228,46 @@ def fa_decode_chunk_len(max_len, num_splits) -> int:
 
 def fa_decode_workspace_bytes(B, H, max_len, d, num_splits) -> int:
     return load().fa_decode_workspace_bytes(B, H, max_len, d, num_splits)
+
+
+def fa_cache_append(cache, q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, page_table,
+                    max_pages, seq_lens, cu_seqlens, positions, B, Hq, total, rope, max_positions,
+                    rope_dim, interleaved, stream=0) -> int:
+    return load().fa_cache_append(ctypes.byref(cache), q, k, v, q_out, q_stride, k_stride, v_stride,
+                                  q_out_stride, page_table, max_pages, seq_lens, cu_seqlens,
+                                  positions, B, Hq, total, rope, max_positions, rope_dim,
+                                  int(interleaved), stream)
+
+
+def fa_decode_paged(cache, q, out, page_table, max_pages, seq_lens, B, Hq, scale, out_dtype,
+                    workspace=None, workspace_bytes=0, stream=0) -> int:
+    return load().fa_decode_paged(ctypes.byref(cache), q, out, page_table, max_pages, seq_lens, B,
+                                  Hq, scale, out_dtype, workspace, workspace_bytes, stream)
+
+
+def fa_prefill_paged(cache, q, out, lse, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq,
+                     total_q, max_seqlen_q, causal, scale, out_dtype, workspace=None,
+                     workspace_bytes=0, stream=0) -> int:
+    return load().fa_prefill_paged(ctypes.byref(cache), q, out, lse, page_table, max_pages,
+                                   seq_lens, cu_seqlens_q, B, Hq, total_q, max_seqlen_q,
+                                   int(causal), scale, out_dtype, workspace, workspace_bytes,
+                                   stream)
+
+
+def fa_decode_shared(cache, q, out, prefix_table, max_prefix_pages, prefix_len, page_table,
+                     max_pages, seq_lens, B, Hq, scale, out_dtype, workspace=None,
+                     workspace_bytes=0, stream=0) -> int:
+    return load().fa_decode_shared(ctypes.byref(cache), q, out, prefix_table, max_prefix_pages,
+                                   prefix_len, page_table, max_pages, seq_lens, B, Hq, scale,
+                                   out_dtype, workspace, workspace_bytes, stream)
+
+
+def fa_paged_workspace_bytes(Hq, Hkv, max_seqlen_q, d, device=-1) -> int:
+    return load().fa_paged_workspace_bytes(Hq, Hkv, max_seqlen_q, d, device)
+
+
+def fa_shared_workspace_bytes(B, Hq, Hkv, d, device=-1) -> int:
+    return load().fa_shared_workspace_bytes(B, Hq, Hkv, d, device)
 
 
 def status_string(status: int) -> str:
@@ -471,4 +529,244 @@ def decode(q, k_cache, v_cache, seq_lens, scale: float | None = None, out_dtype=
                        _stream_handle(q.device))
     if rc != FA_OK:
         raise FaError(rc, "fa_decode_gqa")
+    return out
+
+
+# ---------------------------------------------------------------- paged cache
+def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cuda"):
+    """Cosines and sines of p * base^(-2 i / rope_dim) as cache_append takes them: fp32
+    [positions, rope_dim], a row's cosines first.  The angles are computed in 64 bits."""
+    torch = _torch()
+    freq = base ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device) / rope_dim)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def _pages(k_pages, v_pages):
+    """fa_paged_cache of two [pages, heads, slots, d] tensors (any strides, the same for both)."""
+    if not (k_pages.is_cuda and v_pages.is_cuda):
+        raise ValueError("k_pages and v_pages must be CUDA tensors")
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected [pages, heads, slots, d]")
+    if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride() or \
+            v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
+        raise ValueError("v_pages must have the shape, strides, dtype and device of k_pages")
+    pages, heads, slots, d = k_pages.shape
+    page_stride, head_stride, slot_stride, one = k_pages.stride()
+    if one != 1:
+        raise ValueError("the channels of a slot must be contiguous")
+    return PagedCacheArg(k_pages.data_ptr(), v_pages.data_ptr(), page_stride, head_stride, slot_stride,
+                         pages, heads, slots, d, dtype_code(k_pages.dtype))
+
+
+def _check_on(device, **tensors):
+    """int32 arrays of the device: contiguous and where the cache is."""
+    torch = _torch()
+    for name, t in tensors.items():
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, as the cache is")
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected torch.int32")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _check_rows(name, t, heads, k_pages):
+    """[tokens, heads, d] rows in the cache's type; only the tokens may have a stride."""
+    d = k_pages.shape[3]
+    if t.device != k_pages.device or t.dtype != k_pages.dtype:
+        raise ValueError(f"{name} must have the dtype and device of the cache")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, "
+                         f"{'heads' if heads is None else heads}, {d}]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+
+
+def _on_device(device, call):
+    """call(stream) with `device` current, on its current stream."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        return call(_stream_handle(device))
+    with torch.cuda.device(device):
+        return call(_stream_handle(device))
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    _check_cuda("workspace", workspace)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=None, rope=None,
+                 interleaved: bool = False, positions=None, out=None):
+    """Put the keys and values of new tokens into their slots of a paged cache and give q and k
+    their rotary positions on the way; returns the turned q (None when q is None).
+
+    q [T, Hq, d] (or None), k, v [T, Hkv, d]: a token's heads contiguous, tokens any stride
+    apart, as slices of one fused projection are.  k_pages, v_pages [pages, Hkv, slots, d], any
+    strides; page_table int32 [B, max_pages].  seq_lens int32 [B]: the lengths with the new
+    tokens in.  cu_seqlens int32 [B + 1]: the sequences' token offsets; None: one token each.
+    rope: rope_table(...)'s rows, as wide as the channels that turn, or None.  positions int32
+    [T]: the rotary positions where they are not the positions in the sequence.  out may be q.
+    """
+    torch = _torch()
+    cache = _pages(k_pages, v_pages)
+    device = k_pages.device
+    _check_rows("k", k, cache.num_heads, k_pages)
+    _check_rows("v", v, cache.num_heads, k_pages)
+    total = k.shape[0]
+    if v.shape[0] != total:
+        raise ValueError(f"v has {v.shape[0]} tokens, k has {total}")
+    _check_on(device, page_table=page_table, seq_lens=seq_lens)
+    B = seq_lens.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B}, max_pages]")
+    if cu_seqlens is not None:
+        _check_on(device, cu_seqlens=cu_seqlens)
+        if cu_seqlens.shape != (B + 1,):
+            raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected [{B + 1}]")
+    if positions is not None:
+        _check_on(device, positions=positions)
+        if positions.shape != (total,):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{total}]")
+    max_positions = rope_dim = 0
+    if rope is not None:
+        if rope.device != device or rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 [positions, rope_dim] tensor beside the cache")
+        max_positions, rope_dim = rope.shape
+    Hq = q_ptr = out_ptr = q_stride = out_stride = 0
+    if q is not None:
+        _check_rows("q", q, None, k_pages)
+        if q.shape[0] != total:
+            raise ValueError(f"q has {q.shape[0]} tokens, k has {total}")
+        Hq = q.shape[1]
+        if out is None:
+            # rows behind the last sequence stay what they are: unwritten memory
+            out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        else:
+            _check_rows("out", out, Hq, k_pages)
+            if out.shape[0] != total:
+                raise ValueError(f"out has {out.shape[0]} tokens, expected {total}")
+        q_ptr, out_ptr, q_stride, out_stride = q.data_ptr(), out.data_ptr(), q.stride(0), out.stride(0)
+    elif out is not None:
+        raise ValueError("out without q")
+    if total == 0:
+        return out
+    rc = _on_device(device, lambda stream: fa_cache_append(
+        cache, q_ptr or None, k.data_ptr(), v.data_ptr(), out_ptr or None, q_stride, k.stride(0), v.stride(0),
+        out_stride, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(),
+        None if positions is None else positions.data_ptr(), B, Hq, total,
+        rope.data_ptr() if rope_dim else None, max_positions, rope_dim, interleaved, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_cache_append")
+    return out
+
+
+def _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype, out):
+    """The checks, defaults and output that the paged attention calls have in common."""
+    torch = _torch()
+    cache = _pages(k_pages, v_pages)
+    device = k_pages.device
+    d = cache.head_dim
+    if q.device != device or q.dtype != k_pages.dtype:
+        raise ValueError("q must have the dtype and device of the cache")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _check_on(device, page_table=page_table, seq_lens=seq_lens)
+    B = seq_lens.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B}, max_pages]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out_dtype = q.dtype if out_dtype is None else out_dtype
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=device)
+    else:
+        _check_cuda("out", out, q.shape, out_dtype)
+        if out.device != device:
+            raise ValueError("out must be on the device of the cache")
+    return cache, device, B, scale, dtype_code(out_dtype), out
+
+
+def _decode_rows(q, B, d):
+    """Query heads of q [B, Hq, d] or [B, Hq, 1, d]."""
+    if not (q.dim() == 3 or (q.dim() == 4 and q.shape[2] == 1)) or q.shape[0] != B or q.shape[-1] != d:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [{B}, Hq, {d}] or [{B}, Hq, 1, {d}]")
+    return q.shape[1]
+
+
+def decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale: float | None = None,
+                 out_dtype=None, workspace=None, out=None):
+    """One query token per sequence over the first seq_lens[b] tokens of its pages.
+
+    q [B, Hq, d] or [B, Hq, 1, d]; k_pages, v_pages [pages, Hkv, slots, d], any strides;
+    page_table int32 [B, max_pages]; seq_lens int32 [B].  Returns rows shaped as q.
+    """
+    cache, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
+                                                     out_dtype, out)
+    Hq = _decode_rows(q, B, cache.head_dim)
+    ws, ws_bytes = _workspace(workspace)
+    rc = _on_device(device, lambda stream: fa_decode_paged(
+        cache, q.data_ptr(), out.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+        seq_lens.data_ptr(), B, Hq, scale, code, ws, ws_bytes, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_decode_paged")
+    return out
+
+
+def prefill_paged(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q: int,
+                  causal: bool = False, scale: float | None = None, out_dtype=None, workspace=None,
+                  out=None, lse=None):
+    """Chunks of query tokens over a paged cache that already holds their keys.
+
+    q [T, Hq, d] with sequence b's tokens at cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (int32
+    [B + 1]); causal queries are the last positions of their sequence's seq_lens[b] tokens.
+    lse: optional fp32 [T, Hq] that receives the row log-sum-exp.  Returns [T, Hq, d]; rows
+    outside every sequence are not written.
+    """
+    torch = _torch()
+    cache, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
+                                                     out_dtype, out)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, Hq, {cache.head_dim}]")
+    total, Hq = q.shape[0], q.shape[1]
+    _check_on(device, cu_seqlens_q=cu_seqlens_q)
+    if cu_seqlens_q.shape != (B + 1,):
+        raise ValueError(f"cu_seqlens_q has shape {tuple(cu_seqlens_q.shape)}, expected [{B + 1}]")
+    if lse is not None:
+        _check_cuda("lse", lse, (total, Hq), torch.float32)
+    if total == 0:
+        return out
+    ws, ws_bytes = _workspace(workspace)
+    rc = _on_device(device, lambda stream: fa_prefill_paged(
+        cache, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), B,
+        Hq, total, int(max_seqlen_q), causal, scale, code, ws, ws_bytes, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_prefill_paged")
+    return out
+
+
+def decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens,
+                  scale: float | None = None, out_dtype=None, workspace=None, out=None):
+    """decode_paged for a batch that shares a prefix: every row sees the first prefix_len tokens
+    (int32 [1], on the device) of prefix_table's pages (int32 [n]), then its own.  The prefix is
+    read once for the whole batch.
+    """
+    cache, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
+                                                     out_dtype, out)
+    Hq = _decode_rows(q, B, cache.head_dim)
+    _check_on(device, prefix_table=prefix_table, prefix_len=prefix_len)
+    if prefix_table.dim() != 1 or prefix_len.numel() != 1:
+        raise ValueError("prefix_table must be [pages] and prefix_len [1]")
+    ws, ws_bytes = _workspace(workspace)
+    rc = _on_device(device, lambda stream: fa_decode_shared(
+        cache, q.data_ptr(), out.data_ptr(), prefix_table.data_ptr(), prefix_table.shape[0],
+        prefix_len.data_ptr(), page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), B, Hq,
+        scale, code, ws, ws_bytes, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_decode_shared")
     return out

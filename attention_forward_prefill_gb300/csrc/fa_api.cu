@@ -136,6 +136,7 @@ const char *fa_status_string(int status) {
         case FA_ERR_SEQ_LEN: return "a device-resident sequence length was out of range (clamped)";
         case FA_ERR_ALIAS: return "output overlaps an input";
         case FA_ERR_SPLITS: return "num_splits out of range";
+        case FA_ERR_PAGE: return "a page table entry in use was outside the cache";
         default: return "unknown status";
     }
 }
@@ -144,13 +145,17 @@ int fa_last_cuda_error(void) { return t_last_cuda_error; }
 
 int fa_device_status(int reset) {
     if (cudaDeviceSynchronize() != cudaSuccess) return -1;
-    const int a = read_prefill_status(reset), b = read_decode_status(reset),
-              c = read_backward_status(reset);
-    if (a < 0 || b < 0 || c < 0) return -1;
+    const int words[5] = {read_prefill_status(reset), read_decode_status(reset), read_backward_status(reset),
+                          read_paged_status(reset), read_append_status(reset)};
+    int first = 0;
+    for (int v : words) {
+        if (v < 0) return -1;
+        if (!first) first = v;
+    }
     // a watchdog report wins over a clamped length
-    for (int v : {a, b, c})
+    for (int v : words)
         if (v == FA_ERR_WATCHDOG) return v;
-    return a ? a : (b ? b : c);
+    return first;
 }
 
 int fa_pool_stats(long long *out, int reset_high) {

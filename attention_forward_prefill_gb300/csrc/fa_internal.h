@@ -102,9 +102,47 @@ struct BackwardLaunch {
 
 int launch_backward(const BackwardLaunch &a, cudaStream_t stream);
 
+// Attention over a paged cache (fa_decode_paged, fa_prefill_paged, and both steps
+// of fa_decode_shared).
+struct PagedLaunch {
+    fa_paged_cache c;
+    const void *q;              // [total_q][Hq][d]
+    void *out;                  // [total_q][Hq][d] in out_dtype
+    float *lse;                 // optional [total_q][Hq]
+    const float *init_o;        // optional earlier result of the same rows over other keys: fp32 rows
+    const float *init_lse;      //   and their natural-log log-sum-exp
+    const int32_t *page_table;  // [B][max_pages]
+    const int32_t *seq_lens;    // [B]
+    const int32_t *cu_q;        // [B + 1], or null: max_q tokens for every sequence
+    int B, Hq, total_q, max_q, max_pages;
+    int causal;
+    float scale;
+    int out_dtype;
+    void *scratch;              // paged_scratch_bytes(max_q * group, d, SMs), 16-byte aligned
+    int grid;
+};
+
+size_t paged_scratch_bytes(long long rows, int d, int num_sms);
+int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
+
+struct AppendLaunch {
+    fa_paged_cache c;
+    const void *q, *k, *v;      // [total][H][d], tokens the given strides (elements) apart
+    void *q_out;
+    long long q_stride, k_stride, v_stride, q_out_stride;
+    const int32_t *page_table, *seq_lens, *cu_seqlens, *positions;
+    int B, Hq, total, max_pages;
+    const float *rope;          // [max_positions][rope_dim]: cosines, then sines
+    int max_positions, rope_dim, interleaved;
+};
+
+int launch_append(const AppendLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
+
 // Device-side watchdog words (one per kernel translation unit).
 int read_prefill_status(int reset);
 int read_decode_status(int reset);
 int read_backward_status(int reset);
+int read_paged_status(int reset);
+int read_append_status(int reset);
 
 }  // namespace fa

@@ -57,7 +57,9 @@ typedef enum {
     FA_ERR_SEQ_LEN = 11,   /* a device-resident length was out of range and was
                               clamped (reported by fa_device_status only)         */
     FA_ERR_ALIAS = 12,     /* out overlaps an input                               */
-    FA_ERR_SPLITS = 13     /* num_splits outside [0, ceil(max_len / 64)]          */
+    FA_ERR_SPLITS = 13,    /* num_splits outside [0, ceil(max_len / 64)]          */
+    FA_ERR_PAGE = 14       /* a page table entry in use was outside the cache
+                              (reported by fa_device_status only)                 */
 } fa_status;
 
 /* Flags for fa_prefill_gqa and the other prefill forms that take `flags`. */
@@ -410,6 +412,133 @@ int fa_decode_noalloc(const void *q, const void *k_cache, const void *v_cache,
 /* Bytes of the static scratch array behind fa_decode_noalloc. */
 size_t fa_decode_noalloc_max_bytes(void);
 
+/* ---------------------------------------------------------------- paged cache
+ * Keys and values kept in pages of page_size token slots, so that sequences of
+ * any length share one pool: token j of sequence b lives in slot j % page_size
+ * of page page_table[b][j / page_size].  The calls below fill such a cache and
+ * attend over it; they run on the same terms as the calls above (pointers of
+ * the device, 16-byte aligned, work enqueued on `stream`, nothing kept after
+ * the call, status codes for bad arguments before any CUDA call).
+ *
+ * k_pages and v_pages are [num_pages][num_heads][page_size][head_dim] with any
+ * strides, in elements (the same for both): the channels of a slot are
+ * contiguous, strides are multiples of 8 and no two elements share a place
+ * (FA_ERR_ALIGN, FA_ERR_SHAPE).  [page][slot][head][channel] storage, or K and
+ * V in one tensor, are strides like any other.  The stride of an extent of 1 is
+ * ignored.
+ *   page_size : a power of two, 16 .. 2^20
+ *   page tables : int32 [B][max_pages] rows; entries behind a sequence's last
+ *     token are never read.  max_pages * page_size must stay below 2^30.  An
+ *     entry in use that is not a page of the cache is recorded as FA_ERR_PAGE
+ *     (fa_device_status): its tokens read as zero keys and values, and are not
+ *     written by fa_cache_append.
+ *   lengths : device int32, clamped to [0, max_pages * page_size] and recorded
+ *     as FA_ERR_SEQ_LEN when they were outside.
+ * Slots behind a sequence's last token may hold anything, NaN included.
+ */
+typedef struct {
+    void *k_pages, *v_pages;
+    long long page_stride, head_stride, slot_stride;
+    int num_pages, num_heads, page_size, head_dim;
+    fa_dtype dtype; /* FA_F16 or FA_BF16: of the cache, and of q, k, v */
+} fa_paged_cache;
+
+/*
+ * Append: the keys and values of `total` new tokens go into their slots, and q
+ * and k are given their rotary positions on the way.
+ *   q, q_out : [total][Hq][d]; k, v : [total][num_heads][d]; a token's heads are
+ *     contiguous and tokens lie *_stride elements apart (multiples of 8), so
+ *     slices of one fused projection are fine.  q_out may be q (in place, same
+ *     stride).  Hq == 0 with q == q_out == NULL appends only.
+ *   seq_lens : device int32 [B], the lengths with the new tokens in (what the
+ *     attention calls below then take): token i of a sequence's n new ones has
+ *     position seq_lens[b] - n + i.
+ *   cu_seqlens : device int32 [B + 1], the sequences' token offsets (n of
+ *     sequence b is cu_seqlens[b + 1] - cu_seqlens[b], 0 allowed); NULL when
+ *     total == B, one token each.  Tokens at and after cu_seqlens[B] are left
+ *     alone, in q_out too.
+ *   rope : device fp32 [max_positions][rope_dim]: the cosines of a position's
+ *     rope_dim / 2 angles, then their sines.  The first rope_dim channels turn
+ *     in pairs (x1, x2) -> (x1 cos - x2 sin, x1 sin + x2 cos), channels i and
+ *     i + rope_dim / 2, or 2 i and 2 i + 1 with `interleaved`.  rope_dim is a
+ *     multiple of 16 up to d; 0 turns nothing (rope NULL allowed).
+ *   positions : device int32 [total], the tokens' rotary positions; NULL takes
+ *     their positions in the sequence.  One outside [0, max_positions) is
+ *     clamped and recorded as FA_ERR_SEQ_LEN.
+ * Arithmetic is fp32, each value is rounded once.  A token whose position is
+ * outside [0, max_pages * page_size) is not written (FA_ERR_SEQ_LEN recorded).
+ * Two tokens with the same slot are the caller's error.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEAD_DIM, FA_ERR_DTYPE, FA_ERR_ALIGN,
+ * FA_ERR_ALIAS (the pages, or q_out other than q, overlap an input), FA_ERR_ARCH,
+ * FA_ERR_CUDA.
+ */
+int fa_cache_append(const fa_paged_cache *cache, const void *q, const void *k,
+                    const void *v, void *q_out, long long q_stride,
+                    long long k_stride, long long v_stride,
+                    long long q_out_stride, const int32_t *page_table,
+                    int max_pages, const int32_t *seq_lens,
+                    const int32_t *cu_seqlens, const int32_t *positions, int B,
+                    int Hq, int total, const float *rope, int max_positions,
+                    int rope_dim, int interleaved, void *stream);
+
+/*
+ * Decode over pages: one query token per sequence.
+ *   q, out : [B][Hq][d], Hq a multiple of the cache's heads (query head h reads
+ *     head h / (Hq / num_heads)); out in out_dtype
+ *   seq_lens : device int32 [B]; a sequence of length 0 gives zero rows
+ *   workspace : NULL (the library's stream-ordered pool) or at least
+ *     fa_paged_workspace_bytes(Hq, num_heads, 1, d, -1) bytes, which one call
+ *     at a time may use
+ * The lengths are read on the device and the work is cut there, so a captured
+ * call follows lengths and tables that change between replays.  The same
+ * arguments and lengths give the same bits on every run.
+ */
+int fa_decode_paged(const fa_paged_cache *cache, const void *q, void *out,
+                    const int32_t *page_table, int max_pages,
+                    const int32_t *seq_lens, int B, int Hq, float scale,
+                    fa_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
+ * Prefill over pages: chunks of query tokens, the keys (theirs included) in the
+ * cache already.
+ *   q, out : [total_q][Hq][d], sequence b's tokens at [cu_seqlens_q[b],
+ *     cu_seqlens_q[b + 1]) (device int32 [B + 1]; empty sequences allowed, each
+ *     at most max_seqlen_q); rows outside every sequence are left alone
+ *   lse : NULL or fp32 [total_q][Hq], natural-log row log-sum-exp
+ *   causal : the queries are the last positions: token i of nq sees keys
+ *     j <= seq_lens[b] - nq + i.  A row that sees no key gives zeros (lse -inf).
+ *   workspace : NULL or fa_paged_workspace_bytes(Hq, num_heads, max_seqlen_q, d, -1)
+ * Offsets outside [0, total_q], decreasing, or longer than max_seqlen_q are
+ * clamped and recorded as FA_ERR_SEQ_LEN.
+ */
+int fa_prefill_paged(const fa_paged_cache *cache, const void *q, void *out,
+                     float *lse, const int32_t *page_table, int max_pages,
+                     const int32_t *seq_lens, const int32_t *cu_seqlens_q, int B,
+                     int Hq, int total_q, int max_seqlen_q, int causal,
+                     float scale, fa_dtype out_dtype, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Decode of a batch that shares a prefix: row b attends to the first
+ * *prefix_len tokens of prefix_table's pages and then to its own seq_lens[b]
+ * tokens in page_table[b] (either may be 0).  The prefix's keys and values are
+ * read once for the whole batch.  prefix_table : int32 [max_prefix_pages];
+ * prefix_len : device int32; workspace : NULL or
+ * fa_shared_workspace_bytes(B, Hq, num_heads, d, -1); the rest as fa_decode_paged.
+ */
+int fa_decode_shared(const fa_paged_cache *cache, const void *q, void *out,
+                     const int32_t *prefix_table, int max_prefix_pages,
+                     const int32_t *prefix_len, const int32_t *page_table,
+                     int max_pages, const int32_t *seq_lens, int B, int Hq,
+                     float scale, fa_dtype out_dtype, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the calls above on `device` (< 0 = the current device);
+ * 0 on bad arguments or when the device cannot be queried. */
+size_t fa_paged_workspace_bytes(int Hq, int Hkv, int max_seqlen_q, int d, int device);
+size_t fa_shared_workspace_bytes(int B, int Hq, int Hkv, int d, int device);
+
 /* Static text for a status code ("unknown status" for other values). */
 const char *fa_status_string(int status);
 
@@ -417,8 +546,9 @@ const char *fa_status_string(int status);
 int fa_last_cuda_error(void);
 
 /* Device-side status word of the current device: 0, FA_ERR_WATCHDOG after a
- * kernel's bounded wait ran out (this wins when both were recorded), or
- * FA_ERR_SEQ_LEN after a kernel clamped a device-resident length.
+ * kernel's bounded wait ran out (this wins when several were recorded),
+ * FA_ERR_SEQ_LEN after a kernel clamped a device-resident length, or FA_ERR_PAGE
+ * after a page table entry in use was outside the cache.
  * Synchronises the device.  If reset is nonzero the word is cleared.  Returns
  * a negative value if it cannot be read. */
 int fa_device_status(int reset);
