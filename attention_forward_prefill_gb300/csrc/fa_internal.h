@@ -118,11 +118,10 @@ struct PagedLaunch {
     int causal;
     float scale;
     int out_dtype;
-    void *scratch;              // paged_scratch_bytes(max_q * group, d, SMs), 16-byte aligned
-    int grid;
+    void *scratch;              // paged_scratch_bytes(max_q, group, d, SMs), 16-byte aligned
 };
 
-size_t paged_scratch_bytes(long long rows, int d, int num_sms);
+size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms);
 int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
 
 struct AppendLaunch {
@@ -143,6 +142,7 @@ int read_prefill_status(int reset);
 int read_decode_status(int reset);
 int read_backward_status(int reset);
 int read_paged_status(int reset);
+int read_tiles_status(int reset);
 int read_append_status(int reset);
 
 }  // namespace fa

@@ -6,7 +6,7 @@
 // token j lives in page page_table[b][j / page_size], slot j % page_size.  A
 // sequence with nq query tokens gives each kv head nq * G query rows
 // (G = query heads per kv head), row r = (token r / G, head r % G), cut into
-// blocks of RB rows.  A unit = (sequence, kv head, row block); it costs one
+// blocks of block_rows.  A unit = (sequence, kv head, row block); it costs one
 // step per key tile its rows can see (at least one, so that a unit without
 // keys still writes its rows).  The W steps of the whole call, in the order
 // (sequence, kv head, block), are cut into gridDim.x equal ranges, one per
@@ -42,10 +42,11 @@ struct PagedParams {
     int total_q, max_q;
     int max_pages, max_len;
     int num_pages, page_shift;
+    int block_rows;         // query rows of a unit
     int causal;             // query token i of nq sees keys j <= len - nq + i
     float scale_log2;       // scale * log2(e)
     int out_dtype;
-    float *part_o;          // [gridDim.x][2][RB][D]
+    float *part_o;          // [gridDim.x][2][RB][D], RB >= block_rows the kernel's slot size
     float *part_ml;         // [gridDim.x][2][RB][2]: m (log2 units), l
     int4 *open;             // [gridDim.x][2]: the unit a CTA leaves unfinished
 };
@@ -86,30 +87,32 @@ __device__ __forceinline__ bool paged_seq_bad(const PagedParams &p, int b) {
     return bad;
 }
 
-// Key tiles (TK keys each) that row block rb must visit, at least one.
-template <int RB, int TK>
-__device__ __forceinline__ int paged_tiles(const PagedParams &p, const SeqView &s, int rb) {
+// Key tiles (TK keys each) that rows up to last_row of a sequence, or row block rb, must
+// visit: at least one.
+template <int TK>
+__device__ __forceinline__ int paged_tiles_to_row(const PagedParams &p, const SeqView &s, int last_row) {
     int seen = s.len;
-    if (p.causal) {
-        const int last = min(s.nq - 1, (rb * RB + RB - 1) / p.G);
-        seen = max(0, s.len - s.nq + last + 1);
-    }
+    if (p.causal) seen = max(0, s.len - s.nq + min(s.nq - 1, last_row / p.G) + 1);
     return max(1, (seen + TK - 1) / TK);
 }
 
-template <int RB>
+template <int TK>
+__device__ __forceinline__ int paged_tiles(const PagedParams &p, const SeqView &s, int rb) {
+    return paged_tiles_to_row<TK>(p, s, rb * p.block_rows + p.block_rows - 1);
+}
+
 __device__ __forceinline__ int paged_blocks(const PagedParams &p, const SeqView &s) {
-    return static_cast<int>((static_cast<long long>(s.nq) * p.G + RB - 1) / RB);
+    return (s.nq * p.G + p.block_rows - 1) / p.block_rows;
 }
 
 // Steps of one kv head of a sequence.
-template <int RB, int TK>
+template <int TK>
 __device__ __forceinline__ long long paged_head_steps(const PagedParams &p, const SeqView &s) {
-    const int n = paged_blocks<RB>(p, s);
+    const int n = paged_blocks(p, s);
     if (n == 0) return 0;
-    if (!p.causal || n == 1) return static_cast<long long>(n) * paged_tiles<RB, TK>(p, s, n - 1);
+    if (!p.causal || n == 1) return static_cast<long long>(n) * paged_tiles<TK>(p, s, n - 1);
     long long sum = 0;
-    for (int rb = 0; rb < n; ++rb) sum += paged_tiles<RB, TK>(p, s, rb);
+    for (int rb = 0; rb < n; ++rb) sum += paged_tiles<TK>(p, s, rb);
     return sum;
 }
 
@@ -123,7 +126,7 @@ struct PagedStart {
 };
 
 // The whole CTA (NT threads) adds up the sequences' steps and finds its range.
-template <int RB, int TK, int NT>
+template <int TK, int NT>
 __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st, long long *warp_sum, int *status) {
     constexpr int NW = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -132,7 +135,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
     long long mine = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
-        mine += paged_head_steps<RB, TK>(p, paged_seq(p, b)) * p.Hkv;
+        mine += paged_head_steps<TK>(p, paged_seq(p, b)) * p.Hkv;
         bad |= paged_seq_bad(p, b);
     }
     if (bad && blockIdx.x == 0) atomicCAS(status, 0, static_cast<int>(FA_ERR_SEQ_LEN));
@@ -165,7 +168,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
         long long rem = first - before;
         int b = b0;
         for (; b < b1 - 1; ++b) {
-            const long long c = paged_head_steps<RB, TK>(p, paged_seq(p, b)) * p.Hkv;
+            const long long c = paged_head_steps<TK>(p, paged_seq(p, b)) * p.Hkv;
             if (rem < c) break;
             rem -= c;
         }
@@ -184,7 +187,7 @@ struct PagedPiece {
 };
 
 // Walks a CTA's pieces in order.
-template <int RB, int TK>
+template <int TK>
 struct PagedCursor {
     SeqView s;
     int b, hk, rb, blocks, j;
@@ -195,18 +198,18 @@ struct PagedCursor {
         if (left <= 0) return;
         b = st.b;
         s = paged_seq(p, b);
-        blocks = paged_blocks<RB>(p, s);
-        const long long per_head = paged_head_steps<RB, TK>(p, s);
+        blocks = paged_blocks(p, s);
+        const long long per_head = paged_head_steps<TK>(p, s);
         hk = static_cast<int>(st.rem / per_head);
         long long rem = st.rem - hk * per_head;
         if (!p.causal) {
-            const int c = paged_tiles<RB, TK>(p, s, 0);
+            const int c = paged_tiles<TK>(p, s, 0);
             rb = static_cast<int>(rem / c);
             j = static_cast<int>(rem - static_cast<long long>(rb) * c);
             return;
         }
         for (rb = 0; rb < blocks - 1; ++rb) {
-            const int c = paged_tiles<RB, TK>(p, s, rb);
+            const int c = paged_tiles<TK>(p, s, rb);
             if (rem < c) break;
             rem -= c;
         }
@@ -216,13 +219,13 @@ struct PagedCursor {
     // The next piece; false when the range is used up.  cost: the whole unit's steps.
     __device__ __forceinline__ bool next(const PagedParams &p, PagedPiece &u, int &cost) {
         if (left <= 0) return false;
-        cost = paged_tiles<RB, TK>(p, s, rb);
+        cost = paged_tiles<TK>(p, s, rb);
         u.b = b;
         u.t0 = s.t0;
         u.nq = s.nq;
         u.len = s.len;
         u.hk = hk;
-        u.row0 = rb * RB;
+        u.row0 = rb * p.block_rows;
         u.j0 = j;
         u.j1 = static_cast<int>(min(static_cast<long long>(cost), j + left));
         u.kind = u.j0 > 0 ? 2 : (u.j1 < cost ? 1 : 0);
@@ -234,7 +237,7 @@ struct PagedCursor {
                 hk = 0;
                 do {  // steps are left, so a later sequence has rows
                     s = paged_seq(p, ++b);
-                    blocks = paged_blocks<RB>(p, s);
+                    blocks = paged_blocks(p, s);
                 } while (blocks == 0);
             }
         }
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     if (a.x < 0) return;
     const int4 b = p.open[2 * c + 1];
     const int n = a.x - c + 1;  // pieces
-    const int rows = static_cast<int>(min(static_cast<long long>(RB), static_cast<long long>(b.x) * p.G - a.w));
+    const int rows = min(p.block_rows, b.x * p.G - a.w);
     auto rec = [&](int k, int r) { return (static_cast<size_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; };
     for (int r = blockIdx.y * kJoinRows + warp; r < min(rows, (blockIdx.y + 1) * kJoinRows); r += kJoinWarps) {
         float M = -INFINITY;
@@ -404,6 +407,33 @@ inline int make_page_map(CUtensorMap *map, const void *base, const fa_paged_cach
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
     return FA_OK;
+}
+
+int launch_paged_tiles(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream_t stream);
+
+// Launch attributes of the paged kernels; `early`: may start before the kernels
+// ahead of it in the stream have finished (it waits for them where it must).
+struct PagedConfig {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[1];
+    PagedConfig(dim3 grid, int threads, size_t smem, bool early, cudaStream_t stream) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        c.gridDim = grid;
+        c.blockDim = dim3(threads);
+        c.dynamicSmemBytes = smem;
+        c.stream = stream;
+        c.attrs = attr;
+        c.numAttrs = early ? 1 : 0;
+    }
+    PagedConfig(const PagedConfig &) = delete;
+};
+
+template <int D, int RB>
+int launch_join(const PagedParams &p, int grid, cudaStream_t stream) {
+    PagedConfig cfg(dim3(grid, (p.block_rows + kJoinRows - 1) / kJoinRows), kJoinWarps * 32, 0, true, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, p);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
 }  // namespace fa

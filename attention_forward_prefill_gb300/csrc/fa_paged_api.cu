@@ -83,8 +83,8 @@ int check_attention(const Attention &a) {
     if (a.B < 1 || a.Hq < 1 || a.Hq % a.c->num_heads != 0 || a.max_pages < 1 || a.total < 0 || a.max_q < 1)
         return FA_ERR_SHAPE;
     if (static_cast<long long>(a.max_pages) * a.c->page_size > INT_MAX / 2 ||
-        static_cast<long long>(a.B) * a.Hq > INT_MAX || static_cast<long long>(a.total) * a.Hq > INT_MAX ||
-        static_cast<long long>(a.max_q) * a.Hq > INT_MAX)
+        static_cast<long long>(a.B) * a.Hq > INT_MAX / 2 || static_cast<long long>(a.total) * a.Hq > INT_MAX / 2 ||
+        static_cast<long long>(a.max_q) * a.Hq > INT_MAX / 2)
         return FA_ERR_SHAPE;
     if (a.out_dtype != FA_F16 && a.out_dtype != FA_BF16 && a.out_dtype != FA_F32) return FA_ERR_DTYPE;
     if (off16(a.q) || off16(a.out) || off4(a.lse) || off4(a.page_table) || off4(a.seq_lens) || off4(a.cu) ||
@@ -118,7 +118,7 @@ PagedLaunch launch_of(const Attention &a, int causal) {
     l.B = a.B;
     l.Hq = a.Hq;
     l.total_q = a.total;
-    l.max_q = std::min(a.max_q, a.total);
+    l.max_q = a.max_q;
     l.max_pages = a.max_pages;
     l.causal = causal ? 1 : 0;
     l.scale = a.scale;
@@ -162,9 +162,9 @@ int run_attention(const Attention &a, int causal, void *workspace, size_t worksp
     PagedLaunch l = launch_of(a, causal);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Scratch s(st);
-    const long long rows = static_cast<long long>(l.max_q) * (a.Hq / a.c->num_heads);
-    if ((rc = s.take(workspace, workspace_bytes, paged_scratch_bytes(rows, a.c->head_dim, dev.num_sms))) != FA_OK)
-        return rc;
+    // (a workspace is sized for max_seqlen_q, which fewer tokens than that do not change)
+    const size_t need = paged_scratch_bytes(a.max_q, a.Hq / a.c->num_heads, a.c->head_dim, dev.num_sms);
+    if ((rc = s.take(workspace, workspace_bytes, need)) != FA_OK) return rc;
     l.scratch = s.ptr;
     return s.done(launch_paged(l, dev, st));
 }
@@ -176,8 +176,8 @@ struct SharedScratch {
     size_t first, second, rows, lse, total;
     SharedScratch(int B, int Hq, int group, int d, int num_sms) {
         first = 0;
-        second = align256(paged_scratch_bytes(static_cast<long long>(B) * group, d, num_sms));
-        rows = second + align256(paged_scratch_bytes(group, d, num_sms));
+        second = align256(paged_scratch_bytes(B, group, d, num_sms));
+        rows = second + align256(paged_scratch_bytes(1, group, d, num_sms));
         lse = rows + align256(static_cast<size_t>(B) * Hq * d * 4);
         total = lse + align256(static_cast<size_t>(B) * Hq * 4);
     }
@@ -289,7 +289,7 @@ int fa_cache_append(const fa_paged_cache *cache, const void *q, const void *k, c
 size_t fa_paged_workspace_bytes(int Hq, int Hkv, int max_seqlen_q, int d, int device) {
     if (!head_sizes_ok(Hq, Hkv, d) || max_seqlen_q < 1) return 0;
     const int sms = sms_of(device);
-    return sms < 0 ? 0 : paged_scratch_bytes(static_cast<long long>(max_seqlen_q) * (Hq / Hkv), d, sms);
+    return sms < 0 ? 0 : paged_scratch_bytes(max_seqlen_q, Hq / Hkv, d, sms);
 }
 
 size_t fa_shared_workspace_bytes(int B, int Hq, int Hkv, int d, int device) {

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
-    paged_plan<RB, kTile, kPagedThreads>(p, *start, warp_sum, &g_paged_status);
+    paged_plan<kTile, kPagedThreads>(p, *start, warp_sum, &g_paged_status);
     uint32_t units = 0, tiles = 0;  // handed over / taken so far
 
     if (warp == kConsumers) {
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         // lane -> (operand, slab, box) of a tile's copies
         const int my_box = lane % boxes, my_slab = lane / boxes % (D / 64), my_op = lane / boxes / (D / 64);
         bool ok = true;
-        PagedCursor<RB, kTile> cur;
+        PagedCursor<kTile> cur;
         cur.begin(p, *start);
         PagedPiece u;
         int cost = 0;
@@ -398,72 +398,57 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 }
 
 template <int D, int RT, bool BF16>
-int launch_rows(const PagedLaunch &a, const CUtensorMap &mk, const CUtensorMap &mv, const PagedParams &p,
-                cudaStream_t stream) {
+int launch_rows(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream_t stream) {
     using L = PagedLayout<D, RT>;
-    const auto kernel = paged_rows_kernel<D, RT, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
-    if (e != cudaSuccess) return cuda_fail(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.grid);
-    cfg.blockDim = dim3(kPagedThreads);
-    cfg.dynamicSmemBytes = L::kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.init_o ? 1 : 0;  // the second step of a shared prefix starts under the first
-    e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e);
-    cfg.gridDim = dim3(a.grid, (L::kRows + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, L::kRows>, p);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e);
-    return FA_OK;
-}
-
-// Row tiles of 16 per unit: as many as the largest sequence fills, up to four.
-int row_tiles(long long rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
-
-template <int D, bool BF16>
-int launch_paged_d(const PagedLaunch &a, const CUtensorMap &mk, const CUtensorMap &mv, const PagedParams &p,
-                   cudaStream_t stream) {
-    switch (row_tiles(static_cast<long long>(a.max_q) * p.G)) {
-        case 1: return launch_rows<D, 1, BF16>(a, mk, mv, p, stream);
-        case 2: return launch_rows<D, 2, BF16>(a, mk, mv, p, stream);
-        default: return launch_rows<D, 4, BF16>(a, mk, mv, p, stream);
-    }
-}
-
-}  // namespace
-
-// Two CTAs per SM, or one per step where the call has fewer.
-int paged_grid(const PagedLaunch &a, int num_sms) {
-    const long long rows = static_cast<long long>(a.max_q) * (a.Hq / a.c.num_heads);
-    const int block = 16 * row_tiles(rows);
-    const long long max_len = static_cast<long long>(a.max_pages) * a.c.page_size;
-    const long long steps = static_cast<long long>(a.B) * a.c.num_heads * ((rows + block - 1) / block) *
-                            std::max(1LL, (max_len + kTile - 1) / kTile);
-    return static_cast<int>(std::min<long long>(2LL * num_sms, steps));
-}
-
-// Partial rows, (m, l) and unit notes of one attention over pages, for the largest grid.
-size_t paged_scratch_bytes(long long rows, int d, int num_sms) {
-    const size_t slots = static_cast<size_t>(2) * num_sms * 2;
-    const size_t rec = slots * 16 * row_tiles(rows);
-    return rec * d * 4 + rec * 8 + slots * sizeof(int4);
-}
-
-int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
     CUtensorMap mk, mv;
     int rc;
     if ((rc = make_page_map(&mk, a.c.k_pages, a.c, kTile)) != FA_OK) return rc;
     if ((rc = make_page_map(&mv, a.c.v_pages, a.c, kTile)) != FA_OK) return rc;
+    const auto kernel = paged_rows_kernel<D, RT, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    if (e != cudaSuccess) return cuda_fail(e);
+    PagedConfig cfg(grid, kPagedThreads, L::kSmemBytes, a.init_o != nullptr, stream);
+    e = cudaLaunchKernelEx(&cfg.c, kernel, mk, mv, p);
+    if (e != cudaSuccess) return cuda_fail(e);
+    return launch_join<D, L::kRows>(p, grid, stream);
+}
+
+template <int D, bool BF16>
+int launch_rows_d(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream_t stream) {
+    switch (p.block_rows) {
+        case 16: return launch_rows<D, 1, BF16>(a, p, grid, stream);
+        case 32: return launch_rows<D, 2, BF16>(a, p, grid, stream);
+        default: return launch_rows<D, 4, BF16>(a, p, grid, stream);
+    }
+}
+
+// How a call runs, from its sizes alone.
+struct PagedPlan {
+    bool tiles;      // 128-row tensor-memory tiles (paged_tiles_kernel), else paged_rows_kernel
+    int block_rows;  // query rows of a unit
+    int slot_rows;   // rows of a partial slot
+    int tile;        // keys per step
+    int per_sm;      // CTAs per SM
+};
+
+PagedPlan plan_paged(int max_q, int group) {
+    const long long rows = static_cast<long long>(max_q) * group;
+    if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256, 128, 1};
+    const int rb = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    return {false, rb, rb, kTile, 2};
+}
+
+}  // namespace
+
+// Partial rows, (m, l) and unit notes of one attention over pages, for the largest grid.
+size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms) {
+    const PagedPlan pl = plan_paged(max_q, group);
+    const size_t slots = static_cast<size_t>(pl.per_sm) * num_sms * 2;
+    const size_t rec = slots * pl.slot_rows;
+    return rec * d * 4 + rec * 8 + slots * sizeof(int4);
+}
+
+int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
     PagedParams p;
     p.q = static_cast<const uint16_t *>(a.q);
     p.out = a.out;
@@ -488,20 +473,23 @@ int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t strea
     p.causal = a.causal;
     p.scale_log2 = a.scale * kLog2e;
     p.out_dtype = a.out_dtype;
-    const long long rows = static_cast<long long>(a.max_q) * p.G;
-    const size_t slots = static_cast<size_t>(2) * dev.num_sms * 2;
-    const size_t rec = slots * 16 * row_tiles(rows);
+    const PagedPlan pl = plan_paged(a.max_q, p.G);
+    p.block_rows = pl.block_rows;
+    const int most = pl.per_sm * dev.num_sms;
+    const size_t slots = static_cast<size_t>(most) * 2, rec = slots * pl.slot_rows;
     p.part_o = static_cast<float *>(a.scratch);
     p.part_ml = p.part_o + rec * a.c.head_dim;
     p.open = reinterpret_cast<int4 *>(p.part_ml + rec * 2);
-    PagedLaunch b = a;
-    b.grid = paged_grid(a, dev.num_sms);
+    // no more CTAs than the call can have steps
+    const long long rows = static_cast<long long>(a.max_q) * p.G;
+    const long long steps = static_cast<long long>(a.B) * p.Hkv * ((rows + pl.block_rows - 1) / pl.block_rows) *
+                            ((p.max_len + pl.tile - 1) / pl.tile);
+    const int grid = static_cast<int>(std::min<long long>(most, steps));
+    if (pl.tiles) return launch_paged_tiles(a, p, grid, stream);
     const bool bf16 = a.c.dtype == FA_BF16;
     if (a.c.head_dim == 64)
-        return bf16 ? launch_paged_d<64, true>(b, mk, mv, p, stream) : launch_paged_d<64, false>(b, mk, mv, p, stream);
-    if (a.c.head_dim == 128)
-        return bf16 ? launch_paged_d<128, true>(b, mk, mv, p, stream) : launch_paged_d<128, false>(b, mk, mv, p, stream);
-    return FA_ERR_HEAD_DIM;
+        return bf16 ? launch_rows_d<64, true>(a, p, grid, stream) : launch_rows_d<64, false>(a, p, grid, stream);
+    return bf16 ? launch_rows_d<128, true>(a, p, grid, stream) : launch_rows_d<128, false>(a, p, grid, stream);
 }
 
 int read_paged_status(int reset) {
