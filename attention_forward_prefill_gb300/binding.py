@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -302,9 +303,15 @@ def fa_read_probe(src, nbytes, xor_out, stream=0) -> int:
 
 
 # ---------------------------------------------------------------- torch calls
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def dtype_code(dt) -> int:
@@ -542,60 +549,86 @@ def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cud
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
+# A call of a few microseconds on the GPU is bound by what happens here on the host, so the calls
+# below test what they need in one expression and look for the reason only when it is false.
+_PACK_CACHE = struct.Struct("@PPqqqiiiii4x").pack  # fa_paged_cache, its tail padding with it
+_codes = {}
+
+
+def _code_of(dtype) -> int:
+    code = _codes.get(dtype)
+    if code is None:
+        code = _codes[dtype] = dtype_code(dtype)
+    return code
+
+
 def _pages(k_pages, v_pages):
-    """fa_paged_cache of two [pages, heads, slots, d] tensors (any strides, the same for both)."""
-    if not (k_pages.is_cuda and v_pages.is_cuda):
-        raise ValueError("k_pages and v_pages must be CUDA tensors")
-    if k_pages.dim() != 4:
-        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected [pages, heads, slots, d]")
-    if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride() or \
-            v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
+    """(fa_paged_cache as bytes, heads, d) of two [pages, heads, slots, d] tensors (any strides, the
+    same for both)."""
+    shape, stride, dtype = k_pages.shape, k_pages.stride(), k_pages.dtype
+    if not (k_pages.is_cuda and len(shape) == 4 and stride[3] == 1 and v_pages.shape == shape and
+            v_pages.stride() == stride and v_pages.dtype == dtype and v_pages.device == k_pages.device):
+        if not (k_pages.is_cuda and v_pages.is_cuda):
+            raise ValueError("k_pages and v_pages must be CUDA tensors")
+        if len(shape) != 4:
+            raise ValueError(f"k_pages has shape {tuple(shape)}, expected [pages, heads, slots, d]")
+        if stride[3] != 1:
+            raise ValueError("the channels of a slot must be contiguous")
         raise ValueError("v_pages must have the shape, strides, dtype and device of k_pages")
-    pages, heads, slots, d = k_pages.shape
-    page_stride, head_stride, slot_stride, one = k_pages.stride()
-    if one != 1:
-        raise ValueError("the channels of a slot must be contiguous")
-    return PagedCacheArg(k_pages.data_ptr(), v_pages.data_ptr(), page_stride, head_stride, slot_stride,
-                         pages, heads, slots, d, dtype_code(k_pages.dtype))
+    pages, heads, slots, d = shape
+    return _PACK_CACHE(k_pages.data_ptr(), v_pages.data_ptr(), stride[0], stride[1], stride[2], pages, heads,
+                       slots, d, _code_of(dtype)), heads, d
 
 
-def _check_on(device, **tensors):
-    """int32 arrays of the device: contiguous and where the cache is."""
-    torch = _torch()
-    for name, t in tensors.items():
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, as the cache is")
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected torch.int32")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _check_ints(device, name, t, shape):
+    """int32 arrays of the device: contiguous and where the cache is; a None in `shape` is any size."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, as the cache is")
+    if t.dtype != _torch().int32:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected torch.int32")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"[{', '.join('any' if n is None else str(n) for n in shape)}]")
 
 
-def _check_rows(name, t, heads, k_pages):
-    """[tokens, heads, d] rows in the cache's type; only the tokens may have a stride."""
-    d = k_pages.shape[3]
-    if t.device != k_pages.device or t.dtype != k_pages.dtype:
-        raise ValueError(f"{name} must have the dtype and device of the cache")
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens, "
-                         f"{'heads' if heads is None else heads}, {d}]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+def _check_rows(name, t, tokens, heads, k_pages):
+    """[tokens, heads, d] rows in the cache's type, of which only the tokens may have a stride; returns
+    it and the number of heads."""
+    shape, stride, d = t.shape, t.stride(), k_pages.shape[3]
+    if not (t.dtype == k_pages.dtype and t.device == k_pages.device and len(shape) == 3 and shape[0] == tokens and
+            shape[2] == d and stride[2] == 1 and (stride[1] == d or shape[1] == 1) and
+            (heads is None or shape[1] == heads)):
+        if t.device != k_pages.device or t.dtype != k_pages.dtype:
+            raise ValueError(f"{name} must have the dtype and device of the cache")
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != d or (heads is not None and shape[1] != heads):
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected [{tokens}, "
+                             f"{'heads' if heads is None else heads}, {d}]")
         raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return stride[0], shape[1]
 
 
-def _on_device(device, call):
-    """call(stream) with `device` current, on its current stream."""
+def _run(name, device, *args):
+    """The library's call `name` with `device` current, on its current stream."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
-        return call(_stream_handle(device))
-    with torch.cuda.device(device):
-        return call(_stream_handle(device))
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != FA_OK:
+        raise FaError(rc, name)
 
 
-def _workspace(workspace):
+def _workspace(workspace, device):
     if workspace is None:
         return None, 0
     _check_cuda("workspace", workspace)
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, as the cache is")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -609,93 +642,82 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
     strides; page_table int32 [B, max_pages].  seq_lens int32 [B]: the lengths with the new
     tokens in.  cu_seqlens int32 [B + 1]: the sequences' token offsets; None: one token each.
     rope: rope_table(...)'s rows, as wide as the channels that turn, or None.  positions int32
-    [T]: the rotary positions where they are not the positions in the sequence.  out may be q.
+    [T]: the rotary positions where they are not the positions in the sequence.  out may be q;
+    its rows behind the last sequence are not written.
     """
     torch = _torch()
-    cache = _pages(k_pages, v_pages)
+    cache, Hkv, _ = _pages(k_pages, v_pages)
     device = k_pages.device
-    _check_rows("k", k, cache.num_heads, k_pages)
-    _check_rows("v", v, cache.num_heads, k_pages)
     total = k.shape[0]
-    if v.shape[0] != total:
-        raise ValueError(f"v has {v.shape[0]} tokens, k has {total}")
-    _check_on(device, page_table=page_table, seq_lens=seq_lens)
-    B = seq_lens.shape[0]
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B}, max_pages]")
-    if cu_seqlens is not None:
-        _check_on(device, cu_seqlens=cu_seqlens)
-        if cu_seqlens.shape != (B + 1,):
-            raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected [{B + 1}]")
-    if positions is not None:
-        _check_on(device, positions=positions)
-        if positions.shape != (total,):
-            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{total}]")
+    k_stride, _ = _check_rows("k", k, total, Hkv, k_pages)
+    v_stride, _ = _check_rows("v", v, total, Hkv, k_pages)
+    B = seq_lens.numel()
+    _check_ints(device, "seq_lens", seq_lens, (B,))
+    _check_ints(device, "page_table", page_table, (B, None))
+    cu_ptr = pos_ptr = rope_ptr = None
     max_positions = rope_dim = 0
+    if cu_seqlens is not None:
+        _check_ints(device, "cu_seqlens", cu_seqlens, (B + 1,))
+        cu_ptr = cu_seqlens.data_ptr()
+    if positions is not None:
+        _check_ints(device, "positions", positions, (total,))
+        pos_ptr = positions.data_ptr()
     if rope is not None:
         if rope.device != device or rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous float32 [positions, rope_dim] tensor beside the cache")
         max_positions, rope_dim = rope.shape
-    Hq = q_ptr = out_ptr = q_stride = out_stride = 0
+        if rope_dim:
+            rope_ptr = rope.data_ptr()
+    Hq = q_stride = out_stride = 0
+    q_ptr = out_ptr = None
     if q is not None:
-        _check_rows("q", q, None, k_pages)
-        if q.shape[0] != total:
-            raise ValueError(f"q has {q.shape[0]} tokens, k has {total}")
-        Hq = q.shape[1]
+        q_stride, Hq = _check_rows("q", q, total, None, k_pages)
         if out is None:
-            # rows behind the last sequence stay what they are: unwritten memory
             out = torch.empty(q.shape, dtype=q.dtype, device=device)
+            out_stride = Hq * q.shape[2]
         else:
-            _check_rows("out", out, Hq, k_pages)
-            if out.shape[0] != total:
-                raise ValueError(f"out has {out.shape[0]} tokens, expected {total}")
-        q_ptr, out_ptr, q_stride, out_stride = q.data_ptr(), out.data_ptr(), q.stride(0), out.stride(0)
+            out_stride, _ = _check_rows("out", out, total, Hq, k_pages)
+        q_ptr, out_ptr = q.data_ptr(), out.data_ptr()
     elif out is not None:
         raise ValueError("out without q")
-    if total == 0:
-        return out
-    rc = _on_device(device, lambda stream: fa_cache_append(
-        cache, q_ptr or None, k.data_ptr(), v.data_ptr(), out_ptr or None, q_stride, k.stride(0), v.stride(0),
-        out_stride, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
-        None if cu_seqlens is None else cu_seqlens.data_ptr(),
-        None if positions is None else positions.data_ptr(), B, Hq, total,
-        rope.data_ptr() if rope_dim else None, max_positions, rope_dim, interleaved, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_cache_append")
+    if total:
+        _run("fa_cache_append", device, cache, q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, q_stride, k_stride,
+             v_stride, out_stride, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), cu_ptr, pos_ptr,
+             B, Hq, total, rope_ptr, max_positions, rope_dim, 1 if interleaved else 0)
     return out
 
 
 def _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype, out):
     """The checks, defaults and output that the paged attention calls have in common."""
     torch = _torch()
-    cache = _pages(k_pages, v_pages)
+    cache, _, d = _pages(k_pages, v_pages)
     device = k_pages.device
-    d = cache.head_dim
-    if q.device != device or q.dtype != k_pages.dtype:
-        raise ValueError("q must have the dtype and device of the cache")
-    if not q.is_contiguous():
+    if not (q.dtype == k_pages.dtype and q.device == device and q.is_contiguous()):
+        if q.device != device or q.dtype != k_pages.dtype:
+            raise ValueError("q must have the dtype and device of the cache")
         raise ValueError("q must be contiguous")
-    _check_on(device, page_table=page_table, seq_lens=seq_lens)
-    B = seq_lens.shape[0]
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{B}, max_pages]")
+    B = seq_lens.numel()
+    _check_ints(device, "seq_lens", seq_lens, (B,))
+    _check_ints(device, "page_table", page_table, (B, None))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out_dtype = q.dtype if out_dtype is None else out_dtype
+    if out_dtype is None:
+        out_dtype = q.dtype
     if out is None:
         out = torch.empty(q.shape, dtype=out_dtype, device=device)
     else:
         _check_cuda("out", out, q.shape, out_dtype)
         if out.device != device:
             raise ValueError("out must be on the device of the cache")
-    return cache, device, B, scale, dtype_code(out_dtype), out
+    return cache, d, device, B, scale, _code_of(out_dtype), out
 
 
 def _decode_rows(q, B, d):
     """Query heads of q [B, Hq, d] or [B, Hq, 1, d]."""
-    if not (q.dim() == 3 or (q.dim() == 4 and q.shape[2] == 1)) or q.shape[0] != B or q.shape[-1] != d:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected [{B}, Hq, {d}] or [{B}, Hq, 1, {d}]")
-    return q.shape[1]
+    shape = q.shape
+    if not (len(shape) == 3 or (len(shape) == 4 and shape[2] == 1)) or shape[0] != B or shape[-1] != d:
+        raise ValueError(f"q has shape {tuple(shape)}, expected [{B}, Hq, {d}] or [{B}, Hq, 1, {d}]")
+    return shape[1]
 
 
 def decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale: float | None = None,
@@ -705,15 +727,11 @@ def decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale: float | None 
     q [B, Hq, d] or [B, Hq, 1, d]; k_pages, v_pages [pages, Hkv, slots, d], any strides;
     page_table int32 [B, max_pages]; seq_lens int32 [B].  Returns rows shaped as q.
     """
-    cache, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
-                                                     out_dtype, out)
-    Hq = _decode_rows(q, B, cache.head_dim)
-    ws, ws_bytes = _workspace(workspace)
-    rc = _on_device(device, lambda stream: fa_decode_paged(
-        cache, q.data_ptr(), out.data_ptr(), page_table.data_ptr(), page_table.shape[1],
-        seq_lens.data_ptr(), B, Hq, scale, code, ws, ws_bytes, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_decode_paged")
+    cache, d, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype,
+                                                        out)
+    ws, ws_bytes = _workspace(workspace, device)
+    _run("fa_decode_paged", device, cache, q.data_ptr(), out.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+         seq_lens.data_ptr(), B, _decode_rows(q, B, d), scale, code, ws, ws_bytes)
     return out
 
 
@@ -727,26 +745,23 @@ def prefill_paged(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_s
     lse: optional fp32 [T, Hq] that receives the row log-sum-exp.  Returns [T, Hq, d]; rows
     outside every sequence are not written.
     """
-    torch = _torch()
-    cache, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
-                                                     out_dtype, out)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, Hq, {cache.head_dim}]")
-    total, Hq = q.shape[0], q.shape[1]
-    _check_on(device, cu_seqlens_q=cu_seqlens_q)
-    if cu_seqlens_q.shape != (B + 1,):
-        raise ValueError(f"cu_seqlens_q has shape {tuple(cu_seqlens_q.shape)}, expected [{B + 1}]")
+    cache, d, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype,
+                                                        out)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, Hq, {d}]")
+    total, Hq, _ = q.shape
+    _check_ints(device, "cu_seqlens_q", cu_seqlens_q, (B + 1,))
+    lse_ptr = None
     if lse is not None:
-        _check_cuda("lse", lse, (total, Hq), torch.float32)
-    if total == 0:
-        return out
-    ws, ws_bytes = _workspace(workspace)
-    rc = _on_device(device, lambda stream: fa_prefill_paged(
-        cache, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), B,
-        Hq, total, int(max_seqlen_q), causal, scale, code, ws, ws_bytes, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_prefill_paged")
+        _check_cuda("lse", lse, (total, Hq), _torch().float32)
+        if lse.device != device:
+            raise ValueError("lse must be on the device of the cache")
+        lse_ptr = lse.data_ptr()
+    if total:
+        ws, ws_bytes = _workspace(workspace, device)
+        _run("fa_prefill_paged", device, cache, q.data_ptr(), out.data_ptr(), lse_ptr, page_table.data_ptr(),
+             page_table.shape[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), B, Hq, total, int(max_seqlen_q),
+             1 if causal else 0, scale, code, ws, ws_bytes)
     return out
 
 
@@ -756,17 +771,12 @@ def decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq
     (int32 [1], on the device) of prefix_table's pages (int32 [n]), then its own.  The prefix is
     read once for the whole batch.
     """
-    cache, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
-                                                     out_dtype, out)
-    Hq = _decode_rows(q, B, cache.head_dim)
-    _check_on(device, prefix_table=prefix_table, prefix_len=prefix_len)
-    if prefix_table.dim() != 1 or prefix_len.numel() != 1:
-        raise ValueError("prefix_table must be [pages] and prefix_len [1]")
-    ws, ws_bytes = _workspace(workspace)
-    rc = _on_device(device, lambda stream: fa_decode_shared(
-        cache, q.data_ptr(), out.data_ptr(), prefix_table.data_ptr(), prefix_table.shape[0],
-        prefix_len.data_ptr(), page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), B, Hq,
-        scale, code, ws, ws_bytes, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_decode_shared")
+    cache, d, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype,
+                                                        out)
+    _check_ints(device, "prefix_table", prefix_table, (None,))
+    _check_ints(device, "prefix_len", prefix_len, (1,))
+    ws, ws_bytes = _workspace(workspace, device)
+    _run("fa_decode_shared", device, cache, q.data_ptr(), out.data_ptr(), prefix_table.data_ptr(),
+         prefix_table.shape[0], prefix_len.data_ptr(), page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
+         B, _decode_rows(q, B, d), scale, code, ws, ws_bytes)
     return out

@@ -115,6 +115,9 @@ struct PagedLaunch {
     const int32_t *seq_lens;    // [B]
     const int32_t *cu_q;        // [B + 1], or null: max_q tokens for every sequence
     int B, Hq, total_q, max_q, max_pages;
+    int device;
+    int num_sms;      // (set by launch_paged)
+    long long units;  // (set by launch_paged) no more units of work than this
     int causal;
     float scale;
     int out_dtype;

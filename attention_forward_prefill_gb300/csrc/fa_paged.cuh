@@ -6,9 +6,9 @@
 // token j lives in page page_table[b][j / page_size], slot j % page_size.  A
 // sequence with nq query tokens gives each kv head nq * G query rows
 // (G = query heads per kv head), row r = (token r / G, head r % G), cut into
-// blocks of block_rows.  A unit = (sequence, kv head, row block); it costs one
-// step per key tile its rows can see (at least one, so that a unit without
-// keys still writes its rows).  The W steps of the whole call, in the order
+// blocks of block_rows.  A unit = (sequence, kv head, row block); it costs
+// unit_steps for its own start and end and a step per key tile its rows can see
+// (at least one, so that a unit without keys still writes its rows).  The W steps of the whole call, in the order
 // (sequence, kv head, block), are cut into gridDim.x equal ranges, one per
 // CTA, whatever the lengths are: they live on the device, so the cut is made
 // there, by every CTA for itself.  A unit inside one range is written
@@ -19,6 +19,8 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "fa_internal.h"
@@ -43,6 +45,7 @@ struct PagedParams {
     int max_pages, max_len;
     int num_pages, page_shift;
     int block_rows;         // query rows of a unit
+    int unit_steps;         // what a unit costs besides its key tiles, in steps
     int causal;             // query token i of nq sees keys j <= len - nq + i
     float scale_log2;       // scale * log2(e)
     int out_dtype;
@@ -110,8 +113,8 @@ template <int TK>
 __device__ __forceinline__ long long paged_head_steps(const PagedParams &p, const SeqView &s) {
     const int n = paged_blocks(p, s);
     if (n == 0) return 0;
-    if (!p.causal || n == 1) return static_cast<long long>(n) * paged_tiles<TK>(p, s, n - 1);
-    long long sum = 0;
+    long long sum = static_cast<long long>(n) * p.unit_steps;
+    if (!p.causal || n == 1) return sum + static_cast<long long>(n) * paged_tiles<TK>(p, s, n - 1);
     for (int rb = 0; rb < n; ++rb) sum += paged_tiles<TK>(p, s, rb);
     return sum;
 }
@@ -186,11 +189,12 @@ struct PagedPiece {
     int kind;       // 0 whole unit, 1 opens a unit that the next CTA continues, 2 continues one, -1 no more work
 };
 
-// Walks a CTA's pieces in order.
+// Walks a CTA's pieces in order.  A unit's steps are its unit_steps, then its key
+// tiles: a range that ends among the former leaves the whole unit to the next CTA.
 template <int TK>
 struct PagedCursor {
     SeqView s;
-    int b, hk, rb, blocks, j;
+    int b, hk, rb, blocks, v;  // v: the next step of unit (b, hk, rb)
     long long left;
 
     __device__ __forceinline__ void begin(const PagedParams &p, const PagedStart &st) {
@@ -203,45 +207,53 @@ struct PagedCursor {
         hk = static_cast<int>(st.rem / per_head);
         long long rem = st.rem - hk * per_head;
         if (!p.causal) {
-            const int c = paged_tiles<TK>(p, s, 0);
+            const int c = paged_tiles<TK>(p, s, 0) + p.unit_steps;
             rb = static_cast<int>(rem / c);
-            j = static_cast<int>(rem - static_cast<long long>(rb) * c);
+            v = static_cast<int>(rem - static_cast<long long>(rb) * c);
             return;
         }
         for (rb = 0; rb < blocks - 1; ++rb) {
-            const int c = paged_tiles<TK>(p, s, rb);
+            const int c = paged_tiles<TK>(p, s, rb) + p.unit_steps;
             if (rem < c) break;
             rem -= c;
         }
-        j = static_cast<int>(rem);
+        v = static_cast<int>(rem);
     }
 
-    // The next piece; false when the range is used up.  cost: the whole unit's steps.
-    __device__ __forceinline__ bool next(const PagedParams &p, PagedPiece &u, int &cost) {
-        if (left <= 0) return false;
-        cost = paged_tiles<TK>(p, s, rb);
-        u.b = b;
-        u.t0 = s.t0;
-        u.nq = s.nq;
-        u.len = s.len;
-        u.hk = hk;
-        u.row0 = rb * p.block_rows;
-        u.j0 = j;
-        u.j1 = static_cast<int>(min(static_cast<long long>(cost), j + left));
-        u.kind = u.j0 > 0 ? 2 : (u.j1 < cost ? 1 : 0);
-        left -= u.j1 - u.j0;
-        j = 0;
-        if (left > 0 && ++rb == blocks) {
-            rb = 0;
-            if (++hk == p.Hkv) {
-                hk = 0;
-                do {  // steps are left, so a later sequence has rows
-                    s = paged_seq(p, ++b);
-                    blocks = paged_blocks(p, s);
-                } while (blocks == 0);
+    // The next piece with key tiles; false when the range is used up.  tiles: the whole unit's.
+    __device__ __forceinline__ bool next(const PagedParams &p, PagedPiece &u, int &tiles) {
+        while (left > 0) {
+            const int t = paged_tiles<TK>(p, s, rb), cost = t + p.unit_steps;
+            const int end = static_cast<int>(min(static_cast<long long>(cost), v + left));
+            const int j0 = max(0, v - p.unit_steps), j1 = max(0, end - p.unit_steps);
+            const bool some = j1 > j0;
+            if (some) {
+                tiles = t;
+                u.b = b;
+                u.t0 = s.t0;
+                u.nq = s.nq;
+                u.len = s.len;
+                u.hk = hk;
+                u.row0 = rb * p.block_rows;
+                u.j0 = j0;
+                u.j1 = j1;
+                u.kind = j0 > 0 ? 2 : (j1 < t ? 1 : 0);
             }
+            left -= end - v;
+            v = 0;
+            if (left > 0 && ++rb == blocks) {
+                rb = 0;
+                if (++hk == p.Hkv) {
+                    hk = 0;
+                    do {  // steps are left, so a later sequence has rows
+                        s = paged_seq(p, ++b);
+                        blocks = paged_blocks(p, s);
+                    } while (blocks == 0);
+                }
+            }
+            if (some) return true;
         }
-        return true;
+        return false;
     }
 };
 
@@ -254,15 +266,16 @@ __device__ __forceinline__ int paged_cta_of(long long step, long long W, int G) 
     return static_cast<int>(c);
 }
 
-// What a CTA notes about the unit it leaves unfinished (or that there is none).
-__device__ __forceinline__ void paged_note_open(const PagedParams &p, const PagedPiece *u, int cost, long long end,
+// What a CTA notes about the unit it leaves unfinished (or that there is none): u, its
+// last piece, ended where the CTA's range does.
+__device__ __forceinline__ void paged_note_open(const PagedParams &p, const PagedPiece *u, int tiles, long long end,
                                                 long long W, int G) {
     int4 *o = p.open + 2 * blockIdx.x;
     if (!u || u->kind != 1) {
         o[0] = make_int4(-1, 0, 0, 0);
         return;
     }
-    o[0] = make_int4(paged_cta_of(end + (cost - u->j1) - 1, W, G), u->t0, u->hk, u->row0);
+    o[0] = make_int4(paged_cta_of(end + (tiles - u->j1) - 1, W, G), u->t0, u->hk, u->row0);
     o[1] = make_int4(u->nq, 0, 0, 0);
 }
 
@@ -289,22 +302,39 @@ __device__ __forceinline__ void paged_store(const PagedParams &p, long long off,
     }
 }
 
+// N columns of the earlier result of a row, loaded ahead of their use.
+template <int N>
+struct PagedInit {
+    float o[N], m;  // m: log2 units
+    __device__ __forceinline__ void load(const PagedParams &p, int D, long long row, int col) {
+        if (!p.init_o) return;
+        const float *src = p.init_o + row * D + col;
+        m = p.init_lse[row] * kLog2e;
+        if constexpr (N == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src);
+            o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(src);
+            o[0] = v.x; o[1] = v.y;
+        }
+    }
+};
+
 // A whole row's (or all pieces') unnormalised columns acc with (m, l), m in log2
 // units: joins the optional earlier result and writes out, and the row's lse once.
 template <int N>
 __device__ __forceinline__ void paged_finish(const PagedParams &p, int D, long long row, int col, float (&acc)[N],
-                                             float m, float l) {
+                                             float m, float l, const PagedInit<N> &init) {
     const long long off = row * D + col;
     float inv;
     if (p.init_o) {
-        const float mi = p.init_lse[row] * kLog2e;
-        const float M = fmaxf(m, mi);
-        const float w = ex2_from(m, M), wi = ex2_from(mi, M);
+        const float M = fmaxf(m, init.m);
+        const float w = ex2_from(m, M), wi = ex2_from(init.m, M);
         const float total = fmaf(w, l, wi);
         inv = total > 0.f ? 1.f / total : 0.f;
         const float a = w * inv, c = wi * inv;
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(a, acc[e], c * p.init_o[off + e]);
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(a, acc[e], c * init.o[e]);
         if (p.lse && col == 0) p.lse[row] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
     } else {
         inv = l > 0.f ? 1.f / l : 0.f;
@@ -315,14 +345,18 @@ __device__ __forceinline__ void paged_finish(const PagedParams &p, int D, long l
     paged_store<N>(p, off, acc);
 }
 
+// Row r of a block among the rows of the output.
+__device__ __forceinline__ long long paged_row(const PagedParams &p, const PagedPiece &u, int r) {
+    const int rr = u.row0 + r;
+    return (static_cast<long long>(u.t0) + rr / p.G) * p.Hq + u.hk * p.G + rr % p.G;
+}
+
 // N columns of a row of the current piece: finished rows go to out, cut ones to the CTA's partial slot.
 template <int D, int RB, int N>
-__device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiece &u, int r, int col, float (&acc)[N],
-                                           float m, float l) {
-    const int rr = u.row0 + r;
+__device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiece &u, int r, long long row, int col,
+                                           float (&acc)[N], float m, float l, const PagedInit<N> &init) {
     if (u.kind == 0) {
-        const long long row = (static_cast<long long>(u.t0) + rr / p.G) * p.Hq + u.hk * p.G + rr % p.G;
-        paged_finish<N>(p, D, row, col, acc, m, l);
+        paged_finish<N>(p, D, row, col, acc, m, l, init);
     } else {
         const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + (u.kind == 1 ? 1 : 0)) * RB + r;
         float *o = p.part_o + rec * D + col;
@@ -332,56 +366,134 @@ __device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiec
     }
 }
 
-// Joins the pieces of the units that ranges cut.  CTA (c, y): the unit that CTA c
-// of the main kernel left open (slot 1 of c, slot 0 of the CTAs after it up to the
-// one that closed the unit), rows [y * kJoinRows, ...).  A warp takes a row, its
-// lanes D / 32 columns each; pieces are added in CTA order.
-constexpr int kJoinWarps = 4;
-constexpr int kJoinRows = 8;
+// Joins the pieces of the units that ranges cut: the unit that CTA c of the main
+// kernel left open has its pieces in slot 1 of c and slot 0 of the CTAs after it, up
+// to the one that closed the unit.  They are added in CTA order.
+// All latency.  Every CTA reads all notes at once and numbers the items (two rows
+// of a unit of at most four pieces, or one row of one with more), the warps of the
+// grid take the items in turn, and an item's loads (2 rows x 4 pieces, or 12
+// pieces) are in flight together.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinMax = 512;  // CTAs of the main kernel
 
-template <int D, int RB>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedParams p) {
+template <int D, int RB, int R, int F>
+__device__ __forceinline__ void paged_join_rows(const PagedParams &p, int c, const int4 &a, int r0, int rows, int lane) {
     constexpr int N = D / 32;
-    constexpr int U = 4;  // pieces in flight
     using Vec = typename std::conditional<N == 4, float4, float2>::type;
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 a = p.open[2 * c];
-    if (a.x < 0) return;
-    const int4 b = p.open[2 * c + 1];
     const int n = a.x - c + 1;  // pieces
-    const int rows = min(p.block_rows, b.x * p.G - a.w);
     auto rec = [&](int k, int r) { return (static_cast<size_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; };
-    for (int r = blockIdx.y * kJoinRows + warp; r < min(rows, (blockIdx.y + 1) * kJoinRows); r += kJoinWarps) {
-        float M = -INFINITY;
-        for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[rec(k, r) * 2]);
+    float M[R], L[R], acc[R][N];
+    PagedInit<N> init[R];
+    long long row[R];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        float acc[N] = {}, L = 0.f;
-        for (int k0 = 0; k0 < n; k0 += U) {
-            Vec x[U];
-            float2 ml[U];
+    for (int r = 0; r < R; ++r) {
+        M[r] = -INFINITY;
+        L[r] = 0.f;
+        const int rr = a.w + min(r0 + r, rows - 1);
+        row[r] = (static_cast<long long>(a.y) + rr / p.G) * p.Hq + a.z * p.G + rr % p.G;
+        init[r].load(p, D, row[r], lane * N);
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int k = min(k0 + i, n - 1);
-                x[i] = reinterpret_cast<const Vec *>(p.part_o + rec(k, r) * D)[lane];
-                ml[i] = *reinterpret_cast<const float2 *>(p.part_ml + rec(k, r) * 2);
+        for (int e = 0; e < N; ++e) acc[r][e] = 0.f;
+    }
+    for (int k0 = 0; k0 < n; k0 += F) {
+        Vec x[R][F];
+        // lane i * R + r holds the (m, l) of piece k0 + i and row r
+        const int lk = k0 + lane / R, lr = r0 + lane % R;
+        const float2 ml = lane < R * F && lk < n && lr < rows
+                              ? *reinterpret_cast<const float2 *>(p.part_ml + rec(lk, lr) * 2)
+                              : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (k0 + i < n && r0 + r < rows)
+                    x[r][i] = reinterpret_cast<const Vec *>(p.part_o + rec(k0 + i, r0 + r) * D)[lane];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float next = M[r], mi[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                mi[i] = __shfl_sync(0xffffffffu, ml.x, i * R + r);
+                next = fmaxf(next, mi[i]);
             }
+            const float keep = ex2_from(M[r], next);
+            M[r] = next;
+            L[r] *= keep;
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const float w = k0 + i < n ? ex2_from(ml[i].x, M) : 0.f;
-                const float *xv = reinterpret_cast<const float *>(&x[i]);
-                if (w > 0.f) {  // a piece without visible keys leaves l = 0 and no weight
-                    L = fmaf(w, ml[i].y, L);
+            for (int e = 0; e < N; ++e) acc[r][e] *= keep;
 #pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] = fmaf(w, xv[e], acc[e]);
+            for (int i = 0; i < F; ++i) {
+                const float w = ex2_from(mi[i], next), li = __shfl_sync(0xffffffffu, ml.y, i * R + r);
+                if (w > 0.f) {  // 0: the row saw no key in this piece, whose columns may be unwritten
+                    const float *xv = reinterpret_cast<const float *>(&x[r][i]);
+                    L[r] = fmaf(w, li, L[r]);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) acc[r][e] = fmaf(w, xv[e], acc[r][e]);
                 }
             }
         }
-        const int rr = a.w + r;
-        const long long row = (static_cast<long long>(a.y) + rr / p.G) * p.Hq + a.z * p.G + rr % p.G;
-        paged_finish<N>(p, D, row, lane * N, acc, M, L);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r0 + r < rows) paged_finish<N>(p, D, row[r], lane * N, acc[r], M[r], L[r], init[r]);
+}
+
+template <int D, int RB>
+__global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const PagedParams p, const int ctas) {
+    __shared__ int4 note[kJoinMax];
+    __shared__ int first[kJoinMax];  // items before CTA c's unit
+    __shared__ int rows_of[kJoinMax];
+    __shared__ int warp_items[kJoinThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kEach = kJoinMax / kJoinThreads;
+    int items[kEach], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int c = tid * kEach + i;
+        items[i] = 0;
+        if (c < ctas) {
+            const int4 a = p.open[2 * c], b = p.open[2 * c + 1];
+            note[c] = a;
+            if (a.x >= 0) {
+                const int rows = min(p.block_rows, b.x * p.G - a.w);
+                rows_of[c] = rows;
+                items[i] = a.x - c < 4 ? (rows + 1) / 2 : rows;
+            }
+        }
+        mine += items[i];
+    }
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) warp_items[warp] = incl;
+    __syncthreads();
+    int before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        if (w < warp) before += warp_items[w];
+        total += warp_items[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (tid * kEach + i < ctas) first[tid * kEach + i] = before;
+        before += items[i];
+    }
+    __syncthreads();
+    for (int item = blockIdx.x * (kJoinThreads / 32) + warp; item < total; item += gridDim.x * (kJoinThreads / 32)) {
+        int lo = 0, hi = ctas - 1;  // the last c with first[c] <= item (those without a unit have none after it)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= item) lo = mid; else hi = mid - 1;
+        }
+        const int4 a = note[lo];
+        const int i = item - first[lo];
+        if (a.x - lo < 4) paged_join_rows<D, RB, 2, 4>(p, lo, a, i * 2, rows_of[lo], lane);
+        else paged_join_rows<D, RB, 1, 12>(p, lo, a, i, rows_of[lo], lane);
     }
 }
 
@@ -429,10 +541,29 @@ struct PagedConfig {
     PagedConfig(const PagedConfig &) = delete;
 };
 
+// Dynamic shared memory of a kernel allowed on a device, once (`ready`: a static
+// array of the kernel's own); min_regs: registers at launch that its setmaxnreg
+// split needs (it would wait forever with fewer).
+template <typename K>
+int ready_kernel(K kernel, int smem, int min_regs, int device, std::atomic<bool> *ready) {
+    if (ready[device].load(std::memory_order_acquire)) return FA_OK;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e);
+    cudaFuncAttributes f;
+    if ((e = cudaFuncGetAttributes(&f, kernel)) != cudaSuccess) return cuda_fail(e);
+    if (f.numRegs < min_regs) return cuda_fail(cudaErrorInvalidConfiguration);
+    ready[device].store(true, std::memory_order_release);
+    return FA_OK;
+}
+
+// ctas: the main kernel's; units: no more units than this exist.
 template <int D, int RB>
-int launch_join(const PagedParams &p, int grid, cudaStream_t stream) {
-    PagedConfig cfg(dim3(grid, (p.block_rows + kJoinRows - 1) / kJoinRows), kJoinWarps * 32, 0, true, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, p);
+int launch_join(const PagedParams &p, int ctas, long long units, int num_sms, cudaStream_t stream) {
+    if (ctas > kJoinMax) return cuda_fail(cudaErrorInvalidConfiguration);
+    const long long items = std::min<long long>(ctas, units) * p.block_rows, warps = kJoinThreads / 32;
+    const int grid = static_cast<int>(std::min<long long>(2LL * num_sms, (items + warps - 1) / warps));
+    PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, p, ctas);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

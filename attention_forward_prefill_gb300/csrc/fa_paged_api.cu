@@ -106,7 +106,7 @@ int check_attention(const Attention &a) {
     return FA_OK;
 }
 
-PagedLaunch launch_of(const Attention &a, int causal) {
+PagedLaunch launch_of(const Attention &a, int causal, const DeviceInfo &dev) {
     PagedLaunch l = {};
     l.c = *a.c;
     l.q = a.q;
@@ -120,6 +120,7 @@ PagedLaunch launch_of(const Attention &a, int causal) {
     l.total_q = a.total;
     l.max_q = a.max_q;
     l.max_pages = a.max_pages;
+    l.device = dev.device;
     l.causal = causal ? 1 : 0;
     l.scale = a.scale;
     l.out_dtype = a.out_dtype;
@@ -159,7 +160,7 @@ int run_attention(const Attention &a, int causal, void *workspace, size_t worksp
     int rc = current_device_info(&dev);
     if (rc != FA_OK) return rc;
     if (a.total == 0) return FA_OK;
-    PagedLaunch l = launch_of(a, causal);
+    PagedLaunch l = launch_of(a, causal, dev);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Scratch s(st);
     // (a workspace is sized for max_seqlen_q, which fewer tokens than that do not change)
@@ -341,14 +342,14 @@ int fa_decode_shared(const fa_paged_cache *cache, const void *q, void *out, cons
     Scratch s(st);
     if ((rc = s.take(workspace, workspace_bytes, w.total)) != FA_OK) return rc;
     char *base = static_cast<char *>(s.ptr);
-    PagedLaunch l = launch_of(pre, 0);
+    PagedLaunch l = launch_of(pre, 0, dev);
     l.out = base + w.rows;
     l.out_dtype = FA_F32;
     l.lse = reinterpret_cast<float *>(base + w.lse);
     l.scratch = base + w.first;
     rc = launch_paged(l, dev, st);
     if (rc == FA_OK) {
-        PagedLaunch o = launch_of(own, 0);
+        PagedLaunch o = launch_of(own, 0, dev);
         o.init_o = static_cast<const float *>(l.out);
         o.init_lse = l.lse;
         o.scratch = base + w.second;

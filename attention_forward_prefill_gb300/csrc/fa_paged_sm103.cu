@@ -48,7 +48,7 @@ struct PagedLayout {
     static constexpr int kJoinOff = kQOff + kRows * kQPitch;
     static constexpr int kJoinBytes = kGroups > 1 ? kConsumers * 16 * (kJoinCols * 4 + 8) : 0;
     static constexpr int kBarOff = kJoinOff + kJoinBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 + RT;  // full, empty, unit full, unit empty, join
+    static constexpr int kNumBars = 2 * kStages + 2 + 2 * RT;  // full, empty, unit full, unit empty, join full, join empty
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kPieceOff = kMiscOff + 8;
     static constexpr int kStartOff = kPieceOff + ((int)sizeof(PagedPiece) + 7) / 8 * 8;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     uint64_t *empty = full + L::kStages;
     uint64_t *u_full = empty + L::kStages;
     uint64_t *u_empty = u_full + 1;
-    uint64_t *joined = u_empty + 1;  // [RT]
+    uint64_t *j_full = u_empty + 1, *j_empty = j_full + RT;  // [RT] each
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMiscOff);
     PagedPiece *piece = reinterpret_cast<PagedPiece *>(smem + L::kPieceOff);
     PagedStart *start = reinterpret_cast<PagedStart *>(smem + L::kStartOff);
@@ -88,7 +88,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         }
         mbar_init(u_full, 1);
         mbar_init(u_empty, kConsumers);
-        for (int t = 0; t < RT; ++t) mbar_init(joined + t, KG);
+        for (int t = 0; t < RT; ++t) {
+            mbar_init(j_full + t, KG);
+            mbar_init(j_empty + t, KG);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -110,12 +113,12 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         PagedCursor<kTile> cur;
         cur.begin(p, *start);
         PagedPiece u;
-        int cost = 0;
+        int unit_tiles = 0;
         bool any = false;
         while (ok) {
-            const bool more = cur.next(p, u, cost);
+            const bool more = cur.next(p, u, unit_tiles);
             if (!more) {
-                if (lane == 0) paged_note_open(p, any ? &u : nullptr, cost, start->end, start->W, start->G);
+                if (lane == 0) paged_note_open(p, any ? &u : nullptr, unit_tiles, start->end, start->W, start->G);
                 u.kind = -1;
             }
             any = true;
@@ -317,68 +320,109 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             }
             const int rows = min(RB, u.nq * p.G - u.row0);
             if constexpr (KG == 1) {
-                const int rh = r0 + 8;
+                auto write = [&](int r, float m, float l, auto half) {
+                    constexpr int H = decltype(half)::value;
+                    if (r >= rows) return;
+                    const long long row = paged_row(p, u, r);
+                    constexpr int U = 1;  // column pairs whose earlier result is in flight
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    float a[2] = {o[i][0], o[i][1]}, c[2] = {o[i][2], o[i][3]};
-                    if (r0 < rows) paged_emit<D, RB, 2>(p, u, r0, i * 8 + quad * 2, a, m0, l0);
-                    if (rh < rows) paged_emit<D, RB, 2>(p, u, rh, i * 8 + quad * 2, c, m1, l1);
-                }
-            } else {
-                // join the KG key groups of row tile rw, kJoinCols columns at a time
-                auto sync = [&] {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(joined + rw);
-                    ok = lanes_wait(joined + rw, joins++ & 1, abort_flag);
-                };
-                auto slot = [&](int g) { return (g * RT + rw) * 16; };
-                if (quad == 0) {
-                    join_ml[slot(kw) + qrow] = make_float2(m0, l0);
-                    join_ml[slot(kw) + qrow + 8] = make_float2(m1, l1);
-                }
-                sync();
-                if (!ok) break;
-                float M0 = -INFINITY, M1 = -INFINITY;
+                    for (int i0 = 0; i0 < D / 8; i0 += U) {
+                        PagedInit<2> init[U];
+                        if (u.kind == 0)
 #pragma unroll
-                for (int g = 0; g < KG; ++g) {
-                    M0 = fmaxf(M0, join_ml[slot(g) + qrow].x);
-                    M1 = fmaxf(M1, join_ml[slot(g) + qrow + 8].x);
-                }
-                const float f0 = ex2_from(m0, M0), f1 = ex2_from(m1, M1);
+                            for (int i = 0; i < U; ++i) init[i].load(p, D, row, (i0 + i) * 8 + quad * 2);
 #pragma unroll
-                for (int pass = 0; pass < D / kJoinCols; ++pass) {
-                    float *mine = join + slot(kw) * kJoinCols;
-#pragma unroll
-                    for (int i = 0; i < kJoinCols / 8; ++i) {
-                        const int nb = pass * (kJoinCols / 8) + i;
-                        *reinterpret_cast<float2 *>(mine + qrow * kJoinCols + i * 8 + quad * 2) =
-                            make_float2(o[nb][0] * f0, o[nb][1] * f0);
-                        *reinterpret_cast<float2 *>(mine + (qrow + 8) * kJoinCols + i * 8 + quad * 2) =
-                            make_float2(o[nb][2] * f1, o[nb][3] * f1);
-                    }
-                    sync();
-                    if (!ok) break;
-                    for (int i = kw * 32 + lane; i < 16 * kJoinCols / 4; i += KG * 32) {
-                        const int r = i / (kJoinCols / 4), c4 = i % (kJoinCols / 4) * 4;
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                        float M = -INFINITY, Ls = 0.f;
-#pragma unroll
-                        for (int g = 0; g < KG; ++g) M = fmaxf(M, join_ml[slot(g) + r].x);
-#pragma unroll
-                        for (int g = 0; g < KG; ++g) {
-                            const float4 v = *reinterpret_cast<const float4 *>(join + (slot(g) + r) * kJoinCols + c4);
-                            const float2 ml = join_ml[slot(g) + r];
-                            Ls = fmaf(ex2_from(ml.x, M), ml.y, Ls);
-                            acc[0] += v.x;
-                            acc[1] += v.y;
-                            acc[2] += v.z;
-                            acc[3] += v.w;
+                        for (int i = 0; i < U; ++i) {
+                            float a[2] = {o[i0 + i][2 * H], o[i0 + i][2 * H + 1]};
+                            paged_emit<D, RB, 2>(p, u, r, row, (i0 + i) * 8 + quad * 2, a, m, l, init[i]);
                         }
-                        if (rw * 16 + r < rows)
-                            paged_emit<D, RB, 4>(p, u, rw * 16 + r, pass * kJoinCols + c4, acc, M, Ls);
                     }
-                    sync();
-                }
+                };
+                write(r0, m0, l0, std::integral_constant<int, 0>{});
+                write(r0 + 8, m1, l1, std::integral_constant<int, 1>{});
+            } else {
+                // join the KG key groups of row tile rw through shared memory: as many columns per
+                // pass as the unit's rows leave room for
+                float *buf = join + rw * KG * 16 * kJoinCols;
+                float2 *buf_ml = join_ml + rw * KG * 16;
+                auto passes = [&](auto used) {
+                    constexpr int RU = decltype(used)::value;    // rows that exist, rounded up
+                    constexpr int C = kJoinCols * 16 / RU < D ? kJoinCols * 16 / RU : D;  // columns per pass
+                    constexpr int kCells = RU * C / 4, kPer = (kCells + KG * 32 - 1) / (KG * 32);
+                    constexpr int kAhead = kPer == 1 ? D / C : 1;  // passes whose earlier result is in flight
+                    const int cell = kw * 32 + lane;
+                    auto cell_row = [&](int i) { return (cell + i * KG * 32) / (C / 4); };
+                    const int cell_col = cell % (C / 4) * 4;
+                    // 16-byte chunks of a row change places by row, against bank conflicts
+                    auto at = [&](int g, int r, int col) {
+                        return buf + (g * RU + r) * C + (((col >> 2) ^ (r & 7)) << 2) + (col & 3);
+                    };
+                    PagedInit<4> init[kPer][kAhead];
+                    long long row[kPer];
+                    bool live[kPer];
+                    auto load_init = [&](int pass0) {
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i)
+                            if (u.kind == 0 && live[i])
+#pragma unroll
+                                for (int k = 0; k < kAhead; ++k) init[i][k].load(p, D, row[i], (pass0 + k) * C + cell_col);
+                    };
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        live[i] = cell + i * KG * 32 < kCells && rw * 16 + cell_row(i) < rows;
+                        row[i] = paged_row(p, u, rw * 16 + cell_row(i));
+                    }
+                    load_init(0);
+#pragma unroll
+                    for (int pass = 0; pass < D / C; ++pass) {
+                        if (pass > 0 && pass % kAhead == 0) load_init(pass);
+                        if (joins > 0 && !lanes_wait(j_empty + rw, (joins - 1) & 1, abort_flag)) { ok = false; return; }
+#pragma unroll
+                        for (int i = 0; i < C / 8; ++i) {
+                            const int nb = pass * (C / 8) + i, col = i * 8 + quad * 2;
+                            if (RU >= 8 || qrow < RU)
+                                *reinterpret_cast<float2 *>(at(kw, qrow, col)) = make_float2(o[nb][0], o[nb][1]);
+                            if constexpr (RU == 16)
+                                *reinterpret_cast<float2 *>(at(kw, qrow + 8, col)) = make_float2(o[nb][2], o[nb][3]);
+                        }
+                        if (pass == 0 && quad == 0) {
+                            buf_ml[kw * 16 + qrow] = make_float2(m0, l0);
+                            buf_ml[kw * 16 + qrow + 8] = make_float2(m1, l1);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(j_full + rw);
+                        if (!lanes_wait(j_full + rw, joins & 1, abort_flag)) { ok = false; return; }
+                        ++joins;
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i) {
+                            if (!live[i]) continue;
+                            const int r = cell_row(i);
+                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                            float M = -INFINITY, Ls = 0.f;
+#pragma unroll
+                            for (int g = 0; g < KG; ++g) M = fmaxf(M, buf_ml[g * 16 + r].x);
+#pragma unroll
+                            for (int g = 0; g < KG; ++g) {
+                                const float4 v = *reinterpret_cast<const float4 *>(at(g, r, cell_col));
+                                const float2 ml = buf_ml[g * 16 + r];
+                                const float w = ex2_from(ml.x, M);
+                                Ls = fmaf(w, ml.y, Ls);
+                                acc[0] = fmaf(w, v.x, acc[0]);
+                                acc[1] = fmaf(w, v.y, acc[1]);
+                                acc[2] = fmaf(w, v.z, acc[2]);
+                                acc[3] = fmaf(w, v.w, acc[3]);
+                            }
+                            paged_emit<D, RB, 4>(p, u, rw * 16 + r, row[i], pass * C + cell_col, acc, M, Ls,
+                                                 init[i][pass % kAhead]);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(j_empty + rw);
+                    }
+                };
+                const int used = rows - rw * 16;
+                if (RT == 1 && used <= 8) passes(std::integral_constant<int, 8>{});
+                else passes(std::integral_constant<int, 16>{});
+                if (!ok) break;
             }
         }
         __syncwarp();
@@ -405,12 +449,12 @@ int launch_rows(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream
     if ((rc = make_page_map(&mk, a.c.k_pages, a.c, kTile)) != FA_OK) return rc;
     if ((rc = make_page_map(&mv, a.c.v_pages, a.c, kTile)) != FA_OK) return rc;
     const auto kernel = paged_rows_kernel<D, RT, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
-    if (e != cudaSuccess) return cuda_fail(e);
+    static std::atomic<bool> ready[kMaxDevices];
+    if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, a.device, ready)) != FA_OK) return rc;
     PagedConfig cfg(grid, kPagedThreads, L::kSmemBytes, a.init_o != nullptr, stream);
-    e = cudaLaunchKernelEx(&cfg.c, kernel, mk, mv, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mk, mv, p);
     if (e != cudaSuccess) return cuda_fail(e);
-    return launch_join<D, L::kRows>(p, grid, stream);
+    return launch_join<D, L::kRows>(p, grid, a.units, a.num_sms, stream);
 }
 
 template <int D, bool BF16>
@@ -429,13 +473,14 @@ struct PagedPlan {
     int slot_rows;   // rows of a partial slot
     int tile;        // keys per step
     int per_sm;      // CTAs per SM
+    int unit_steps;  // what a unit costs besides its key tiles
 };
 
 PagedPlan plan_paged(int max_q, int group) {
     const long long rows = static_cast<long long>(max_q) * group;
-    if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256, 128, 1};
+    if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256, 128, 1, 2};
     const int rb = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    return {false, rb, rb, kTile, 2};
+    return {false, rb, rb, kTile, 2, 2};
 }
 
 }  // namespace
@@ -475,6 +520,7 @@ int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t strea
     p.out_dtype = a.out_dtype;
     const PagedPlan pl = plan_paged(a.max_q, p.G);
     p.block_rows = pl.block_rows;
+    p.unit_steps = pl.unit_steps;
     const int most = pl.per_sm * dev.num_sms;
     const size_t slots = static_cast<size_t>(most) * 2, rec = slots * pl.slot_rows;
     p.part_o = static_cast<float *>(a.scratch);
@@ -482,14 +528,16 @@ int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t strea
     p.open = reinterpret_cast<int4 *>(p.part_ml + rec * 2);
     // no more CTAs than the call can have steps
     const long long rows = static_cast<long long>(a.max_q) * p.G;
-    const long long steps = static_cast<long long>(a.B) * p.Hkv * ((rows + pl.block_rows - 1) / pl.block_rows) *
-                            ((p.max_len + pl.tile - 1) / pl.tile);
+    PagedLaunch l = a;
+    l.num_sms = dev.num_sms;
+    l.units = static_cast<long long>(a.B) * p.Hkv * ((rows + pl.block_rows - 1) / pl.block_rows);
+    const long long steps = l.units * ((p.max_len + pl.tile - 1) / pl.tile);
     const int grid = static_cast<int>(std::min<long long>(most, steps));
-    if (pl.tiles) return launch_paged_tiles(a, p, grid, stream);
+    if (pl.tiles) return launch_paged_tiles(l, p, grid, stream);
     const bool bf16 = a.c.dtype == FA_BF16;
     if (a.c.head_dim == 64)
-        return bf16 ? launch_rows_d<64, true>(a, p, grid, stream) : launch_rows_d<64, false>(a, p, grid, stream);
-    return bf16 ? launch_rows_d<128, true>(a, p, grid, stream) : launch_rows_d<128, false>(a, p, grid, stream);
+        return bf16 ? launch_rows_d<64, true>(l, p, grid, stream) : launch_rows_d<64, false>(l, p, grid, stream);
+    return bf16 ? launch_rows_d<128, true>(l, p, grid, stream) : launch_rows_d<128, false>(l, p, grid, stream);
 }
 
 int read_paged_status(int reset) {

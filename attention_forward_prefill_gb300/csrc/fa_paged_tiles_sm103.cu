@@ -169,12 +169,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         PagedCursor<kKeys> cur;
         cur.begin(p, *start);
         PagedPiece u;
-        int cost = 0;
+        int unit_tiles = 0;
         bool any = false;
         while (ok) {
-            const bool more = cur.next(p, u, cost);
+            const bool more = cur.next(p, u, unit_tiles);
             if (!more) {
-                if (lane == 0) paged_note_open(p, any ? &u : nullptr, cost, start->end, start->W, start->G);
+                if (lane == 0) paged_note_open(p, any ? &u : nullptr, unit_tiles, start->end, start->W, start->G);
                 u.kind = -1;
             }
             any = true;
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const float m = m_ref - kShift;  // (-inf stays)
-            const long long row = (static_cast<long long>(u.t0) + rr / p.G) * p.Hq + u.hk * p.G + rr % p.G;
+            const long long row = paged_row(p, u, t * tile_rows + r);
             float a = 1.f, ai = 0.f;  // weights of this pass and of the earlier result
             if (u.kind == 0 && row_ok) {
                 if (p.init_o) {
@@ -490,8 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (p.init_o) {
                             const float *e = p.init_o + row * D + q * 32;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                o[c] = __float_as_uint(fmaf(a, __uint_as_float(o[c]), ai * e[c]));
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 v = *reinterpret_cast<const float4 *>(e + c);
+                                o[c] = __float_as_uint(fmaf(a, __uint_as_float(o[c]), ai * v.x));
+                                o[c + 1] = __float_as_uint(fmaf(a, __uint_as_float(o[c + 1]), ai * v.y));
+                                o[c + 2] = __float_as_uint(fmaf(a, __uint_as_float(o[c + 2]), ai * v.z));
+                                o[c + 3] = __float_as_uint(fmaf(a, __uint_as_float(o[c + 3]), ai * v.w));
+                            }
                         }
                         store_out32(static_cast<uint8_t *>(p.out) + (row * D + q * 32) * osize, o, p.init_o ? 1.f : a,
                                     p.out_dtype);
@@ -571,15 +576,12 @@ int launch_tiles_d(const PagedLaunch &a, PagedParams p, int grid, cudaStream_t s
     const float scale = a.scale == 0.f ? 0x1p-100f : a.scale;
     p.scale_log2 = scale * kLog2e;
     const auto kernel = paged_tiles_kernel<D, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
-    if (e != cudaSuccess) return cuda_fail(e);
-    cudaFuncAttributes fattr;
-    if ((e = cudaFuncGetAttributes(&fattr, kernel)) != cudaSuccess) return cuda_fail(e);
-    if (fattr.numRegs < kMinLaunchRegs) return cuda_fail(cudaErrorInvalidConfiguration);
+    static std::atomic<bool> ready[kMaxDevices];
+    if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, a.device, ready)) != FA_OK) return rc;
     PagedConfig cfg(grid, kThreads, L::kSmemBytes, a.init_o != nullptr, stream);
-    e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, tile_tokens, scale < 0.f ? 1 : 0);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, tile_tokens, scale < 0.f ? 1 : 0);
     if (e != cudaSuccess) return cuda_fail(e);
-    return launch_join<D, 2 * kM>(p, grid, stream);
+    return launch_join<D, 2 * kM>(p, grid, a.units, a.num_sms, stream);
 }
 
 }  // namespace
