@@ -580,6 +580,11 @@ def _pages(k_pages, v_pages):
                        slots, d, _code_of(dtype)), heads, d
 
 
+def _is_ints(t, device, int32, dims):
+    """t is an int32 array that _check_ints has nothing to say on but its sizes."""
+    return t.dtype is int32 and t.dim() == dims and t.is_contiguous() and t.device == device
+
+
 def _check_ints(device, name, t, shape):
     """int32 arrays of the device: contiguous and where the cache is; a None in `shape` is any size."""
     if t.device != device:
@@ -607,6 +612,19 @@ def _check_rows(name, t, tokens, heads, k_pages):
                              f"{'heads' if heads is None else heads}, {d}]")
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     return stride[0], shape[1]
+
+
+def _tables(device, page_table, seq_lens):
+    """Checks both; the batch and the width of the table."""
+    int32 = _torch().int32
+    B = seq_lens.numel()
+    if _is_ints(seq_lens, device, int32, 1) and _is_ints(page_table, device, int32, 2):
+        rows, width = page_table.shape
+        if rows == B:
+            return B, width
+    _check_ints(device, "seq_lens", seq_lens, (B,))
+    _check_ints(device, "page_table", page_table, (B, None))
+    raise AssertionError("unreachable")
 
 
 def _run(name, device, *args):
@@ -651,13 +669,12 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
     total = k.shape[0]
     k_stride, _ = _check_rows("k", k, total, Hkv, k_pages)
     v_stride, _ = _check_rows("v", v, total, Hkv, k_pages)
-    B = seq_lens.numel()
-    _check_ints(device, "seq_lens", seq_lens, (B,))
-    _check_ints(device, "page_table", page_table, (B, None))
+    B, max_pages = _tables(device, page_table, seq_lens)
     cu_ptr = pos_ptr = rope_ptr = None
     max_positions = rope_dim = 0
     if cu_seqlens is not None:
-        _check_ints(device, "cu_seqlens", cu_seqlens, (B + 1,))
+        if not (_is_ints(cu_seqlens, device, torch.int32, 1) and cu_seqlens.numel() == B + 1):
+            _check_ints(device, "cu_seqlens", cu_seqlens, (B + 1,))
         cu_ptr = cu_seqlens.data_ptr()
     if positions is not None:
         _check_ints(device, "positions", positions, (total,))
@@ -673,8 +690,8 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
     if q is not None:
         q_stride, Hq = _check_rows("q", q, total, None, k_pages)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=device)
-            out_stride = Hq * q.shape[2]
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out_stride = out.stride(0)
         else:
             out_stride, _ = _check_rows("out", out, total, Hq, k_pages)
         q_ptr, out_ptr = q.data_ptr(), out.data_ptr()
@@ -682,7 +699,7 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
         raise ValueError("out without q")
     if total:
         _run("fa_cache_append", device, cache, q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, q_stride, k_stride,
-             v_stride, out_stride, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), cu_ptr, pos_ptr,
+             v_stride, out_stride, page_table.data_ptr(), max_pages, seq_lens.data_ptr(), cu_ptr, pos_ptr,
              B, Hq, total, rope_ptr, max_positions, rope_dim, 1 if interleaved else 0)
     return out
 
@@ -696,20 +713,18 @@ def _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype, out
         if q.device != device or q.dtype != k_pages.dtype:
             raise ValueError("q must have the dtype and device of the cache")
         raise ValueError("q must be contiguous")
-    B = seq_lens.numel()
-    _check_ints(device, "seq_lens", seq_lens, (B,))
-    _check_ints(device, "page_table", page_table, (B, None))
+    B, max_pages = _tables(device, page_table, seq_lens)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out_dtype is None:
         out_dtype = q.dtype
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=device)
+        out = torch.empty_like(q, dtype=out_dtype)
     else:
         _check_cuda("out", out, q.shape, out_dtype)
         if out.device != device:
             raise ValueError("out must be on the device of the cache")
-    return cache, d, device, B, scale, _code_of(out_dtype), out
+    return cache, d, device, B, max_pages, scale, _code_of(out_dtype), out
 
 
 def _decode_rows(q, B, d):
@@ -727,10 +742,10 @@ def decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale: float | None 
     q [B, Hq, d] or [B, Hq, 1, d]; k_pages, v_pages [pages, Hkv, slots, d], any strides;
     page_table int32 [B, max_pages]; seq_lens int32 [B].  Returns rows shaped as q.
     """
-    cache, d, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype,
-                                                        out)
+    cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
+                                                                   out_dtype, out)
     ws, ws_bytes = _workspace(workspace, device)
-    _run("fa_decode_paged", device, cache, q.data_ptr(), out.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+    _run("fa_decode_paged", device, cache, q.data_ptr(), out.data_ptr(), page_table.data_ptr(), max_pages,
          seq_lens.data_ptr(), B, _decode_rows(q, B, d), scale, code, ws, ws_bytes)
     return out
 
@@ -745,12 +760,13 @@ def prefill_paged(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_s
     lse: optional fp32 [T, Hq] that receives the row log-sum-exp.  Returns [T, Hq, d]; rows
     outside every sequence are not written.
     """
-    cache, d, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype,
-                                                        out)
+    cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
+                                                                   out_dtype, out)
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, Hq, {d}]")
     total, Hq, _ = q.shape
-    _check_ints(device, "cu_seqlens_q", cu_seqlens_q, (B + 1,))
+    if not (_is_ints(cu_seqlens_q, device, _torch().int32, 1) and cu_seqlens_q.numel() == B + 1):
+        _check_ints(device, "cu_seqlens_q", cu_seqlens_q, (B + 1,))
     lse_ptr = None
     if lse is not None:
         _check_cuda("lse", lse, (total, Hq), _torch().float32)
@@ -760,7 +776,7 @@ def prefill_paged(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_s
     if total:
         ws, ws_bytes = _workspace(workspace, device)
         _run("fa_prefill_paged", device, cache, q.data_ptr(), out.data_ptr(), lse_ptr, page_table.data_ptr(),
-             page_table.shape[1], seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), B, Hq, total, int(max_seqlen_q),
+             max_pages, seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), B, Hq, total, int(max_seqlen_q),
              1 if causal else 0, scale, code, ws, ws_bytes)
     return out
 
@@ -771,12 +787,15 @@ def decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq
     (int32 [1], on the device) of prefix_table's pages (int32 [n]), then its own.  The prefix is
     read once for the whole batch.
     """
-    cache, d, device, B, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale, out_dtype,
-                                                        out)
-    _check_ints(device, "prefix_table", prefix_table, (None,))
-    _check_ints(device, "prefix_len", prefix_len, (1,))
+    cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
+                                                                   out_dtype, out)
+    int32 = _torch().int32
+    if not (_is_ints(prefix_table, device, int32, 1) and _is_ints(prefix_len, device, int32, 1) and
+            prefix_len.numel() == 1):
+        _check_ints(device, "prefix_table", prefix_table, (None,))
+        _check_ints(device, "prefix_len", prefix_len, (1,))
     ws, ws_bytes = _workspace(workspace, device)
     _run("fa_decode_shared", device, cache, q.data_ptr(), out.data_ptr(), prefix_table.data_ptr(),
-         prefix_table.shape[0], prefix_len.data_ptr(), page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
+         prefix_table.numel(), prefix_len.data_ptr(), page_table.data_ptr(), max_pages, seq_lens.data_ptr(),
          B, _decode_rows(q, B, d), scale, code, ws, ws_bytes)
     return out
