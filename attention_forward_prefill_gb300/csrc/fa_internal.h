@@ -102,30 +102,30 @@ struct BackwardLaunch {
 
 int launch_backward(const BackwardLaunch &a, cudaStream_t stream);
 
-// Attention over a paged cache (fa_decode_paged, fa_prefill_paged, and both steps
+// Attention over a paged cache (fa_decode_paged, fa_prefill_paged, and both passes
 // of fa_decode_shared).
 struct PagedLaunch {
     fa_paged_cache c;
     const void *q;              // [total_q][Hq][d]
     void *out;                  // [total_q][Hq][d] in out_dtype
     float *lse;                 // optional [total_q][Hq]
-    const float *init_o;        // optional earlier result of the same rows over other keys: fp32 rows
-    const float *init_lse;      //   and their natural-log log-sum-exp
     const int32_t *page_table;  // [B][max_pages]
     const int32_t *seq_lens;    // [B]
     const int32_t *cu_q;        // [B + 1], or null: max_q tokens for every sequence
     int B, Hq, total_q, max_q, max_pages;
-    int device;
-    int num_sms;      // (set by launch_paged)
-    long long units;  // (set by launch_paged) no more units of work than this
     int causal;
     float scale;
     int out_dtype;
-    void *scratch;              // paged_scratch_bytes(max_q, group, d, SMs), 16-byte aligned
+    void *scratch;              // paged_scratch_bytes(...), 16-byte aligned
 };
 
 size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms);
 int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
+
+// pre: one sequence of own.B query tokens; own: the same tokens, one per sequence.
+size_t paged_pair_scratch_bytes(int B, int Hq, int Hkv, int d, int num_sms);
+int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scratch, const DeviceInfo &dev,
+                      cudaStream_t stream);
 
 struct AppendLaunch {
     fa_paged_cache c;

@@ -33,9 +33,6 @@ struct PagedParams {
     const uint16_t *q;     // [total_q][Hq][D]
     void *out;             // [total_q][Hq][D]
     float *lse;            // optional [total_q][Hq]: natural-log row log-sum-exp, -inf for a row without keys
-    // Optional result over other keys that the rows also see (a shared prefix):
-    // normalised fp32 rows and their natural-log log-sum-exp, joined at the end.
-    const float *init_o, *init_lse;
     const int *page_table;  // [B][max_pages]
     const int *seq_lens;    // [B] keys of each sequence
     const int *cu_q;        // [B + 1] query token offsets, or null: nq_each tokens per sequence
@@ -52,6 +49,16 @@ struct PagedParams {
     float *part_o;          // [gridDim.x][2][RB][D], RB >= block_rows the kernel's slot size
     float *part_ml;         // [gridDim.x][2][RB][2]: m (log2 units), l
     int4 *open;             // [gridDim.x][2]: the unit a CTA leaves unfinished
+    // One of two passes over the same query rows, each over keys of its own (a shared
+    // prefix, then the sequences'), that paged_pair_join_kernel joins: whole units'
+    // rows go to dense_* as pieces do, and unit_note says where a unit's pieces are.
+    float *dense_o, *dense_ml;  // [total_q][Hq][D] and [total_q][Hq][2], or null: rows go to out
+    int2 *unit_note;            // [B][Hkv][row blocks]: the CTA that opened the unit, its pieces (1: dense)
+    // Such a pass also leaves SMs to the other one, in proportion to their work.
+    const int *peer_lens;       // the other pass's seq_lens
+    int peer_B, peer_max_len, peer_blocks, peer_tile, peer_unit_steps;
+    int step_ns, peer_step_ns;  // SM time of a step of this pass, and of the other
+    int num_sms, per_sm, first; // first: the pass that is launched first
 };
 
 // Bounded wait in which every lane polls the barrier itself, so that every lane's
@@ -157,8 +164,29 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
         if (w < warp) before += v;
         W += v;
     }
+    int most = gridDim.x;
+    if (p.peer_lens) {  // SMs in proportion to the two passes' work, at least one each
+        long long theirs = 0;
+        for (int b = tid; b < p.peer_B; b += NT) {
+            const int len = min(max(__ldg(p.peer_lens + b), 0), p.peer_max_len);
+            theirs += max(1, (len + p.peer_tile - 1) / p.peer_tile) + p.peer_unit_steps;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) theirs += __shfl_xor_sync(0xffffffffu, theirs, off);
+        __syncthreads();
+        if (lane == 0) warp_sum[warp] = theirs;
+        __syncthreads();
+        theirs = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) theirs += warp_sum[w];
+        const long long mine_ns = W * p.step_ns, their_ns = theirs * p.peer_blocks * p.Hkv * p.peer_step_ns;
+        const long long first_ns = p.first ? mine_ns : their_ns;
+        const int first_sms = static_cast<int>(min(max(p.num_sms * first_ns / (mine_ns + their_ns), 1LL),
+                                                   static_cast<long long>(max(p.num_sms - 1, 1))));
+        most = min(most, p.per_sm * (p.first ? first_sms : max(p.num_sms - first_sms, 1)));
+    }
     const int c = blockIdx.x;
-    const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), max(W, 1LL)));
+    const int G = static_cast<int>(min(static_cast<long long>(most), max(W, 1LL)));
     const long long first = c < G ? c * W / G : W;
     const long long end = c < G ? (c + 1) * W / G : W;
     if (tid == 0) {
@@ -266,6 +294,16 @@ __device__ __forceinline__ int paged_cta_of(long long step, long long W, int G) 
     return static_cast<int>(c);
 }
 
+// Where a unit's pieces are, for paged_pair_join_kernel: noted by the CTA whose piece starts it.
+__device__ __forceinline__ void paged_note_unit(const PagedParams &p, const PagedPiece &u, int tiles, const PagedStart &st) {
+    if (!p.unit_note || u.kind == 2) return;
+    const int blocks = (u.nq * p.G + p.block_rows - 1) / p.block_rows;
+    int2 *note = p.unit_note + (static_cast<long long>(u.b) * p.Hkv + u.hk) * blocks + u.row0 / p.block_rows;
+    const int c = blockIdx.x;
+    *note = u.kind == 0 ? make_int2(c, 1)
+                        : make_int2(c, paged_cta_of(st.end + (tiles - u.j1) - 1, st.W, st.G) - c + 1);
+}
+
 // What a CTA notes about the unit it leaves unfinished (or that there is none): u, its
 // last piece, ended where the CTA's range does.
 __device__ __forceinline__ void paged_note_open(const PagedParams &p, const PagedPiece *u, int tiles, long long end,
@@ -302,47 +340,16 @@ __device__ __forceinline__ void paged_store(const PagedParams &p, long long off,
     }
 }
 
-// N columns of the earlier result of a row, loaded ahead of their use.
-template <int N>
-struct PagedInit {
-    float o[N], m;  // m: log2 units
-    __device__ __forceinline__ void load(const PagedParams &p, int D, long long row, int col) {
-        if (!p.init_o) return;
-        const float *src = p.init_o + row * D + col;
-        m = p.init_lse[row] * kLog2e;
-        if constexpr (N == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src);
-            o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(src);
-            o[0] = v.x; o[1] = v.y;
-        }
-    }
-};
-
 // A whole row's (or all pieces') unnormalised columns acc with (m, l), m in log2
-// units: joins the optional earlier result and writes out, and the row's lse once.
+// units: writes out, and the row's lse once.
 template <int N>
 __device__ __forceinline__ void paged_finish(const PagedParams &p, int D, long long row, int col, float (&acc)[N],
-                                             float m, float l, const PagedInit<N> &init) {
-    const long long off = row * D + col;
-    float inv;
-    if (p.init_o) {
-        const float M = fmaxf(m, init.m);
-        const float w = ex2_from(m, M), wi = ex2_from(init.m, M);
-        const float total = fmaf(w, l, wi);
-        inv = total > 0.f ? 1.f / total : 0.f;
-        const float a = w * inv, c = wi * inv;
+                                             float m, float l) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(a, acc[e], c * init.o[e]);
-        if (p.lse && col == 0) p.lse[row] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
-    } else {
-        inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] *= inv;
-        if (p.lse && col == 0) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-    }
-    paged_store<N>(p, off, acc);
+    for (int e = 0; e < N; ++e) acc[e] *= inv;
+    if (p.lse && col == 0) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    paged_store<N>(p, row * D + col, acc);
 }
 
 // Row r of a block among the rows of the output.
@@ -351,19 +358,29 @@ __device__ __forceinline__ long long paged_row(const PagedParams &p, const Paged
     return (static_cast<long long>(u.t0) + rr / p.G) * p.Hq + u.hk * p.G + rr % p.G;
 }
 
-// N columns of a row of the current piece: finished rows go to out, cut ones to the CTA's partial slot.
+// Whether a piece's rows are kept as they are (unnormalised, with their m and l) for a
+// join, and the record of its row r in part_* or, for a whole unit, of row `row` in dense_*.
+__device__ __forceinline__ bool paged_keeps(const PagedParams &p, const PagedPiece &u) {
+    return u.kind != 0 || p.dense_o != nullptr;
+}
+template <int RB>
+__device__ __forceinline__ long long paged_record(const PagedPiece &u, int r, long long row) {
+    return u.kind == 0 ? row : (static_cast<long long>(blockIdx.x) * 2 + (u.kind == 1 ? 1 : 0)) * RB + r;
+}
+
+// N columns of row r of the current piece, row `row` of the output.
 template <int D, int RB, int N>
 __device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiece &u, int r, long long row, int col,
-                                           float (&acc)[N], float m, float l, const PagedInit<N> &init) {
-    if (u.kind == 0) {
-        paged_finish<N>(p, D, row, col, acc, m, l, init);
-    } else {
-        const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + (u.kind == 1 ? 1 : 0)) * RB + r;
-        float *o = p.part_o + rec * D + col;
-        if constexpr (N == 4) *reinterpret_cast<float4 *>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        else *reinterpret_cast<float2 *>(o) = make_float2(acc[0], acc[1]);
-        if (col == 0) *reinterpret_cast<float2 *>(p.part_ml + rec * 2) = make_float2(m, l);
+                                           float (&acc)[N], float m, float l) {
+    if (!paged_keeps(p, u)) {
+        paged_finish<N>(p, D, row, col, acc, m, l);
+        return;
     }
+    const long long rec = paged_record<RB>(u, r, row);
+    float *o = (u.kind == 0 ? p.dense_o : p.part_o) + rec * D + col;
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    else *reinterpret_cast<float2 *>(o) = make_float2(acc[0], acc[1]);
+    if (col == 0) *reinterpret_cast<float2 *>((u.kind == 0 ? p.dense_ml : p.part_ml) + rec * 2) = make_float2(m, l);
 }
 
 // Joins the pieces of the units that ranges cut: the unit that CTA c of the main
@@ -372,42 +389,37 @@ __device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiec
 // All latency.  Every CTA reads all notes at once and numbers the items (two rows
 // of a unit of at most four pieces, or one row of one with more), the warps of the
 // grid take the items in turn, and an item's loads (2 rows x 4 pieces, or 12
-// pieces) are in flight together.
+// pieces) are in flight together.  Where the items leave most warps idle, a CTA takes
+// an item and its warps a share of the pieces each (one long sequence: 300 pieces of
+// 64 rows took 26 us a warp per row).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinMax = 512;  // CTAs of the main kernel
 
-template <int D, int RB, int R, int F>
-__device__ __forceinline__ void paged_join_rows(const PagedParams &p, int c, const int4 &a, int r0, int rows, int lane) {
+// The sums of R rows over n pieces, F pieces at a time: ml_at(k, r) and row_at(k, r)
+// give a piece's (m, l) and its columns.  Lanes hold D / 32 columns each.
+template <int D, int R, int F, typename MlAt, typename RowAt>
+__device__ __forceinline__ void paged_add_pieces(int n, int rows, int lane, MlAt ml_at, RowAt row_at, float (&M)[R],
+                                                 float (&L)[R], float (&acc)[R][D / 32]) {
     constexpr int N = D / 32;
     using Vec = typename std::conditional<N == 4, float4, float2>::type;
-    const int n = a.x - c + 1;  // pieces
-    auto rec = [&](int k, int r) { return (static_cast<size_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; };
-    float M[R], L[R], acc[R][N];
-    PagedInit<N> init[R];
-    long long row[R];
+    static_assert(R * F <= 32, "a lane per (m, l)");
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         M[r] = -INFINITY;
         L[r] = 0.f;
-        const int rr = a.w + min(r0 + r, rows - 1);
-        row[r] = (static_cast<long long>(a.y) + rr / p.G) * p.Hq + a.z * p.G + rr % p.G;
-        init[r].load(p, D, row[r], lane * N);
 #pragma unroll
         for (int e = 0; e < N; ++e) acc[r][e] = 0.f;
     }
     for (int k0 = 0; k0 < n; k0 += F) {
         Vec x[R][F];
         // lane i * R + r holds the (m, l) of piece k0 + i and row r
-        const int lk = k0 + lane / R, lr = r0 + lane % R;
-        const float2 ml = lane < R * F && lk < n && lr < rows
-                              ? *reinterpret_cast<const float2 *>(p.part_ml + rec(lk, lr) * 2)
-                              : make_float2(-INFINITY, 0.f);
+        const int lk = k0 + lane / R, lr = lane % R;
+        const float2 ml = lane < R * F && lk < n && lr < rows ? ml_at(lk, lr) : make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int i = 0; i < F; ++i)
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (k0 + i < n && r0 + r < rows)
-                    x[r][i] = reinterpret_cast<const Vec *>(p.part_o + rec(k0 + i, r0 + r) * D)[lane];
+                if (k0 + i < n && r < rows) x[r][i] = reinterpret_cast<const Vec *>(row_at(k0 + i, r))[lane];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float next = M[r], mi[F];
@@ -433,9 +445,21 @@ __device__ __forceinline__ void paged_join_rows(const PagedParams &p, int c, con
             }
         }
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (r0 + r < rows) paged_finish<N>(p, D, row[r], lane * N, acc[r], M[r], L[r], init[r]);
+}
+
+template <int D, int RB, int R, int F>
+__device__ __forceinline__ void paged_join_rows(const PagedParams &p, int c, const int4 &a, int r0, int rows, int lane,
+                                                int k0, int n, float (&M)[R], float (&L)[R], float (&acc)[R][D / 32]) {
+    auto rec = [&](int k, int r) { return (static_cast<size_t>(c + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0)) * RB + r0 + r; };
+    paged_add_pieces<D, R, F>(
+        n, rows - r0, lane, [&](int k, int r) { return *reinterpret_cast<const float2 *>(p.part_ml + rec(k, r) * 2); },
+        [&](int k, int r) { return p.part_o + rec(k, r) * D; }, M, L, acc);
+}
+
+// The output row of row r of the unit that note a describes.
+__device__ __forceinline__ long long paged_noted_row(const PagedParams &p, const int4 &a, int r) {
+    const int rr = a.w + r;
+    return (static_cast<long long>(a.y) + rr / p.G) * p.Hq + a.z * p.G + rr % p.G;
 }
 
 template <int D, int RB>
@@ -484,17 +508,148 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
         before += items[i];
     }
     __syncthreads();
-    for (int item = blockIdx.x * (kJoinThreads / 32) + warp; item < total; item += gridDim.x * (kJoinThreads / 32)) {
-        int lo = 0, hi = ctas - 1;  // the last c with first[c] <= item (those without a unit have none after it)
+    constexpr int N = D / 32, kWarps = kJoinThreads / 32;
+    auto unit_of = [&](int item) {  // the last c with first[c] <= item (those without a unit have none after it)
+        int lo = 0, hi = ctas - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (first[mid] <= item) lo = mid; else hi = mid - 1;
         }
-        const int4 a = note[lo];
-        const int i = item - first[lo];
-        if (a.x - lo < 4) paged_join_rows<D, RB, 2, 4>(p, lo, a, i * 2, rows_of[lo], lane);
-        else paged_join_rows<D, RB, 1, 12>(p, lo, a, i, rows_of[lo], lane);
+        return lo;
+    };
+    if (total <= static_cast<int>(gridDim.x)) {
+        __shared__ __align__(16) float part[kWarps][D];
+        __shared__ float2 part_ml[kWarps];
+        if (static_cast<int>(blockIdx.x) >= total) return;
+        const int c = unit_of(blockIdx.x), i = blockIdx.x - first[c];
+        const int4 a = note[c];
+        const int n = a.x - c + 1, rows = rows_of[c], per = n <= 4 ? 2 : 1;
+        for (int r = i * per; r < min(rows, i * per + per); ++r) {
+            const int k0 = warp * n / kWarps, k1 = (warp + 1) * n / kWarps;
+            float M[1], L[1], acc[1][N];
+            paged_join_rows<D, RB, 1, 12>(p, c, a, r, rows, lane, k0, k1 - k0, M, L, acc);
+#pragma unroll
+            for (int e = 0; e < N; ++e) part[warp][lane * N + e] = acc[0][e];
+            if (lane == 0) part_ml[warp] = make_float2(M[0], L[0]);
+            __syncthreads();
+            if (warp == 0) {
+                float top = -INFINITY, sum = 0.f, o[N] = {};
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_ml[w].x);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = ex2_from(part_ml[w].x, top);
+                    sum = fmaf(f, part_ml[w].y, sum);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) o[e] = fmaf(f, part[w][lane * N + e], o[e]);
+                }
+                paged_finish<N>(p, D, paged_noted_row(p, a, r), lane * N, o, top, sum);
+            }
+            __syncthreads();
+        }
+        return;
     }
+    for (int item = blockIdx.x * kWarps + warp; item < total; item += gridDim.x * kWarps) {
+        const int c = unit_of(item), i = item - first[c];
+        const int4 a = note[c];
+        const int n = a.x - c + 1, rows = rows_of[c];
+        if (n <= 4) {
+            float M[2], L[2], acc[2][N];
+            paged_join_rows<D, RB, 2, 4>(p, c, a, i * 2, rows, lane, 0, n, M, L, acc);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (i * 2 + r < rows) paged_finish<N>(p, D, paged_noted_row(p, a, i * 2 + r), lane * N, acc[r], M[r], L[r]);
+        } else {
+            float M[1], L[1], acc[1][N];
+            paged_join_rows<D, RB, 1, 12>(p, c, a, i, rows, lane, 0, n, M, L, acc);
+            paged_finish<N>(p, D, paged_noted_row(p, a, i), lane * N, acc[0], M[0], L[0]);
+        }
+    }
+}
+
+// Joins two passes over the same rows, one query token per sequence: a over keys that
+// all sequences share (one sequence of B tokens), b over each sequence's own.  A warp
+// takes R rows at a time; their notes, then their pieces, a's first and in CTA order.
+template <int D, int R, int F>
+__device__ __forceinline__ void paged_pair_rows(const PagedParams &a, const PagedParams &b, int slot_a, int slot_b,
+                                                int blocks_a, int blocks_b, int row0, int rows, int lane) {
+    constexpr int N = D / 32;
+    // lane 2 r: row r's note in a; lane 2 r + 1: in b
+    int2 note = make_int2(0, 0);
+    int off = 0;
+    if (lane < 2 * R && lane / 2 < rows) {
+        const int row = row0 + lane / 2, s = row / b.Hq, h = row % b.Hq, hk = h / b.G, g = h % b.G;
+        if (lane & 1) {
+            note = b.unit_note[(static_cast<long long>(s) * b.Hkv + hk) * blocks_b + g / b.block_rows];
+            off = g % b.block_rows;
+        } else {
+            const int r = s * b.G + g;
+            note = a.unit_note[static_cast<long long>(hk) * blocks_a + r / a.block_rows];
+            off = r % a.block_rows;
+        }
+    }
+    int ca[R], na[R], oa[R], cb[R], nb[R], ob[R], most = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        ca[r] = __shfl_sync(0xffffffffu, note.x, 2 * r);
+        na[r] = __shfl_sync(0xffffffffu, note.y, 2 * r);
+        oa[r] = __shfl_sync(0xffffffffu, off, 2 * r);
+        cb[r] = __shfl_sync(0xffffffffu, note.x, 2 * r + 1);
+        nb[r] = __shfl_sync(0xffffffffu, note.y, 2 * r + 1);
+        ob[r] = __shfl_sync(0xffffffffu, off, 2 * r + 1);
+        most = max(most, na[r] + nb[r]);
+    }
+    // Piece k of row r: in pass a or b, and its record there; false behind the row's last one.
+    auto find = [&](int k, int r, bool &in_a, bool &dense, long long &rec) {
+        int c = ca[0], n = na[0], o = oa[0], c2 = cb[0], n2 = nb[0], o2 = ob[0];
+#pragma unroll
+        for (int i = 1; i < R; ++i)
+            if (r == i) { c = ca[i]; n = na[i]; o = oa[i]; c2 = cb[i]; n2 = nb[i]; o2 = ob[i]; }
+        in_a = k < n;
+        if (!in_a) { k -= n; c = c2; n = n2; o = o2; }
+        dense = n == 1;
+        rec = dense ? row0 + r : (static_cast<long long>(c + k) * 2 + (k == 0 ? 1 : 0)) * (in_a ? slot_a : slot_b) + o;
+        return k < n;
+    };
+    float M[R], L[R], acc[R][N];
+    paged_add_pieces<D, R, F>(
+        most, rows, lane,
+        [&](int k, int r) {
+            bool in_a, dense;
+            long long rec;
+            if (!find(k, r, in_a, dense, rec)) return make_float2(-INFINITY, 0.f);
+            const PagedParams &x = in_a ? a : b;
+            return *reinterpret_cast<const float2 *>((dense ? x.dense_ml : x.part_ml) + rec * 2);
+        },
+        [&](int k, int r) -> const float * {
+            bool in_a, dense;
+            long long rec;
+            if (!find(k, r, in_a, dense, rec)) return b.dense_o;  // any row: it has no weight
+            const PagedParams &x = in_a ? a : b;
+            return (dense ? x.dense_o : x.part_o) + rec * D;
+        },
+        M, L, acc);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r < rows) paged_finish<N>(b, D, row0 + r, lane * N, acc[r], M[r], L[r]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    paged_pair_join_kernel(const PagedParams a, const PagedParams b, const int slot_a, const int slot_b,
+                           const int blocks_a, const int blocks_b) {
+    const int lane = threadIdx.x & 31;
+    const int rows = b.total_q * b.Hq;
+    const int warps = gridDim.x * (kJoinThreads / 32), w = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // rows enough for every warp: two at a time, few pieces each; else one with more of its pieces in flight
+    if (rows >= 2 * warps)
+        for (int r = 2 * w; r < rows; r += 2 * warps)
+            paged_pair_rows<D, 2, 4>(a, b, slot_a, slot_b, blocks_a, blocks_b, r, rows - r, lane);
+    else
+        for (int r = w; r < rows; r += warps)
+            paged_pair_rows<D, 1, 12>(a, b, slot_a, slot_b, blocks_a, blocks_b, r, 1, lane);
 }
 
 // ---------------------------------------------------------------- host side
@@ -521,7 +676,28 @@ inline int make_page_map(CUtensorMap *map, const void *base, const fa_paged_cach
     return FA_OK;
 }
 
-int launch_paged_tiles(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream_t stream);
+// How a call runs, from its sizes alone.
+struct PagedPlan {
+    bool tiles;      // 128-row tensor-memory tiles (paged_tiles_kernel), else paged_rows_kernel
+    int block_rows;  // query rows of a unit
+    int slot_rows;   // rows of a partial slot
+    int tile;        // keys per step
+    int per_sm;      // CTAs per SM
+    int unit_steps;  // what a unit costs besides its key tiles, in steps
+};
+
+// One launch of a main kernel, with its join or without.
+struct PagedPass {
+    fa_paged_cache c;
+    PagedParams p;
+    PagedPlan plan;
+    int grid, blocks;  // CTAs; row blocks of the longest sequence, per kv head
+    long long units;   // no more units than this exist
+    int device, num_sms;
+    bool early, join;  // early: may start before the kernels ahead of it have finished
+};
+
+int launch_paged_tiles(const PagedPass &a, cudaStream_t stream);
 
 // Launch attributes of the paged kernels; `early`: may start before the kernels
 // ahead of it in the stream have finished (it waits for them where it must).
@@ -556,14 +732,13 @@ int ready_kernel(K kernel, int smem, int min_regs, int device, std::atomic<bool>
     return FA_OK;
 }
 
-// ctas: the main kernel's; units: no more units than this exist.
 template <int D, int RB>
-int launch_join(const PagedParams &p, int ctas, long long units, int num_sms, cudaStream_t stream) {
-    if (ctas > kJoinMax) return cuda_fail(cudaErrorInvalidConfiguration);
-    const long long items = std::min<long long>(ctas, units) * p.block_rows, warps = kJoinThreads / 32;
-    const int grid = static_cast<int>(std::min<long long>(2LL * num_sms, (items + warps - 1) / warps));
+int launch_join(const PagedPass &a, cudaStream_t stream) {
+    if (a.grid > kJoinMax) return cuda_fail(cudaErrorInvalidConfiguration);
+    const long long rows = std::min<long long>(a.grid, a.units) * std::min<long long>(a.p.block_rows, 1LL * a.p.max_q * a.p.G);
+    const int grid = static_cast<int>(std::min<long long>(2LL * a.num_sms, rows));
     PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, p, ctas);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, a.p, a.grid);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

@@ -106,7 +106,7 @@ int check_attention(const Attention &a) {
     return FA_OK;
 }
 
-PagedLaunch launch_of(const Attention &a, int causal, const DeviceInfo &dev) {
+PagedLaunch launch_of(const Attention &a, int causal) {
     PagedLaunch l = {};
     l.c = *a.c;
     l.q = a.q;
@@ -120,7 +120,6 @@ PagedLaunch launch_of(const Attention &a, int causal, const DeviceInfo &dev) {
     l.total_q = a.total;
     l.max_q = a.max_q;
     l.max_pages = a.max_pages;
-    l.device = dev.device;
     l.causal = causal ? 1 : 0;
     l.scale = a.scale;
     l.out_dtype = a.out_dtype;
@@ -160,7 +159,7 @@ int run_attention(const Attention &a, int causal, void *workspace, size_t worksp
     int rc = current_device_info(&dev);
     if (rc != FA_OK) return rc;
     if (a.total == 0) return FA_OK;
-    PagedLaunch l = launch_of(a, causal, dev);
+    PagedLaunch l = launch_of(a, causal);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Scratch s(st);
     // (a workspace is sized for max_seqlen_q, which fewer tokens than that do not change)
@@ -169,20 +168,6 @@ int run_attention(const Attention &a, int causal, void *workspace, size_t worksp
     l.scratch = s.ptr;
     return s.done(launch_paged(l, dev, st));
 }
-
-size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
-
-// fa_decode_shared: both steps' partial rows, and the prefix step's rows and log-sum-exp.
-struct SharedScratch {
-    size_t first, second, rows, lse, total;
-    SharedScratch(int B, int Hq, int group, int d, int num_sms) {
-        first = 0;
-        second = align256(paged_scratch_bytes(B, group, d, num_sms));
-        rows = second + align256(paged_scratch_bytes(1, group, d, num_sms));
-        lse = rows + align256(static_cast<size_t>(B) * Hq * d * 4);
-        total = lse + align256(static_cast<size_t>(B) * Hq * 4);
-    }
-};
 
 int sms_of(int device) {
     cudaError_t e;
@@ -296,7 +281,7 @@ size_t fa_paged_workspace_bytes(int Hq, int Hkv, int max_seqlen_q, int d, int de
 size_t fa_shared_workspace_bytes(int B, int Hq, int Hkv, int d, int device) {
     if (!head_sizes_ok(Hq, Hkv, d) || B < 1) return 0;
     const int sms = sms_of(device);
-    return sms < 0 ? 0 : SharedScratch(B, Hq, Hq / Hkv, d, sms).total;
+    return sms < 0 ? 0 : paged_pair_scratch_bytes(B, Hq, Hkv, d, sms);
 }
 
 int fa_prefill_paged(const fa_paged_cache *cache, const void *q, void *out, float *lse, const int32_t *page_table,
@@ -338,24 +323,10 @@ int fa_decode_shared(const fa_paged_cache *cache, const void *q, void *out, cons
     DeviceInfo dev;
     if ((rc = current_device_info(&dev)) != FA_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const SharedScratch w(B, Hq, Hq / cache->num_heads, cache->head_dim, dev.num_sms);
     Scratch s(st);
-    if ((rc = s.take(workspace, workspace_bytes, w.total)) != FA_OK) return rc;
-    char *base = static_cast<char *>(s.ptr);
-    PagedLaunch l = launch_of(pre, 0, dev);
-    l.out = base + w.rows;
-    l.out_dtype = FA_F32;
-    l.lse = reinterpret_cast<float *>(base + w.lse);
-    l.scratch = base + w.first;
-    rc = launch_paged(l, dev, st);
-    if (rc == FA_OK) {
-        PagedLaunch o = launch_of(own, 0, dev);
-        o.init_o = static_cast<const float *>(l.out);
-        o.init_lse = l.lse;
-        o.scratch = base + w.second;
-        rc = launch_paged(o, dev, st);
-    }
-    return s.done(rc);
+    const size_t need = paged_pair_scratch_bytes(B, Hq, cache->num_heads, cache->head_dim, dev.num_sms);
+    if ((rc = s.take(workspace, workspace_bytes, need)) != FA_OK) return rc;
+    return s.done(launch_paged_pair(launch_of(pre, 0), launch_of(own, 0), s.ptr, dev, st));
 }
 
 }  // extern "C"

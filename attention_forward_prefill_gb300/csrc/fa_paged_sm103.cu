@@ -117,7 +117,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         bool any = false;
         while (ok) {
             const bool more = cur.next(p, u, unit_tiles);
-            if (!more) {
+            if (more) {
+                if (lane == 0) paged_note_unit(p, u, unit_tiles, *start);
+            } else {
                 if (lane == 0) paged_note_open(p, any ? &u : nullptr, unit_tiles, start->end, start->W, start->G);
                 u.kind = -1;
             }
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         float *join = reinterpret_cast<float *>(smem + L::kJoinOff);
         float2 *join_ml = reinterpret_cast<float2 *>(smem + L::kJoinOff + kConsumers * 16 * kJoinCols * 4);
         uint32_t joins = 0;
-        bool ok = true, waited = false;
+        bool ok = true;
         while (ok) {
             if (!lanes_wait(u_full, units & 1, abort_flag)) { ok = false; break; }
             ++units;
@@ -313,29 +315,16 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             }
             m0 -= kShift;  // (-inf stays)
             m1 -= kShift;
-            if (!waited) {
-                // an earlier result to join, and the partial slots, are free to use only now
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                waited = true;
-            }
             const int rows = min(RB, u.nq * p.G - u.row0);
             if constexpr (KG == 1) {
                 auto write = [&](int r, float m, float l, auto half) {
                     constexpr int H = decltype(half)::value;
                     if (r >= rows) return;
                     const long long row = paged_row(p, u, r);
-                    constexpr int U = 1;  // column pairs whose earlier result is in flight
 #pragma unroll
-                    for (int i0 = 0; i0 < D / 8; i0 += U) {
-                        PagedInit<2> init[U];
-                        if (u.kind == 0)
-#pragma unroll
-                            for (int i = 0; i < U; ++i) init[i].load(p, D, row, (i0 + i) * 8 + quad * 2);
-#pragma unroll
-                        for (int i = 0; i < U; ++i) {
-                            float a[2] = {o[i0 + i][2 * H], o[i0 + i][2 * H + 1]};
-                            paged_emit<D, RB, 2>(p, u, r, row, (i0 + i) * 8 + quad * 2, a, m, l, init[i]);
-                        }
+                    for (int i = 0; i < D / 8; ++i) {
+                        float a[2] = {o[i][2 * H], o[i][2 * H + 1]};
+                        paged_emit<D, RB, 2>(p, u, r, row, i * 8 + quad * 2, a, m, l);
                     }
                 };
                 write(r0, m0, l0, std::integral_constant<int, 0>{});
@@ -349,7 +338,6 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                     constexpr int RU = decltype(used)::value;    // rows that exist, rounded up
                     constexpr int C = kJoinCols * 16 / RU < D ? kJoinCols * 16 / RU : D;  // columns per pass
                     constexpr int kCells = RU * C / 4, kPer = (kCells + KG * 32 - 1) / (KG * 32);
-                    constexpr int kAhead = kPer == 1 ? D / C : 1;  // passes whose earlier result is in flight
                     const int cell = kw * 32 + lane;
                     auto cell_row = [&](int i) { return (cell + i * KG * 32) / (C / 4); };
                     const int cell_col = cell % (C / 4) * 4;
@@ -357,25 +345,15 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                     auto at = [&](int g, int r, int col) {
                         return buf + (g * RU + r) * C + (((col >> 2) ^ (r & 7)) << 2) + (col & 3);
                     };
-                    PagedInit<4> init[kPer][kAhead];
                     long long row[kPer];
                     bool live[kPer];
-                    auto load_init = [&](int pass0) {
-#pragma unroll
-                        for (int i = 0; i < kPer; ++i)
-                            if (u.kind == 0 && live[i])
-#pragma unroll
-                                for (int k = 0; k < kAhead; ++k) init[i][k].load(p, D, row[i], (pass0 + k) * C + cell_col);
-                    };
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
                         live[i] = cell + i * KG * 32 < kCells && rw * 16 + cell_row(i) < rows;
                         row[i] = paged_row(p, u, rw * 16 + cell_row(i));
                     }
-                    load_init(0);
 #pragma unroll
                     for (int pass = 0; pass < D / C; ++pass) {
-                        if (pass > 0 && pass % kAhead == 0) load_init(pass);
                         if (joins > 0 && !lanes_wait(j_empty + rw, (joins - 1) & 1, abort_flag)) { ok = false; return; }
 #pragma unroll
                         for (int i = 0; i < C / 8; ++i) {
@@ -412,8 +390,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                                 acc[2] = fmaf(w, v.z, acc[2]);
                                 acc[3] = fmaf(w, v.w, acc[3]);
                             }
-                            paged_emit<D, RB, 4>(p, u, rw * 16 + r, row[i], pass * C + cell_col, acc, M, Ls,
-                                                 init[i][pass % kAhead]);
+                            paged_emit<D, RB, 4>(p, u, rw * 16 + r, row[i], pass * C + cell_col, acc, M, Ls);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(j_empty + rw);
@@ -441,8 +418,16 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     }
 }
 
+// How a call runs, from its sizes alone.
+PagedPlan plan_paged(int max_q, int group) {
+    const long long rows = static_cast<long long>(max_q) * group;
+    if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256, 128, 1, 2};
+    const int rb = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+    return {false, rb, rb, kTile, 2, 2};
+}
+
 template <int D, int RT, bool BF16>
-int launch_rows(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream_t stream) {
+int launch_rows(const PagedPass &a, cudaStream_t stream) {
     using L = PagedLayout<D, RT>;
     CUtensorMap mk, mv;
     int rc;
@@ -451,55 +436,57 @@ int launch_rows(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream
     const auto kernel = paged_rows_kernel<D, RT, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, a.device, ready)) != FA_OK) return rc;
-    PagedConfig cfg(grid, kPagedThreads, L::kSmemBytes, a.init_o != nullptr, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mk, mv, p);
+    PagedConfig cfg(a.grid, kPagedThreads, L::kSmemBytes, a.early, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mk, mv, a.p);
     if (e != cudaSuccess) return cuda_fail(e);
-    return launch_join<D, L::kRows>(p, grid, a.units, a.num_sms, stream);
+    return a.join ? launch_join<D, L::kRows>(a, stream) : FA_OK;
 }
 
 template <int D, bool BF16>
-int launch_rows_d(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream_t stream) {
-    switch (p.block_rows) {
-        case 16: return launch_rows<D, 1, BF16>(a, p, grid, stream);
-        case 32: return launch_rows<D, 2, BF16>(a, p, grid, stream);
-        default: return launch_rows<D, 4, BF16>(a, p, grid, stream);
+int launch_rows_d(const PagedPass &a, cudaStream_t stream) {
+    switch (a.plan.block_rows) {
+        case 16: return launch_rows<D, 1, BF16>(a, stream);
+        case 32: return launch_rows<D, 2, BF16>(a, stream);
+        default: return launch_rows<D, 4, BF16>(a, stream);
     }
 }
 
-// How a call runs, from its sizes alone.
-struct PagedPlan {
-    bool tiles;      // 128-row tensor-memory tiles (paged_tiles_kernel), else paged_rows_kernel
-    int block_rows;  // query rows of a unit
-    int slot_rows;   // rows of a partial slot
-    int tile;        // keys per step
-    int per_sm;      // CTAs per SM
-    int unit_steps;  // what a unit costs besides its key tiles
-};
-
-PagedPlan plan_paged(int max_q, int group) {
-    const long long rows = static_cast<long long>(max_q) * group;
-    if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256, 128, 1, 2};
-    const int rb = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    return {false, rb, rb, kTile, 2, 2};
+int launch_pass(const PagedPass &a, cudaStream_t stream) {
+    if (a.plan.tiles) return launch_paged_tiles(a, stream);
+    const bool bf16 = a.c.dtype == FA_BF16;
+    if (a.c.head_dim == 64) return bf16 ? launch_rows_d<64, true>(a, stream) : launch_rows_d<64, false>(a, stream);
+    return bf16 ? launch_rows_d<128, true>(a, stream) : launch_rows_d<128, false>(a, stream);
 }
 
-}  // namespace
+// What a step of a pass costs an SM, in ns, measured on runs confined to a few SMs; only
+// the ratio of two passes counts.  (Shared prefix of 16500 tokens for 256 sequences of
+// 16 to 1024 own ones, 64 query heads: 202 us with the SMs split so, 228 one after the other.)
+int step_ns(const PagedPlan &pl, int d) {
+    if (pl.tiles) return d == 128 ? 1900 : 1400;
+    const int ns = pl.block_rows == 16 ? 420 : (pl.block_rows == 32 ? 800 : 1150);
+    return d == 128 ? ns : ns * 5 / 6;
+}
 
-// Partial rows, (m, l) and unit notes of one attention over pages, for the largest grid.
-size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms) {
-    const PagedPlan pl = plan_paged(max_q, group);
-    const size_t slots = static_cast<size_t>(pl.per_sm) * num_sms * 2;
-    const size_t rec = slots * pl.slot_rows;
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// Partial rows, (m, l) and notes of one pass with the largest grid.
+size_t pass_bytes(const PagedPlan &pl, int d, int num_sms) {
+    const size_t slots = static_cast<size_t>(pl.per_sm) * num_sms * 2, rec = slots * pl.slot_rows;
     return rec * d * 4 + rec * 8 + slots * sizeof(int4);
 }
 
-int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
-    PagedParams p;
+PagedPass make_pass(const PagedLaunch &a, const DeviceInfo &dev, void *scratch) {
+    PagedPass x;
+    x.c = a.c;
+    x.device = dev.device;
+    x.num_sms = dev.num_sms;
+    x.early = false;
+    x.join = true;
+    PagedParams &p = x.p;
+    p = PagedParams{};
     p.q = static_cast<const uint16_t *>(a.q);
     p.out = a.out;
     p.lse = a.lse;
-    p.init_o = a.init_o;
-    p.init_lse = a.init_lse;
     p.page_table = a.page_table;
     p.seq_lens = a.seq_lens;
     p.cu_q = a.cu_q;
@@ -518,26 +505,90 @@ int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t strea
     p.causal = a.causal;
     p.scale_log2 = a.scale * kLog2e;
     p.out_dtype = a.out_dtype;
-    const PagedPlan pl = plan_paged(a.max_q, p.G);
+    const PagedPlan pl = x.plan = plan_paged(a.max_q, p.G);
     p.block_rows = pl.block_rows;
     p.unit_steps = pl.unit_steps;
     const int most = pl.per_sm * dev.num_sms;
     const size_t slots = static_cast<size_t>(most) * 2, rec = slots * pl.slot_rows;
-    p.part_o = static_cast<float *>(a.scratch);
+    p.part_o = static_cast<float *>(scratch);
     p.part_ml = p.part_o + rec * a.c.head_dim;
     p.open = reinterpret_cast<int4 *>(p.part_ml + rec * 2);
     // no more CTAs than the call can have steps
     const long long rows = static_cast<long long>(a.max_q) * p.G;
-    PagedLaunch l = a;
-    l.num_sms = dev.num_sms;
-    l.units = static_cast<long long>(a.B) * p.Hkv * ((rows + pl.block_rows - 1) / pl.block_rows);
-    const long long steps = l.units * ((p.max_len + pl.tile - 1) / pl.tile);
-    const int grid = static_cast<int>(std::min<long long>(most, steps));
-    if (pl.tiles) return launch_paged_tiles(l, p, grid, stream);
-    const bool bf16 = a.c.dtype == FA_BF16;
-    if (a.c.head_dim == 64)
-        return bf16 ? launch_rows_d<64, true>(l, p, grid, stream) : launch_rows_d<64, false>(l, p, grid, stream);
-    return bf16 ? launch_rows_d<128, true>(l, p, grid, stream) : launch_rows_d<128, false>(l, p, grid, stream);
+    x.blocks = static_cast<int>((rows + pl.block_rows - 1) / pl.block_rows);
+    x.units = static_cast<long long>(a.B) * p.Hkv * x.blocks;
+    x.grid = static_cast<int>(std::min<long long>(most, x.units * ((p.max_len + pl.tile - 1) / pl.tile)));
+    return x;
+}
+
+}  // namespace
+
+size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms) {
+    return pass_bytes(plan_paged(max_q, group), d, num_sms);
+}
+
+int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
+    return launch_pass(make_pass(a, dev, a.scratch), stream);
+}
+
+size_t paged_pair_scratch_bytes(int B, int Hq, int Hkv, int d, int num_sms) {
+    const size_t rows = static_cast<size_t>(B) * Hq;
+    size_t total = 0;
+    for (int i = 0; i < 2; ++i) {
+        const PagedPlan pl = plan_paged(i ? 1 : B, Hq / Hkv);
+        const size_t per = static_cast<size_t>(i ? 1 : B) * (Hq / Hkv);
+        const size_t units = static_cast<size_t>(i ? B : 1) * Hkv * ((per + pl.block_rows - 1) / pl.block_rows);
+        total += align256(pass_bytes(pl, d, num_sms)) + align256(rows * d * 4) + align256(rows * 8) +
+                 align256(units * sizeof(int2));
+    }
+    return total;
+}
+
+// The two passes share the SMs: the second starts on those that the first leaves,
+// and neither waits for the other; the join waits for both.
+int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scratch, const DeviceInfo &dev,
+                      cudaStream_t stream) {
+    const size_t rows = static_cast<size_t>(own.B) * own.Hq;
+    const int d = own.c.head_dim;
+    char *at = static_cast<char *>(scratch);
+    PagedPass pass[2];
+    for (int i = 0; i < 2; ++i) {
+        PagedPass &x = pass[i] = make_pass(i ? own : pre, dev, at);
+        at += align256(pass_bytes(x.plan, d, dev.num_sms));
+        x.p.dense_o = reinterpret_cast<float *>(at);
+        at += align256(rows * d * 4);
+        x.p.dense_ml = reinterpret_cast<float *>(at);
+        at += align256(rows * 8);
+        x.p.unit_note = reinterpret_cast<int2 *>(at);
+        at += align256(x.units * sizeof(int2));
+        x.join = false;
+        x.early = i == 1;
+        x.p.first = i == 0;
+        x.p.num_sms = dev.num_sms;
+        x.p.per_sm = x.plan.per_sm;
+        x.p.step_ns = step_ns(x.plan, d);
+    }
+    for (int i = 0; i < 2; ++i) {
+        const PagedPass &o = pass[1 - i];
+        PagedParams &p = pass[i].p;
+        p.peer_lens = o.p.seq_lens;
+        p.peer_B = o.p.B;
+        p.peer_max_len = o.p.max_len;
+        p.peer_blocks = o.blocks;
+        p.peer_tile = o.plan.tile;
+        p.peer_unit_steps = o.plan.unit_steps;
+        p.peer_step_ns = o.p.step_ns;
+    }
+    int rc;
+    for (const PagedPass &x : pass)
+        if ((rc = launch_pass(x, stream)) != FA_OK) return rc;
+    constexpr long long kWarps = kJoinThreads / 32;
+    const int grid = static_cast<int>(std::min<long long>(2LL * dev.num_sms, (static_cast<long long>(rows) + kWarps - 1) / kWarps));
+    PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, d == 64 ? paged_pair_join_kernel<64> : paged_pair_join_kernel<128>,
+                                             pass[0].p, pass[1].p, pass[0].plan.slot_rows, pass[1].plan.slot_rows,
+                                             pass[0].blocks, pass[1].blocks);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
 int read_paged_status(int reset) {

@@ -65,7 +65,8 @@ struct TilesLayout {
     static constexpr int kPieceOff = kMiscOff + 8;
     static constexpr int kStartOff = kPieceOff + 2 * (((int)sizeof(PagedPiece) + 7) / 8 * 8);
     static constexpr int kSumOff = kStartOff + (int)sizeof(PagedStart);
-    static constexpr int kSmemBytes = kSumOff + 8 * (kThreads / 32);
+    static constexpr int kStageOff = (kSumOff + 8 * (kThreads / 32) + 127) / 128 * 128;  // rows on their way out
+    static constexpr int kSmemBytes = kStageOff + 8 * 32 * 32 * 4;
     static constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 256 + D;
     static constexpr bool kSepP = D == 64;
     static constexpr uint32_t kP0 = kSepP ? 256 + 2 * D : kS0;
@@ -173,7 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool any = false;
         while (ok) {
             const bool more = cur.next(p, u, unit_tiles);
-            if (!more) {
+            if (more) {
+                if (lane == 0) paged_note_unit(p, u, unit_tiles, *start);
+            } else {
                 if (lane == 0) paged_note_open(p, any ? &u : nullptr, unit_tiles, start->end, start->W, start->G);
                 u.kind = -1;
             }
@@ -346,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t p_addr = tmem + lanes + (t ? L::kP1 : L::kP0);
         const float cexp = p.scale_log2, cabs = fabsf(p.scale_log2);
         uint32_t sc = 0, oc = 0, pvc = 0;
-        bool waited = false;
         while (ok) {
             const PagedPiece u = take_piece();
             if (u.kind < 0) break;
@@ -355,11 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int end = tile_end(p, u, row_t, tile_rows);
             const int rr = row_t + r;  // row among the sequence's nq * G
             const bool row_ok = r < tile_rows && rr < u.nq * p.G;
-            const size_t rec = (static_cast<size_t>(blockIdx.x) * 2 + (u.kind == 1 ? 1 : 0)) * (2 * kM) + t * tile_rows + r;
-            if (!waited) {  // an earlier result to join, and the partial slots, are free to use only now
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                waited = true;
-            }
+            const long long row = paged_row(p, u, t * tile_rows + r);
+            const bool keep = paged_keeps(p, u);
+            const long long rec = paged_record<2 * kM>(u, t * tile_rows + r, row);
             if (end <= j0) {
                 // a cut unit's piece without keys for this tile: nothing to add
                 if (u.kind != 0 && row_ok) *reinterpret_cast<float2 *>(p.part_ml + rec * 2) = make_float2(-INFINITY, 0.f);
@@ -459,48 +459,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const float m = m_ref - kShift;  // (-inf stays)
-            const long long row = paged_row(p, u, t * tile_rows + r);
-            float a = 1.f, ai = 0.f;  // weights of this pass and of the earlier result
-            if (u.kind == 0 && row_ok) {
-                if (p.init_o) {
-                    const float mi = p.init_lse[row] * kLog2e, M = fmaxf(m, mi);
-                    const float w = ex2_from(m, M), wi = ex2_from(mi, M), total = fmaf(w, l, wi);
-                    const float inv = total > 0.f ? 1.f / total : 0.f;
-                    a = w * inv;
-                    ai = wi * inv;
-                    if (p.lse) p.lse[row] = total > 0.f ? (M + __log2f(total)) * kLn2 : -INFINITY;
-                } else {
-                    a = l > 0.f ? 1.f / l : 0.f;
-                    if (p.lse) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-                }
-            } else if (row_ok) {
-                *reinterpret_cast<float2 *>(p.part_ml + rec * 2) = make_float2(m, l);
+            const float inv = keep ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+            if (row_ok) {
+                if (keep)
+                    *reinterpret_cast<float2 *>((u.kind == 0 ? p.dense_ml : p.part_ml) + rec * 2) = make_float2(m, l);
+                else if (p.lse)
+                    p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
             }
-            const int osize = p.out_dtype == FA_F32 ? 4 : 2;
+            // A lane holds a row, and a row's neighbours in memory are its columns: 32 rows x 32
+            // words at a time turn in shared memory, so that eight lanes write a row's 128 bytes.
+            // (Lanes writing rows of their own took 4 us per piece, as 16-byte stores far apart.)
+            const bool wide = keep || p.out_dtype == FA_F32;
+            const int bf = p.out_dtype == FA_BF16;
+            uint8_t *base = reinterpret_cast<uint8_t *>(keep ? (u.kind == 0 ? p.dense_o : p.part_o) : p.out);
+            const long long offset = row_ok ? (keep ? rec : row) * D * (wide ? 4 : 2) : -1;
+            uint32_t *stage = reinterpret_cast<uint32_t *>(smem + L::kStageOff) + warp * 32 * 32;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tmem_ld32(o_addr + q * 32, o);
                 tmem_ld_wait();
                 reg_fence32(o);
-                if (row_ok) {
-                    if (u.kind != 0) {
-                        store_out32(p.part_o + rec * D + q * 32, o, 1.f, FA_F32);
-                    } else {
-                        if (p.init_o) {
-                            const float *e = p.init_o + row * D + q * 32;
+                // 16-byte chunks of a row change places by row, against bank conflicts
+                auto put = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+                    *reinterpret_cast<uint4 *>(stage + lane * 32 + ((chunk ^ (lane & 7)) << 2)) = make_uint4(x, y, z, w);
+                };
+                auto f = [&](int c) { return __uint_as_float(o[c]) * inv; };
+                if (wide) {
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const float4 v = *reinterpret_cast<const float4 *>(e + c);
-                                o[c] = __float_as_uint(fmaf(a, __uint_as_float(o[c]), ai * v.x));
-                                o[c + 1] = __float_as_uint(fmaf(a, __uint_as_float(o[c + 1]), ai * v.y));
-                                o[c + 2] = __float_as_uint(fmaf(a, __uint_as_float(o[c + 2]), ai * v.z));
-                                o[c + 3] = __float_as_uint(fmaf(a, __uint_as_float(o[c + 3]), ai * v.w));
-                            }
-                        }
-                        store_out32(static_cast<uint8_t *>(p.out) + (row * D + q * 32) * osize, o, p.init_o ? 1.f : a,
-                                    p.out_dtype);
-                    }
+                    for (int c = 0; c < 8; ++c)
+                        put(c, __float_as_uint(f(4 * c)), __float_as_uint(f(4 * c + 1)), __float_as_uint(f(4 * c + 2)),
+                            __float_as_uint(f(4 * c + 3)));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        put((q & 1) * 4 + c, pack2(f(8 * c), f(8 * c + 1), bf), pack2(f(8 * c + 2), f(8 * c + 3), bf),
+                            pack2(f(8 * c + 4), f(8 * c + 5), bf), pack2(f(8 * c + 6), f(8 * c + 7), bf));
+                    if ((q & 1) == 0) continue;  // two quarters make a row's 128 bytes
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int from = i * 4 + (lane >> 3), chunk = lane & 7;
+                    const long long to = __shfl_sync(0xffffffffu, offset, from);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(stage + from * 32 + ((chunk ^ (from & 7)) << 2));
+                    if (to >= 0)
+                        *reinterpret_cast<uint4 *>(base + to + (wide ? q : q >> 1) * 128 + chunk * 16) = v;
                 }
                 __syncwarp();
             }
@@ -552,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool BF16>
-int launch_tiles_d(const PagedLaunch &a, PagedParams p, int grid, cudaStream_t stream) {
+int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
+    PagedParams p = a.p;
     using L = TilesLayout<D>;
     static_assert(L::kSmemBytes <= 227 * 1024, "shared memory budget");
     const int tile_tokens = kM / p.G;
@@ -565,7 +570,7 @@ int launch_tiles_d(const PagedLaunch &a, PagedParams p, int grid, cudaStream_t s
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * p.Hq};
     const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tile_tokens};
     const cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(&mq, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(a.q),
+    if (enc(&mq, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t *>(p.q),
             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cuda_fail(cudaErrorInvalidValue);
@@ -573,24 +578,22 @@ int launch_tiles_d(const PagedLaunch &a, PagedParams p, int grid, cudaStream_t s
     if ((rc = make_page_map(&mv, a.c.v_pages, a.c, kKeys)) != FA_OK) return rc;
     // scale == 0 runs as 2^-100: every weight is then exactly 1 as well, and masked
     // scores (+-inf) never meet a zero multiplier
-    const float scale = a.scale == 0.f ? 0x1p-100f : a.scale;
-    p.scale_log2 = scale * kLog2e;
+    if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-100f;
     const auto kernel = paged_tiles_kernel<D, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, a.device, ready)) != FA_OK) return rc;
-    PagedConfig cfg(grid, kThreads, L::kSmemBytes, a.init_o != nullptr, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, tile_tokens, scale < 0.f ? 1 : 0);
+    PagedConfig cfg(a.grid, kThreads, L::kSmemBytes, a.early, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, tile_tokens, p.scale_log2 < 0.f ? 1 : 0);
     if (e != cudaSuccess) return cuda_fail(e);
-    return launch_join<D, 2 * kM>(p, grid, a.units, a.num_sms, stream);
+    return a.join ? launch_join<D, 2 * kM>(a, stream) : FA_OK;
 }
 
 }  // namespace
 
-int launch_paged_tiles(const PagedLaunch &a, const PagedParams &p, int grid, cudaStream_t stream) {
+int launch_paged_tiles(const PagedPass &a, cudaStream_t stream) {
     const bool bf16 = a.c.dtype == FA_BF16;
-    if (a.c.head_dim == 64)
-        return bf16 ? launch_tiles_d<64, true>(a, p, grid, stream) : launch_tiles_d<64, false>(a, p, grid, stream);
-    return bf16 ? launch_tiles_d<128, true>(a, p, grid, stream) : launch_tiles_d<128, false>(a, p, grid, stream);
+    if (a.c.head_dim == 64) return bf16 ? launch_tiles_d<64, true>(a, stream) : launch_tiles_d<64, false>(a, stream);
+    return bf16 ? launch_tiles_d<128, true>(a, stream) : launch_tiles_d<128, false>(a, stream);
 }
 
 int read_tiles_status(int reset) {
