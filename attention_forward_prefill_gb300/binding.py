@@ -598,6 +598,11 @@ def _check_ints(device, name, t, shape):
                          f"[{', '.join('any' if n is None else str(n) for n in shape)}]")
 
 
+def _stride3(t):
+    stride = t.stride()
+    return stride if len(stride) == 3 else (0, 0, 0)
+
+
 def _check_rows(name, t, tokens, heads, k_pages):
     """[tokens, heads, d] rows in the cache's type, of which only the tokens may have a stride; returns
     it and the number of heads."""
@@ -664,11 +669,14 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
     its rows behind the last sequence are not written.
     """
     torch = _torch()
-    cache, Hkv, _ = _pages(k_pages, v_pages)
-    device = k_pages.device
+    cache, Hkv, d = _pages(k_pages, v_pages)
+    device, dtype = k_pages.device, k_pages.dtype
     total = k.shape[0]
-    k_stride, _ = _check_rows("k", k, total, Hkv, k_pages)
-    v_stride, _ = _check_rows("v", v, total, Hkv, k_pages)
+    rows, (k_stride, k_head, k_one), (v_stride, v_head, v_one) = (total, Hkv, d), _stride3(k), _stride3(v)
+    if not (k.shape == rows and v.shape == rows and k.dtype is dtype and v.dtype is dtype and k.device == device and
+            v.device == device and k_one == v_one == 1 and (k_head == v_head == d or Hkv == 1)):
+        _check_rows("k", k, total, Hkv, k_pages)
+        _check_rows("v", v, total, Hkv, k_pages)
     B, max_pages = _tables(device, page_table, seq_lens)
     cu_ptr = pos_ptr = rope_ptr = None
     max_positions = rope_dim = 0
@@ -680,7 +688,7 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
         _check_ints(device, "positions", positions, (total,))
         pos_ptr = positions.data_ptr()
     if rope is not None:
-        if rope.device != device or rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+        if not (rope.dtype is torch.float32 and rope.dim() == 2 and rope.is_contiguous() and rope.device == device):
             raise ValueError("rope must be a contiguous float32 [positions, rope_dim] tensor beside the cache")
         max_positions, rope_dim = rope.shape
         if rope_dim:
@@ -691,7 +699,7 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
         q_stride, Hq = _check_rows("q", q, total, None, k_pages)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            out_stride = out.stride(0)
+            out_stride = Hq * d
         else:
             out_stride, _ = _check_rows("out", out, total, Hq, k_pages)
         q_ptr, out_ptr = q.data_ptr(), out.data_ptr()

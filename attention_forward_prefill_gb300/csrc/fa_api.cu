@@ -145,8 +145,8 @@ int fa_last_cuda_error(void) { return t_last_cuda_error; }
 
 int fa_device_status(int reset) {
     if (cudaDeviceSynchronize() != cudaSuccess) return -1;
-    const int words[6] = {read_prefill_status(reset), read_decode_status(reset), read_backward_status(reset),
-                          read_paged_status(reset), read_tiles_status(reset), read_append_status(reset)};
+    const int words[7] = {read_prefill_status(reset), read_decode_status(reset), read_backward_status(reset),
+                          read_paged_status(reset), read_tiles_status(reset), read_cluster_status(reset), read_append_status(reset)};
     int first = 0;
     for (int v : words) {
         if (v < 0) return -1;

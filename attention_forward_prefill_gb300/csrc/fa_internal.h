@@ -120,10 +120,12 @@ struct PagedLaunch {
 };
 
 size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms);
+bool paged_needs_scratch(const PagedLaunch &a, const DeviceInfo &dev);  // else a.scratch may be null
 int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
 
 // pre: one sequence of own.B query tokens; own: the same tokens, one per sequence.
 size_t paged_pair_scratch_bytes(int B, int Hq, int Hkv, int d, int num_sms);
+bool paged_pair_needs_scratch(const PagedLaunch &pre, const PagedLaunch &own, const DeviceInfo &dev);
 int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scratch, const DeviceInfo &dev,
                       cudaStream_t stream);
 
@@ -146,6 +148,7 @@ int read_decode_status(int reset);
 int read_backward_status(int reset);
 int read_paged_status(int reset);
 int read_tiles_status(int reset);
+int read_cluster_status(int reset);
 int read_append_status(int reset);
 
 }  // namespace fa

@@ -46,6 +46,9 @@ struct PagedParams {
     int causal;             // query token i of nq sees keys j <= len - nq + i
     float scale_log2;       // scale * log2(e)
     int out_dtype;
+    // paged_cluster_kernel alone: keys that every sequence has in front of its own
+    const int *pre_table, *pre_lens;
+    int pre_max_len;
     float *part_o;          // [gridDim.x][2][RB][D], RB >= block_rows the kernel's slot size
     float *part_ml;         // [gridDim.x][2][RB][2]: m (log2 units), l
     int4 *open;             // [gridDim.x][2]: the unit a CTA leaves unfinished
@@ -698,6 +701,7 @@ struct PagedPass {
 };
 
 int launch_paged_tiles(const PagedPass &a, cudaStream_t stream);
+int launch_paged_cluster(const PagedPass &a, int size, cudaStream_t stream);
 
 // Launch attributes of the paged kernels; `early`: may start before the kernels
 // ahead of it in the stream have finished (it waits for them where it must).

@@ -132,11 +132,13 @@ struct Scratch {
     bool ours = false;
     cudaStream_t stream;
     explicit Scratch(cudaStream_t s) : stream(s) {}
-    int take(void *given, size_t given_bytes, size_t need) {
+    // used: whether this call writes it (a workspace that is given has to be large enough either way)
+    int take(void *given, size_t given_bytes, size_t need, bool used) {
         if (given) {
             ptr = given;
             return given_bytes < need ? FA_ERR_WORKSPACE : FA_OK;
         }
+        if (!used) return FA_OK;
         const cudaError_t e = scratch_alloc(&ptr, need, stream);
         if (e != cudaSuccess) {
             cuda_fail(e);
@@ -164,7 +166,7 @@ int run_attention(const Attention &a, int causal, void *workspace, size_t worksp
     Scratch s(st);
     // (a workspace is sized for max_seqlen_q, which fewer tokens than that do not change)
     const size_t need = paged_scratch_bytes(a.max_q, a.Hq / a.c->num_heads, a.c->head_dim, dev.num_sms);
-    if ((rc = s.take(workspace, workspace_bytes, need)) != FA_OK) return rc;
+    if ((rc = s.take(workspace, workspace_bytes, need, paged_needs_scratch(l, dev))) != FA_OK) return rc;
     l.scratch = s.ptr;
     return s.done(launch_paged(l, dev, st));
 }
@@ -325,8 +327,9 @@ int fa_decode_shared(const fa_paged_cache *cache, const void *q, void *out, cons
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Scratch s(st);
     const size_t need = paged_pair_scratch_bytes(B, Hq, cache->num_heads, cache->head_dim, dev.num_sms);
-    if ((rc = s.take(workspace, workspace_bytes, need)) != FA_OK) return rc;
-    return s.done(launch_paged_pair(launch_of(pre, 0), launch_of(own, 0), s.ptr, dev, st));
+    const PagedLaunch first = launch_of(pre, 0), second = launch_of(own, 0);
+    if ((rc = s.take(workspace, workspace_bytes, need, paged_pair_needs_scratch(first, second, dev))) != FA_OK) return rc;
+    return s.done(launch_paged_pair(first, second, s.ptr, dev, st));
 }
 
 }  // extern "C"

@@ -19,35 +19,26 @@
 // over tiles waits for another consumer.
 #include <algorithm>
 
-#include "fa_paged.cuh"
+#include "fa_paged_rows.cuh"
 
 namespace fa {
 
 namespace {
 
-constexpr int kConsumers = 4;
-constexpr int kPagedThreads = 32 * (kConsumers + 1);
-constexpr int kTile = 64;             // keys per stage
-constexpr float kTau = 8.0f;          // lazy-rescale threshold, log2 units
-constexpr int kJoinCols = 32;         // columns per pass of the join between key groups
-
 __device__ int g_paged_status = 0;
 
 template <int D, int RT>
 struct PagedLayout {
+    using R = PagedRows<D, RT, false>;  // (sizes are the same for both types)
     static constexpr int kRows = 16 * RT;
-    static constexpr int kGroups = kConsumers / RT;   // key groups
-    static constexpr int kSlab = kTile * 128;         // 64 keys x 64 columns
-    static constexpr int kOperand = (D / 64) * kSlab;  // a K or V tile
-    static constexpr int kStage = 2 * kOperand;
+    static constexpr int kStage = 2 * R::kOperand;
     static constexpr int kStages = 98304 / kStage;    // 96 KB in flight per CTA, two CTAs per SM
     // Query rows 16 bytes apart in banks where there is room, so that the fragment
     // loads do not conflict (32 or 64 rows of 256 bytes leave none; it is once per unit).
     static constexpr int kQPitch = D * 2 + (RT == 1 ? 16 : 0);
     static constexpr int kQOff = kStages * kStage;
     static constexpr int kJoinOff = kQOff + kRows * kQPitch;
-    static constexpr int kJoinBytes = kGroups > 1 ? kConsumers * 16 * (kJoinCols * 4 + 8) : 0;
-    static constexpr int kBarOff = kJoinOff + kJoinBytes;
+    static constexpr int kBarOff = kJoinOff + R::kJoinBytes;
     static constexpr int kNumBars = 2 * kStages + 2 + 2 * RT;  // full, empty, unit full, unit empty, join full, join empty
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kPieceOff = kMiscOff + 8;
@@ -63,11 +54,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                       const PagedParams p) {
     using L = PagedLayout<D, RT>;
     constexpr int RB = L::kRows;
-    constexpr int KG = L::kGroups;
-    constexpr int NK = kTile / KG;  // keys of a tile per warp
-    // fp16 weights keep 7 bits of headroom below the largest (2^kTau), which
-    // pushes the smallest ones that do not vanish down to 2^-31 of the reference
-    constexpr float kShift = BF16 ? 0.f : 7.f;
+    using R = PagedRows<D, RT, BF16>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
     uint64_t *empty = full + L::kStages;
@@ -89,8 +76,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         mbar_init(u_full, 1);
         mbar_init(u_empty, kConsumers);
         for (int t = 0; t < RT; ++t) {
-            mbar_init(j_full + t, KG);
-            mbar_init(j_empty + t, KG);
+            mbar_init(j_full + t, R::KG);
+            mbar_init(j_empty + t, R::KG);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -159,7 +146,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                         atomicCAS(&g_paged_status, 0, static_cast<int>(FA_ERR_PAGE));
                         id = p.num_pages;  // outside the tensor: the copy writes zeros
                     }
-                    tma_load_4d(smem + st * L::kStage + my_op * L::kOperand + my_slab * L::kSlab + my_box * box * 128,
+                    tma_load_4d(smem + st * L::kStage + my_op * R::kOperand + my_slab * R::kSlab + my_box * box * 128,
                                 my_op ? &map_v : &map_k, full + st, my_slab * 64, key & (page - 1), u.hk, id, pol);
                 }
                 id = next;
@@ -169,238 +156,40 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ consumers
-        const int rw = warp % RT, kw = warp / RT;  // row tile, key group
-        const int quad = lane & 3, qrow = lane >> 2;
-        const uint32_t q_addr = smem_u32(smem + L::kQOff) +
-                                (rw * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * L::kQPitch + (lane >> 4) * 16;
+        R rows(warp, lane);
         const uint32_t ring = smem_u32(smem);
-        // K fragments: lane = key row lane % 8 of an 8-key block, 16-byte chunk lane / 8 of four
-        const uint32_t k_row = (lane & 7) * 128;
-        // V fragments (transposed): lane = key row of a 16-key block, chunk lane / 16 of two
-        const uint32_t v_row = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128;
-        float *join = reinterpret_cast<float *>(smem + L::kJoinOff);
-        float2 *join_ml = reinterpret_cast<float2 *>(smem + L::kJoinOff + kConsumers * 16 * kJoinCols * 4);
-        uint32_t joins = 0;
         bool ok = true;
         while (ok) {
             if (!lanes_wait(u_full, units & 1, abort_flag)) { ok = false; break; }
             ++units;
             const PagedPiece u = *piece;
             if (u.kind < 0) break;
-            uint32_t qf[D / 16][4];
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) ldmatrix4(q_addr + kk * 32, qf[kk]);
+            rows.begin(smem_u32(smem + L::kQOff), L::kQPitch);
             __syncwarp();
             if (lane == 0) mbar_arrive(u_empty);
-            // the last key each of this thread's two rows sees
-            const int r0 = rw * 16 + qrow;
+            // the last key that each of this thread's two rows sees
             int lim0 = u.len - 1, lim1 = u.len - 1;
             if (p.causal) {
-                lim0 = min(lim0, u.len - u.nq + (u.row0 + r0) / p.G);
-                lim1 = min(lim1, u.len - u.nq + (u.row0 + r0 + 8) / p.G);
+                const int r0 = u.row0 + rows.rw * 16 + rows.qrow;
+                lim0 = min(lim0, u.len - u.nq + r0 / p.G);
+                lim1 = min(lim1, u.len - u.nq + (r0 + 8) / p.G);
             }
-            float o[D / 8][4];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-            // kShift - m once a key has been seen; before, masked scores (-inf) still give weight 0
-            float n0 = 0.f, n1 = 0.f;
-
             for (int j = u.j0; j < u.j1; ++j) {
                 const int st = tiles % L::kStages;
                 if (!lanes_wait(full + st, (tiles / L::kStages) & 1, abort_flag)) { ok = false; break; }
                 ++tiles;
-                const uint32_t kt = ring + st * L::kStage + kw * NK * 128;
-                const uint32_t vt = kt + L::kOperand;
-                const int key0 = j * kTile + kw * NK;  // this warp's first key
-                // ---- S = Q K^T
-                float s[NK / 8][4];
-#pragma unroll
-                for (int nb = 0; nb < NK / 8; ++nb) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nb][e] = 0.f;
-#pragma unroll
-                    for (int k2 = 0; k2 < D / 32; ++k2) {
-                        uint32_t kb[4];
-                        const int chunk = (k2 & 1) * 4 + (lane >> 3);
-                        ldmatrix4(kt + (k2 >> 1) * L::kSlab + nb * 1024 + k_row + ((chunk ^ (lane & 7)) << 4), kb);
-                        mma_16816<BF16>(s[nb], qf[2 * k2], kb[0], kb[1]);
-                        mma_16816<BF16>(s[nb], qf[2 * k2 + 1], kb[2], kb[3]);
-                    }
-                }
-                // ---- scores in log2 units, masked; the tile's row maxima
-                const bool tail = min(lim0, lim1) < key0 + NK - 1;
-                float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-                for (int nb = 0; nb < NK / 8; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = key0 + nb * 8 + quad * 2 + e;
-                        s[nb][e] *= p.scale_log2;
-                        s[nb][2 + e] *= p.scale_log2;
-                        if (tail) {
-                            if (key > lim0) s[nb][e] = -INFINITY;
-                            if (key > lim1) s[nb][2 + e] = -INFINITY;
-                        }
-                        x0 = fmaxf(x0, s[nb][e]);
-                        x1 = fmaxf(x1, s[nb][2 + e]);
-                    }
-                __syncwarp();
-#pragma unroll
-                for (int off = 1; off < 4; off <<= 1) {
-                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-                }
-                const bool up0 = x0 > m0 + kTau, up1 = x1 > m1 + kTau;
-                if (__any_sync(0xffffffffu, up0 || up1)) {
-                    float a0 = 1.f, a1 = 1.f;
-                    if (up0) { a0 = ex2_approx(m0 - x0); m0 = x0; n0 = kShift - x0; }
-                    if (up1) { a1 = ex2_approx(m1 - x1); m1 = x1; n1 = kShift - x1; }
-                    l0 *= a0;
-                    l1 *= a1;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        o[i][0] *= a0;
-                        o[i][1] *= a0;
-                        o[i][2] *= a1;
-                        o[i][3] *= a1;
-                    }
-                }
-                // ---- weights 2^(s - m), rounded to the 16-bit type of V; l adds the rounded ones,
-                // so a row that one key dominates returns that key's value row
-                uint32_t pf[NK / 16][4];
-#pragma unroll
-                for (int nb = 0; nb < NK / 8; ++nb) {
-                    const uint32_t lo = pack2t<BF16>(ex2_approx(s[nb][0] + n0), ex2_approx(s[nb][1] + n0));
-                    const uint32_t hi = pack2t<BF16>(ex2_approx(s[nb][2] + n1), ex2_approx(s[nb][3] + n1));
-                    float e0 = 0.f, e1 = 0.f;
-                    add_pair16<BF16>(l0, e0, lo);
-                    add_pair16<BF16>(l1, e1, hi);
-                    l0 += e0;
-                    l1 += e1;
-                    pf[nb >> 1][(nb & 1) * 2] = lo;
-                    pf[nb >> 1][(nb & 1) * 2 + 1] = hi;
-                }
-                // ---- O += P V.  Slots behind the last key hold anything at all, so
-                // their V rows are read as zero (0 x NaN would be NaN).
-                const int valid = u.len - key0;  // keys of this warp that exist
-#pragma unroll
-                for (int kb = 0; kb < NK / 16; ++kb) {
-                    uint32_t mask0 = 0xffffffffu, mask1 = 0xffffffffu;
-                    if (valid < NK) {
-                        const int a = kb * 16 + quad * 2;
-                        mask0 = (a < valid ? 0xffffu : 0u) | (a + 1 < valid ? 0xffff0000u : 0u);
-                        mask1 = (a + 8 < valid ? 0xffffu : 0u) | (a + 9 < valid ? 0xffff0000u : 0u);
-                    }
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t vb[4];
-                        const int chunk = (c & 3) * 2 + (lane >> 4);
-                        ldmatrix4_trans(vt + (c >> 2) * L::kSlab + kb * 2048 + v_row + ((chunk ^ (lane & 7)) << 4), vb);
-                        mma_16816<BF16>(o[2 * c], pf[kb], vb[0] & mask0, vb[1] & mask1);
-                        mma_16816<BF16>(o[2 * c + 1], pf[kb], vb[2] & mask0, vb[3] & mask1);
-                    }
-                }
+                rows.tile(ring + st * L::kStage, lim0 - j * kTile, lim1 - j * kTile, u.len - j * kTile, p.scale_log2);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + st);
             }
             if (!ok) break;
-            // ---- the unit's rows
-#pragma unroll
-            for (int off = 1; off < 4; off <<= 1) {
-                l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-                l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-            }
-            m0 -= kShift;  // (-inf stays)
-            m1 -= kShift;
-            const int rows = min(RB, u.nq * p.G - u.row0);
-            if constexpr (KG == 1) {
-                auto write = [&](int r, float m, float l, auto half) {
-                    constexpr int H = decltype(half)::value;
-                    if (r >= rows) return;
-                    const long long row = paged_row(p, u, r);
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        float a[2] = {o[i][2 * H], o[i][2 * H + 1]};
-                        paged_emit<D, RB, 2>(p, u, r, row, i * 8 + quad * 2, a, m, l);
-                    }
-                };
-                write(r0, m0, l0, std::integral_constant<int, 0>{});
-                write(r0 + 8, m1, l1, std::integral_constant<int, 1>{});
-            } else {
-                // join the KG key groups of row tile rw through shared memory: as many columns per
-                // pass as the unit's rows leave room for
-                float *buf = join + rw * KG * 16 * kJoinCols;
-                float2 *buf_ml = join_ml + rw * KG * 16;
-                auto passes = [&](auto used) {
-                    constexpr int RU = decltype(used)::value;    // rows that exist, rounded up
-                    constexpr int C = kJoinCols * 16 / RU < D ? kJoinCols * 16 / RU : D;  // columns per pass
-                    constexpr int kCells = RU * C / 4, kPer = (kCells + KG * 32 - 1) / (KG * 32);
-                    const int cell = kw * 32 + lane;
-                    auto cell_row = [&](int i) { return (cell + i * KG * 32) / (C / 4); };
-                    const int cell_col = cell % (C / 4) * 4;
-                    // 16-byte chunks of a row change places by row, against bank conflicts
-                    auto at = [&](int g, int r, int col) {
-                        return buf + (g * RU + r) * C + (((col >> 2) ^ (r & 7)) << 2) + (col & 3);
-                    };
-                    long long row[kPer];
-                    bool live[kPer];
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        live[i] = cell + i * KG * 32 < kCells && rw * 16 + cell_row(i) < rows;
-                        row[i] = paged_row(p, u, rw * 16 + cell_row(i));
-                    }
-#pragma unroll
-                    for (int pass = 0; pass < D / C; ++pass) {
-                        if (joins > 0 && !lanes_wait(j_empty + rw, (joins - 1) & 1, abort_flag)) { ok = false; return; }
-#pragma unroll
-                        for (int i = 0; i < C / 8; ++i) {
-                            const int nb = pass * (C / 8) + i, col = i * 8 + quad * 2;
-                            if (RU >= 8 || qrow < RU)
-                                *reinterpret_cast<float2 *>(at(kw, qrow, col)) = make_float2(o[nb][0], o[nb][1]);
-                            if constexpr (RU == 16)
-                                *reinterpret_cast<float2 *>(at(kw, qrow + 8, col)) = make_float2(o[nb][2], o[nb][3]);
-                        }
-                        if (pass == 0 && quad == 0) {
-                            buf_ml[kw * 16 + qrow] = make_float2(m0, l0);
-                            buf_ml[kw * 16 + qrow + 8] = make_float2(m1, l1);
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(j_full + rw);
-                        if (!lanes_wait(j_full + rw, joins & 1, abort_flag)) { ok = false; return; }
-                        ++joins;
-#pragma unroll
-                        for (int i = 0; i < kPer; ++i) {
-                            if (!live[i]) continue;
-                            const int r = cell_row(i);
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                            float M = -INFINITY, Ls = 0.f;
-#pragma unroll
-                            for (int g = 0; g < KG; ++g) M = fmaxf(M, buf_ml[g * 16 + r].x);
-#pragma unroll
-                            for (int g = 0; g < KG; ++g) {
-                                const float4 v = *reinterpret_cast<const float4 *>(at(g, r, cell_col));
-                                const float2 ml = buf_ml[g * 16 + r];
-                                const float w = ex2_from(ml.x, M);
-                                Ls = fmaf(w, ml.y, Ls);
-                                acc[0] = fmaf(w, v.x, acc[0]);
-                                acc[1] = fmaf(w, v.y, acc[1]);
-                                acc[2] = fmaf(w, v.z, acc[2]);
-                                acc[3] = fmaf(w, v.w, acc[3]);
-                            }
-                            paged_emit<D, RB, 4>(p, u, rw * 16 + r, row[i], pass * C + cell_col, acc, M, Ls);
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(j_empty + rw);
-                    }
-                };
-                const int used = rows - rw * 16;
-                if (RT == 1 && used <= 8) passes(std::integral_constant<int, 8>{});
-                else passes(std::integral_constant<int, 16>{});
-                if (!ok) break;
-            }
+            rows.end();
+            ok = rows.write(
+                min(RB, u.nq * p.G - u.row0), smem + L::kJoinOff, j_full, j_empty, abort_flag,
+                [&](int r) { return paged_row(p, u, r); },
+                [&](int r, long long row, int col, auto &acc, float m, float l) {
+                    paged_emit<D, RB>(p, u, r, row, col, acc, m, l);
+                });
         }
         __syncwarp();
     }
@@ -467,6 +256,20 @@ int step_ns(const PagedPlan &pl, int d) {
     return d == 128 ? ns : ns * 5 / 6;
 }
 
+// CTAs per cluster for calls that paged_cluster_kernel serves best, or 0.  Against the
+// split form it saves a kernel and a scratch allocation (about 3 us) and loses where its
+// eight CTAs per unit get more tiles each than an even share of the whole GPU would be
+// (0.5 to 0.7 us a tile).  The sizes are bounds: lengths are known on the device only.
+int cluster_size(const PagedPass &x, long long prefix_max) {
+    if (x.plan.tiles) return 0;
+    const long long tiles = (x.p.max_len + kTile - 1) / kTile + (prefix_max + kTile - 1) / kTile;
+    const long long all = 2LL * x.num_sms;  // CTAs at a time
+    int size = 8;
+    while (size > 1 && (size / 2 >= tiles || x.units * size > all)) size /= 2;
+    if (x.units * size > all) return 0;
+    return (tiles + size - 1) / size - x.units * tiles / all <= (prefix_max ? 6 : 4) ? size : 0;
+}
+
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Partial rows, (m, l) and notes of one pass with the largest grid.
@@ -527,8 +330,18 @@ size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms) {
     return pass_bytes(plan_paged(max_q, group), d, num_sms);
 }
 
+bool paged_needs_scratch(const PagedLaunch &a, const DeviceInfo &dev) {
+    return cluster_size(make_pass(a, dev, nullptr), 0) == 0;
+}
+
 int launch_paged(const PagedLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
-    return launch_pass(make_pass(a, dev, a.scratch), stream);
+    const PagedPass x = make_pass(a, dev, a.scratch);
+    const int size = cluster_size(x, 0);
+    return size ? launch_paged_cluster(x, size, stream) : launch_pass(x, stream);
+}
+
+bool paged_pair_needs_scratch(const PagedLaunch &pre, const PagedLaunch &own, const DeviceInfo &dev) {
+    return cluster_size(make_pass(own, dev, nullptr), 1LL * pre.max_pages * pre.c.page_size) == 0;
 }
 
 size_t paged_pair_scratch_bytes(int B, int Hq, int Hkv, int d, int num_sms) {
@@ -548,6 +361,11 @@ size_t paged_pair_scratch_bytes(int B, int Hq, int Hkv, int d, int num_sms) {
 // and neither waits for the other; the join waits for both.
 int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scratch, const DeviceInfo &dev,
                       cudaStream_t stream) {
+    PagedPass one = make_pass(own, dev, nullptr);
+    one.p.pre_table = pre.page_table;
+    one.p.pre_lens = pre.seq_lens;
+    one.p.pre_max_len = pre.max_pages * pre.c.page_size;
+    if (const int size = cluster_size(one, one.p.pre_max_len)) return launch_paged_cluster(one, size, stream);
     const size_t rows = static_cast<size_t>(own.B) * own.Hq;
     const int d = own.c.head_dim;
     char *at = static_cast<char *>(scratch);
