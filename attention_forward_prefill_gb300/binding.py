@@ -121,6 +121,21 @@ def load(build_if_missing: bool = False):
     return _lib
 
 
+_calls = None
+
+
+def _fast():
+    """The module _paged_calls over the loaded library."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        from . import _paged_calls
+        _paged_calls.init(_torch(), FaError, *(ctypes.cast(getattr(lib, n), _vp).value for n in (
+            "fa_cache_append", "fa_decode_paged", "fa_prefill_paged", "fa_decode_shared")))
+        _calls = _paged_calls
+    return _calls
+
+
 # ---------------------------------------------------------------- raw C ABI
 def fa_prefill(q, k, v, out, B, H, N, d, causal, scale, stream=0) -> int:
     return load().fa_prefill(q, k, v, out, B, H, N, d, int(causal), float(scale), stream)
@@ -549,8 +564,9 @@ def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cud
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
-# A call of a few microseconds on the GPU is bound by what happens here on the host, so the calls
-# below test what they need in one expression and look for the reason only when it is false.
+# A call of a few microseconds on the GPU is bound by what happens on the host, so arguments go to
+# _paged_calls first, which makes the call where they are what a call mostly gets and returns
+# NotImplemented otherwise; the checks here then say what is wrong, or make the call.
 _PACK_CACHE = struct.Struct("@PPqqqiiiii4x").pack  # fa_paged_cache, its tail padding with it
 _codes = {}
 
@@ -668,6 +684,10 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens=Non
     [T]: the rotary positions where they are not the positions in the sequence.  out may be q;
     its rows behind the last sequence are not written.
     """
+    done = (_calls or _fast()).append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, rope, interleaved,
+                                      positions, out)
+    if done is not NotImplemented:
+        return done
     torch = _torch()
     cache, Hkv, d = _pages(k_pages, v_pages)
     device, dtype = k_pages.device, k_pages.dtype
@@ -750,6 +770,10 @@ def decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale: float | None 
     q [B, Hq, d] or [B, Hq, 1, d]; k_pages, v_pages [pages, Hkv, slots, d], any strides;
     page_table int32 [B, max_pages]; seq_lens int32 [B].  Returns rows shaped as q.
     """
+    if out_dtype is None and workspace is None:
+        done = (_calls or _fast()).decode(q, k_pages, v_pages, page_table, seq_lens, scale, out)
+        if done is not NotImplemented:
+            return done
     cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
                                                                    out_dtype, out)
     ws, ws_bytes = _workspace(workspace, device)
@@ -768,6 +792,11 @@ def prefill_paged(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_s
     lse: optional fp32 [T, Hq] that receives the row log-sum-exp.  Returns [T, Hq, d]; rows
     outside every sequence are not written.
     """
+    if out_dtype is None and workspace is None and lse is None:
+        done = (_calls or _fast()).prefill(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal,
+                                           scale, out)
+        if done is not NotImplemented:
+            return done
     cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
                                                                    out_dtype, out)
     if q.dim() != 3 or q.shape[2] != d:
@@ -795,6 +824,10 @@ def decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq
     (int32 [1], on the device) of prefix_table's pages (int32 [n]), then its own.  The prefix is
     read once for the whole batch.
     """
+    if out_dtype is None and workspace is None:
+        done = (_calls or _fast()).shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale, out)
+        if done is not NotImplemented:
+            return done
     cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
                                                                    out_dtype, out)
     int32 = _torch().int32

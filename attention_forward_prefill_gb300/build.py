@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +21,9 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["fa_api.cu", "fa_prefill_sm103.cu", "fa_decode_sm103.cu", "fa_backward_sm103.cu",
            "fa_paged_api.cu", "fa_paged_sm103.cu", "fa_paged_tiles_sm103.cu",
            "fa_paged_cluster_sm103.cu", "fa_cache_sm103.cu"]
+# The CPython module in front of the paged-cache calls (host code only).
+CALLS_SOURCE = "paged_calls.c"
+CALLS_PATH = os.path.join(HERE, "_paged_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-Xcompiler", "-Wall"]
@@ -39,10 +43,26 @@ def _inputs_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_calls(verbose: bool) -> None:
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("a C compiler is required to build _paged_calls")
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+                        os.path.join(CSRC, CALLS_SOURCE), "-o", tmp, "-lm"], capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on {CALLS_SOURCE}")
+    os.replace(tmp, CALLS_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the path of libfa_gb300.so."""
-    if (not force and os.path.exists(LIB_PATH)
-            and os.path.getmtime(LIB_PATH) >= _inputs_mtime()):
+    newest = _inputs_mtime()
+    if force or not os.path.exists(CALLS_PATH) or os.path.getmtime(CALLS_PATH) < newest:
+        _build_calls(verbose)
+    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= newest:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
