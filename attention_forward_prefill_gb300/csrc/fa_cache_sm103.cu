@@ -79,6 +79,8 @@ template <int D, bool BF16, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams p) {
     constexpr int LPH = D / 16;      // lanes per head
     constexpr int HPW = 32 / LPH;    // heads per warp and step
+    // launched while the kernels ahead of it still run; nothing in global memory before they are done
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarps + warp;
     if (t >= p.total) return;
@@ -191,9 +193,17 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
 }
 
 template <int D, bool BF16>
-void launch_append_d(const AppendParams &p, dim3 grid, bool inter, cudaStream_t stream) {
-    if (inter) append_kernel<D, BF16, true><<<grid, kWarps * 32, 0, stream>>>(p);
-    else append_kernel<D, BF16, false><<<grid, kWarps * 32, 0, stream>>>(p);
+cudaError_t launch_append_d(const AppendParams &p, dim3 grid, bool inter, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, inter ? append_kernel<D, BF16, true> : append_kernel<D, BF16, false>, p);
 }
 
 }  // namespace
@@ -237,11 +247,10 @@ int launch_append(const AppendLaunch &a, const DeviceInfo &dev, cudaStream_t str
     p.heads_each = ((heads + slices - 1) / slices + step - 1) / step * step;
     const dim3 grid((a.total + kWarps - 1) / kWarps, (heads + p.heads_each - 1) / p.heads_each);
     const bool bf16 = a.c.dtype == FA_BF16, inter = a.interleaved != 0;
-    if (a.c.head_dim == 64) bf16 ? launch_append_d<64, true>(p, grid, inter, stream) : launch_append_d<64, false>(p, grid, inter, stream);
-    else bf16 ? launch_append_d<128, true>(p, grid, inter, stream) : launch_append_d<128, false>(p, grid, inter, stream);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e);
-    return FA_OK;
+    const auto launch = a.c.head_dim == 64 ? (bf16 ? launch_append_d<64, true> : launch_append_d<64, false>)
+                                           : (bf16 ? launch_append_d<128, true> : launch_append_d<128, false>);
+    const cudaError_t e = launch(p, grid, inter, stream);
+    return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
 int read_append_status(int reset) {

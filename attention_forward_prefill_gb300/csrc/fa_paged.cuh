@@ -129,6 +129,17 @@ __device__ __forceinline__ long long paged_head_steps(const PagedParams &p, cons
     return sum;
 }
 
+// Every paged kernel may be launched while the kernels ahead of it in the stream
+// still run; it sets itself up and touches nothing in global memory before they
+// are done.  What follows it is let go only after that, so whatever is launched
+// early behind it may read what was complete before it.  The second of two passes
+// over the same rows is the exception: it reads nothing that the first one writes,
+// and the first one has been through here.
+__device__ __forceinline__ void paged_enter(const PagedParams &p) {
+    if (!p.peer_lens || p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Where a CTA's range of steps starts.
 struct PagedStart {
     long long W;    // steps of the call
@@ -697,18 +708,18 @@ struct PagedPass {
     int grid, blocks;  // CTAs; row blocks of the longest sequence, per kv head
     long long units;   // no more units than this exist
     int device, num_sms;
-    bool early, join;  // early: may start before the kernels ahead of it have finished
+    bool join;
 };
 
 int launch_paged_tiles(const PagedPass &a, cudaStream_t stream);
 int launch_paged_cluster(const PagedPass &a, int size, cudaStream_t stream);
 
-// Launch attributes of the paged kernels; `early`: may start before the kernels
-// ahead of it in the stream have finished (it waits for them where it must).
+// Launch attributes of the paged kernels: each may start before the kernels ahead of
+// it in the stream have finished (see paged_enter).
 struct PagedConfig {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute attr[1];
-    PagedConfig(dim3 grid, int threads, size_t smem, bool early, cudaStream_t stream) {
+    PagedConfig(dim3 grid, int threads, size_t smem, cudaStream_t stream) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         c.gridDim = grid;
@@ -716,7 +727,7 @@ struct PagedConfig {
         c.dynamicSmemBytes = smem;
         c.stream = stream;
         c.attrs = attr;
-        c.numAttrs = early ? 1 : 0;
+        c.numAttrs = 1;
     }
     PagedConfig(const PagedConfig &) = delete;
 };
@@ -741,7 +752,7 @@ int launch_join(const PagedPass &a, cudaStream_t stream) {
     if (a.grid > kJoinMax) return cuda_fail(cudaErrorInvalidConfiguration);
     const long long rows = std::min<long long>(a.grid, a.units) * std::min<long long>(a.p.block_rows, 1LL * a.p.max_q * a.p.G);
     const int grid = static_cast<int>(std::min<long long>(2LL * a.num_sms, rows));
-    PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
+    PagedConfig cfg(grid, kJoinThreads, 0, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, a.p, a.grid);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }

@@ -84,6 +84,20 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, kConsumers);
+        }
+        mbar_init(q_full, 1);
+        for (int t = 0; t < RT; ++t) {
+            mbar_init(j_full + t, R::KG);
+            mbar_init(j_empty + t, R::KG);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    paged_enter(p);
     const SeqView s = paged_seq(p, u.b);
     u.t0 = s.t0;
     u.nq = s.nq;
@@ -101,19 +115,6 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     if (p.causal) seen = max(0, u.len - u.nq + min(u.nq - 1, (u.row0 + RB - 1) / p.G) + 1);
     const int tiles = pre_tiles + (seen + kTile - 1) / kTile;
     const int j0 = rank * tiles / size, j1 = (rank + 1) * tiles / size;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < L::kStages; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, kConsumers);
-        }
-        mbar_init(q_full, 1);
-        for (int t = 0; t < RT; ++t) {
-            mbar_init(j_full + t, R::KG);
-            mbar_init(j_empty + t, R::KG);
-        }
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
     __syncthreads();
     float2 *out_ml = reinterpret_cast<float2 *>(smem + L::kOutMlOff);
     uint32_t issued = 0;
@@ -254,17 +255,19 @@ int launch_cluster(const PagedPass &a, int size, cudaStream_t stream) {
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, a.device, ready)) != FA_OK) return rc;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(a.units) * size);
     cfg.blockDim = dim3(kPagedThreads);
     cfg.dynamicSmemBytes = L::kSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, a.p, a.blocks, size);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }

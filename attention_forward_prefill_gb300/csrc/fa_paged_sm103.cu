@@ -67,7 +67,6 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     long long *warp_sum = reinterpret_cast<long long *>(smem + L::kSumOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(full + s, 1);
@@ -86,6 +85,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
+    paged_enter(p);
     paged_plan<kTile, kPagedThreads>(p, *start, warp_sum, &g_paged_status);
     uint32_t units = 0, tiles = 0;  // handed over / taken so far
 
@@ -225,7 +225,7 @@ int launch_rows(const PagedPass &a, cudaStream_t stream) {
     const auto kernel = paged_rows_kernel<D, RT, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, a.device, ready)) != FA_OK) return rc;
-    PagedConfig cfg(a.grid, kPagedThreads, L::kSmemBytes, a.early, stream);
+    PagedConfig cfg(a.grid, kPagedThreads, L::kSmemBytes, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mk, mv, a.p);
     if (e != cudaSuccess) return cuda_fail(e);
     return a.join ? launch_join<D, L::kRows>(a, stream) : FA_OK;
@@ -283,7 +283,6 @@ PagedPass make_pass(const PagedLaunch &a, const DeviceInfo &dev, void *scratch) 
     x.c = a.c;
     x.device = dev.device;
     x.num_sms = dev.num_sms;
-    x.early = false;
     x.join = true;
     PagedParams &p = x.p;
     p = PagedParams{};
@@ -380,7 +379,6 @@ int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scra
         x.p.unit_note = reinterpret_cast<int2 *>(at);
         at += align256(x.units * sizeof(int2));
         x.join = false;
-        x.early = i == 1;
         x.p.first = i == 0;
         x.p.num_sms = dev.num_sms;
         x.p.per_sm = x.plan.per_sm;
@@ -402,7 +400,7 @@ int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scra
         if ((rc = launch_pass(x, stream)) != FA_OK) return rc;
     constexpr long long kWarps = kJoinThreads / 32;
     const int grid = static_cast<int>(std::min<long long>(2LL * dev.num_sms, (static_cast<long long>(rows) + kWarps - 1) / kWarps));
-    PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
+    PagedConfig cfg(grid, kJoinThreads, 0, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, d == 64 ? paged_pair_join_kernel<64> : paged_pair_join_kernel<128>,
                                              pass[0].p, pass[1].p, pass[0].plan.slot_rows, pass[1].plan.slot_rows,
                                              pass[0].blocks, pass[1].blocks);

@@ -105,7 +105,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile_rows = tile_tokens * p.G;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -136,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&map_v);
     }
     tc_fence_before();
+    paged_enter(p);
     paged_plan<kKeys, kThreads>(p, *start, warp_sum, &g_tiles_status);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -582,7 +582,7 @@ int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
     const auto kernel = paged_tiles_kernel<D, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, a.device, ready)) != FA_OK) return rc;
-    PagedConfig cfg(a.grid, kThreads, L::kSmemBytes, a.early, stream);
+    PagedConfig cfg(a.grid, kThreads, L::kSmemBytes, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, tile_tokens, p.scale_log2 < 0.f ? 1 : 0);
     if (e != cudaSuccess) return cuda_fail(e);
     return a.join ? launch_join<D, 2 * kM>(a, stream) : FA_OK;
