@@ -228,6 +228,7 @@ struct PagedPiece {
     int b, t0, nq, len;
     int hk, row0;   // row0: first row of the block among the nq * G rows
     int j0, j1;     // key tiles
+    int end0, end1; // paged_tiles_kernel: the piece's key tiles for its two query tiles are [j0, end0), [j0, end1)
     int kind;       // 0 whole unit, 1 opens a unit that the next CTA continues, 2 continues one, -1 no more work
 };
 

@@ -181,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 u.kind = -1;
             }
             any = true;
+            u.end0 = tile_end(p, u, u.row0, tile_rows);
+            u.end1 = tile_end(p, u, u.row0 + tile_rows, tile_rows);
             const uint32_t slot = pieces & 1;
             if (pieces >= 2 && !lanes_wait(u_empty + slot, ((pieces >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
             if (lane == 0) {
@@ -189,9 +191,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++pieces;
             if (!more) break;
+            // ---- groups {K_j0}, {V_j, K_j+1} ...: group i holds V_(j0 + i - 1) and K_(j0 + i)
+            const int *table = p.page_table + static_cast<long long>(u.b) * p.max_pages;
+            const int steps = u.j1 - u.j0;
+            auto key_of = [&](int i) { return (u.j0 + i - (my_half == 0 ? 1 : 0)) * kKeys + my_box * box; };
+            auto mine = [&](int i) {
+                return my_half < 2 && (my_half == 0 ? i > 0 : i < steps) && key_of(i) < u.len;
+            };
+            auto page_of = [&](int i) { return mine(i) ? __ldg(table + (key_of(i) >> p.page_shift)) : -1; };
+            int id = page_of(0);  // (on its way while the query tiles become free)
             // ---- query tiles with key tiles in this piece
-            const bool need0 = tile_end(p, u, u.row0, tile_rows) > u.j0;
-            const bool need1 = tile_end(p, u, u.row0 + tile_rows, tile_rows) > u.j0;
+            const bool need0 = u.end0 > u.j0, need1 = u.end1 > u.j0;
             if (qc > 0 && !lanes_wait(q_empty, (qc - 1) & 1, abort_flag)) { ok = false; break; }
             if (lane == 0) {
                 mbar_arrive_expect_tx(q_full, ((need0 ? 1 : 0) + (need1 ? 1 : 0)) * tile_rows * 128 * L::kSlabs);
@@ -204,15 +214,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             ++qc;
-            // ---- groups {K_j0}, {V_j, K_j+1} ...: group i holds V_(j0 + i - 1) and K_(j0 + i)
-            const int *table = p.page_table + static_cast<long long>(u.b) * p.max_pages;
-            const int steps = u.j1 - u.j0;
-            auto key_of = [&](int i) { return (u.j0 + i - (my_half == 0 ? 1 : 0)) * kKeys + my_box * box; };
-            auto mine = [&](int i) {
-                return my_half < 2 && (my_half == 0 ? i > 0 : i < steps) && key_of(i) < u.len;
-            };
-            auto page_of = [&](int i) { return mine(i) ? __ldg(table + (key_of(i) >> p.page_shift)) : -1; };
-            int id = page_of(0);
             for (int i = 0; i <= steps; ++i) {
                 const int next = i < steps ? page_of(i + 1) : -1;
                 const uint32_t st = gc % L::kGroups;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const PagedPiece u = take_piece();
             if (u.kind < 0) break;
             const int j0 = u.j0, j1 = u.j1;
-            const int end[2] = {tile_end(p, u, u.row0, tile_rows), tile_end(p, u, u.row0 + tile_rows, tile_rows)};
+            const int end[2] = {u.end0, u.end1};
             if (lane == 0) {
                 do {
                     if (!mbar_wait(q_full, qc & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u.kind < 0) break;
             const int j0 = u.j0;
             const int row_t = u.row0 + t * tile_rows;
-            const int end = tile_end(p, u, row_t, tile_rows);
+            const int end = t ? u.end1 : u.end0;
             const int rr = row_t + r;  // row among the sequence's nq * G
             const bool row_ok = r < tile_rows && rr < u.nq * p.G;
             const long long row = paged_row(p, u, t * tile_rows + r);
