@@ -401,13 +401,14 @@ __device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiec
 // Joins the pieces of the units that ranges cut: the unit that CTA c of the main
 // kernel left open has its pieces in slot 1 of c and slot 0 of the CTAs after it, up
 // to the one that closed the unit.  They are added in CTA order.
-// All latency.  Every CTA reads all notes at once and numbers the items (two rows
-// of a unit of at most four pieces, or one row of one with more), the warps of the
-// grid take the items in turn, and an item's loads (2 rows x 4 pieces, or 12
-// pieces) are in flight together.  Where the items leave most warps idle, a CTA takes
+// All latency.  Every CTA reads all notes at once and numbers the items (four rows of
+// a unit of two pieces, as most are that hold many rows, two of one of three or four, or
+// one row of one with more), the warps of the grid take the items in turn, and an item's
+// loads (4 rows x 2 pieces, 2 x 4, or 8 pieces) are in flight together.  Where the items leave most warps idle, a CTA takes
 // an item and its warps a share of the pieces each (one long sequence: 300 pieces of
 // 64 rows took 26 us a warp per row).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinPerSm = 2;
 constexpr int kJoinMax = 512;  // CTAs of the main kernel
 
 // The sums of R rows over n pieces, F pieces at a time: ml_at(k, r) and row_at(k, r)
@@ -477,8 +478,46 @@ __device__ __forceinline__ long long paged_noted_row(const PagedParams &p, const
     return (static_cast<long long>(a.y) + rr / p.G) * p.Hq + a.z * p.G + rr % p.G;
 }
 
+// R rows of a unit of at most F pieces, all at once.
+template <int D, int RB, int R, int F>
+__device__ __forceinline__ void paged_join_few(const PagedParams &p, int c, const int4 &a, int r0, int rows, int lane) {
+    constexpr int N = D / 32;
+    using Vec = typename std::conditional<N == 4, float4, float2>::type;
+    const int n = a.x - c + 1;
+    Vec x[R][F];
+    float2 ml[R][F];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < F; ++k) {  // (behind the last piece or row: that one again)
+            const int kk = min(k, n - 1);
+            const size_t rec = (static_cast<size_t>(c + kk) * 2 + (kk == 0 ? 1 : 0)) * RB + min(r0 + r, rows - 1);
+            x[r][k] = reinterpret_cast<const Vec *>(p.part_o + rec * D)[lane];
+            ml[r][k] = *reinterpret_cast<const float2 *>(p.part_ml + rec * 2);
+        }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (r0 + r >= rows) break;
+        float M = -INFINITY, L = 0.f, acc[N] = {};
+#pragma unroll
+        for (int k = 0; k < F; ++k) M = fmaxf(M, ml[r][k].x);
+#pragma unroll
+        for (int k = 0; k < F; ++k) {
+            const float w = k < n ? ex2_from(ml[r][k].x, M) : 0.f;
+            const float *xv = reinterpret_cast<const float *>(&x[r][k]);
+            L = fmaf(w, ml[r][k].y, L);
+#pragma unroll
+            for (int e = 0; e < N; ++e)  // no weight: the row saw no key in this piece, whose columns may be unwritten
+                acc[e] += w > 0.f ? w * xv[e] : 0.f;
+        }
+        paged_finish<N>(p, D, paged_noted_row(p, a, r0 + r), lane * N, acc, M, L);
+    }
+}
+
+__device__ __forceinline__ int join_rows_each(int pieces) { return pieces <= 2 ? 4 : (pieces <= 4 ? 2 : 1); }
+
 template <int D, int RB>
-__global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const PagedParams p, const int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) paged_join_kernel(const PagedParams p, const int ctas) {
     __shared__ int4 note[kJoinMax];
     __shared__ int first[kJoinMax];  // items before CTA c's unit
     __shared__ int rows_of[kJoinMax];
@@ -498,7 +537,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
             if (a.x >= 0) {
                 const int rows = min(p.block_rows, b.x * p.G - a.w);
                 rows_of[c] = rows;
-                items[i] = a.x - c < 4 ? (rows + 1) / 2 : rows;
+                const int per = join_rows_each(a.x - c + 1);
+                items[i] = (rows + per - 1) / per;
             }
         }
         mine += items[i];
@@ -538,11 +578,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
         if (static_cast<int>(blockIdx.x) >= total) return;
         const int c = unit_of(blockIdx.x), i = blockIdx.x - first[c];
         const int4 a = note[c];
-        const int n = a.x - c + 1, rows = rows_of[c], per = n <= 4 ? 2 : 1;
+        const int n = a.x - c + 1, rows = rows_of[c], per = join_rows_each(n);
         for (int r = i * per; r < min(rows, i * per + per); ++r) {
             const int k0 = warp * n / kWarps, k1 = (warp + 1) * n / kWarps;
             float M[1], L[1], acc[1][N];
-            paged_join_rows<D, RB, 1, 12>(p, c, a, r, rows, lane, k0, k1 - k0, M, L, acc);
+            paged_join_rows<D, RB, 1, 8>(p, c, a, r, rows, lane, k0, k1 - k0, M, L, acc);
 #pragma unroll
             for (int e = 0; e < N; ++e) part[warp][lane * N + e] = acc[0][e];
             if (lane == 0) part_ml[warp] = make_float2(M[0], L[0]);
@@ -568,16 +608,14 @@ __global__ void __launch_bounds__(kJoinThreads, 2) paged_join_kernel(const Paged
         const int c = unit_of(item), i = item - first[c];
         const int4 a = note[c];
         const int n = a.x - c + 1, rows = rows_of[c];
-        if (n <= 4) {
-            float M[2], L[2], acc[2][N];
-            paged_join_rows<D, RB, 2, 4>(p, c, a, i * 2, rows, lane, 0, n, M, L, acc);
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (i * 2 + r < rows) paged_finish<N>(p, D, paged_noted_row(p, a, i * 2 + r), lane * N, acc[r], M[r], L[r]);
-        } else {
+        if (n > 4) {
             float M[1], L[1], acc[1][N];
-            paged_join_rows<D, RB, 1, 12>(p, c, a, i, rows, lane, 0, n, M, L, acc);
+            paged_join_rows<D, RB, 1, 8>(p, c, a, i, rows, lane, 0, n, M, L, acc);
             paged_finish<N>(p, D, paged_noted_row(p, a, i), lane * N, acc[0], M[0], L[0]);
+        } else if (n > 2) {
+            paged_join_few<D, RB, 2, 4>(p, c, a, i * 2, rows, lane);
+        } else {
+            paged_join_few<D, RB, 4, 2>(p, c, a, i * 4, rows, lane);
         }
     }
 }
@@ -752,7 +790,7 @@ template <int D, int RB>
 int launch_join(const PagedPass &a, cudaStream_t stream) {
     if (a.grid > kJoinMax) return cuda_fail(cudaErrorInvalidConfiguration);
     const long long rows = std::min<long long>(a.grid, a.units) * std::min<long long>(a.p.block_rows, 1LL * a.p.max_q * a.p.G);
-    const int grid = static_cast<int>(std::min<long long>(2LL * a.num_sms, rows));
+    const int grid = static_cast<int>(std::min<long long>(1LL * kJoinPerSm * a.num_sms, rows));
     PagedConfig cfg(grid, kJoinThreads, 0, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, a.p, a.grid);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
