@@ -604,8 +604,14 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) paged_join_kernel(co
         }
         return;
     }
-    for (int item = blockIdx.x * kWarps + warp; item < total; item += gridDim.x * kWarps) {
-        const int c = unit_of(item), i = item - first[c];
+    // a warp takes neighbouring items: one search, then on from unit to unit
+    const int each = (total + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
+    const int item0 = (blockIdx.x * kWarps + warp) * each, item1 = min(item0 + each, total);
+    if (item0 >= item1) return;
+    int c = unit_of(item0);
+    for (int item = item0; item < item1; ++item) {
+        while (c + 1 < ctas && first[c + 1] <= item) ++c;
+        const int i = item - first[c];
         const int4 a = note[c];
         const int n = a.x - c + 1, rows = rows_of[c];
         if (n > 4) {

@@ -153,6 +153,56 @@ def test_keys_alone():
     assert torch.equal(s.vp.double(), want_v)
 
 
+def test_the_python_path_makes_the_same_calls_and_refuses(monkeypatch):
+    def both():
+        s = Step([3, 0, 2], [3, 9, 40], 4, 2, 64, 16, F16, fused=True, seed=4)
+        return s, s.run(binding.rope_table(64, 48), True)
+
+    one, first = both()
+
+    class Nothing:
+        append = staticmethod(lambda *a: NotImplemented)
+
+    real = binding._calls
+    monkeypatch.setattr(binding, "_calls", Nothing)
+    two, second = both()
+    assert torch.equal(first, second) and torch.equal(one.kp, two.kp) and torch.equal(one.vp, two.vp)
+    for fast in (real, Nothing):
+        monkeypatch.setattr(binding, "_calls", fast)
+        s = Step([3, 0, 2], [3, 9, 40], 4, 2, 64, 16, F16, seed=4)
+        good = dict(q=s.q, k=s.k, v=s.v, kp=s.kp, vp=s.vp, table=s.table, lens=s.seq_lens, cu=s.cu,
+                    rope=binding.rope_table(64, 64), positions=None, out=None)
+
+        def call(a):
+            return binding.cache_append(a["q"], a["k"], a["v"], a["kp"], a["vp"], a["table"], a["lens"], cu_seqlens=a["cu"],
+                                        rope=a["rope"], positions=a["positions"], out=a["out"])
+
+        call(good)
+        for change in (dict(q=s.q.float()), dict(q=s.q[:1]), dict(k=s.k[:1]), dict(v=s.v[:, :1]), dict(k=s.k.cpu()),
+                       dict(k=s.k.transpose(0, 1)), dict(q=s.q[..., :32]), dict(kp=s.kp.bfloat16()), dict(vp=s.vp[:1]),
+                       dict(table=s.table[:1]), dict(lens=s.seq_lens.long()), dict(cu=s.cu[:2]), dict(cu=s.cu.long()),
+                       dict(rope=good["rope"].double()), dict(rope=good["rope"][0]), dict(rope=good["rope"].t()),
+                       dict(positions=s.cu), dict(out=s.q[:1]), dict(out=s.q.float()), dict(q=None, out=s.q)):
+            with pytest.raises(ValueError):
+                call({**good, **change})
+        for change, status in ((dict(rope=binding.rope_table(64, 80)), binding.FA_ERR_SHAPE),
+                               (dict(rope=binding.rope_table(64, 8)), binding.FA_ERR_SHAPE),
+                               (dict(cu=None), binding.FA_ERR_SHAPE), (dict(out=s.q[:, :4].clone()[:, :4]), None)):
+            if status is None:
+                call({**good, **change})
+                continue
+            with pytest.raises(binding.FaError) as e:
+                call({**good, **change})
+            assert e.value.status == status
+
+
+def test_no_tokens():
+    s = Step([0, 0], [3, 0], 4, 2, 64, 16, F16)
+    before = s.kp.clone()
+    out = s.run(binding.rope_table(8, 64), False)
+    assert out.shape == (0, 4, 64) and torch.equal(s.kp, before)
+
+
 def test_slots_past_32_bits():
     Hkv, d, page = 8, 128, 64
     count = (1 << 31) // (Hkv * d * page) + 8

@@ -36,23 +36,27 @@ def check_decode(c, q, out, scale, what):
 LENS = [0, 1, 15, 16, 17, 63, 64, 65, 128, 129, 500, 1031]
 
 
+# A table as wide as the lengths need makes few, short units (clusters); a wide one, with room for
+# sequences that are not there, takes the split form with its join.
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("Hq,Hkv,d,page,dtype,slots_first", [
     (12, 12, 64, 16, F16, False), (14, 2, 64, 16, F16, True), (14, 2, 64, 128, BF16, False),
     (32, 8, 128, 64, BF16, False), (8, 8, 128, 32, F16, True), (64, 8, 128, 256, F16, False),
     (20, 1, 128, 16, BF16, True), (40, 1, 64, 32, BF16, False), (71, 1, 128, 64, F16, True),
-    (6, 2, 128, 1024, BF16, False)])
-def test_decode_heads_pages_and_lengths(Hq, Hkv, d, page, dtype, slots_first):
-    c = Cache(LENS, Hkv, d, page, dtype, slots_first, seed=Hq)
+    (130, 1, 64, 16, BF16, False), (6, 2, 128, 1024, BF16, False)])
+def test_decode_heads_pages_and_lengths(Hq, Hkv, d, page, dtype, slots_first, wide):
+    c = Cache(LENS, Hkv, d, page, dtype, slots_first, seed=Hq, extra_cols=(1 << 17) // page if wide else 2)
     q = queries(len(LENS), Hq, d, dtype)
     out = binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens)
     check_decode(c, q, out, d ** -0.5, "decode")
     assert torch.equal(out, binding.decode_paged(q.unsqueeze(2), c.k, c.v, c.table, c.seq_lens).squeeze(2))
 
 
-@pytest.mark.parametrize("lens", [[1], [64], [4097], [40000, 3], [0, 0, 0], [0, 9000, 0, 1], [1] * 700,
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("lens", [[1], [64], [4097], [40000, 3], [0, 0, 0], [0, 9000, 0, 1], [1] * 700, [3, 70] * 2049,
                                   list(range(0, 400, 3))])
-def test_decode_batches(lens):
-    c = Cache(lens, 2, 128, 64, BF16, seed=len(lens))
+def test_decode_batches(lens, wide):
+    c = Cache(lens, 2, 128, 64, BF16, seed=len(lens), extra_cols=500 if wide else 1)
     q = queries(len(lens), 8, 128, BF16)
     check_decode(c, q, binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens), 128 ** -0.5, "decode")
 
@@ -176,16 +180,18 @@ def test_prefill_of_one_token_each_is_decode():
 
 
 # ---------------------------------------------------------------- shared prefixes
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("prefix", [0, 1, 64, 333, 5000])
 @pytest.mark.parametrize("B,Hq,Hkv,d,page,dtype", [
     (1, 12, 12, 64, 16, F16), (5, 14, 2, 64, 32, BF16), (40, 8, 2, 128, 64, BF16), (300, 4, 1, 64, 16, F16),
-    (33, 32, 4, 128, 128, F16)])
-def test_shared_prefix(prefix, B, Hq, Hkv, d, page, dtype):
+    (33, 32, 4, 128, 128, F16), (3, 40, 1, 64, 16, BF16), (2, 140, 1, 64, 16, F16)])
+def test_shared_prefix(prefix, B, Hq, Hkv, d, page, dtype, wide):
     lens = [(i * 37) % 200 if i % 5 else 0 for i in range(B)]
-    c = Cache(lens, Hkv, d, page, dtype, slots_first=prefix % 2 == 1, seed=B, prefix=prefix)
+    c = Cache(lens, Hkv, d, page, dtype, slots_first=prefix % 2 == 1, seed=B, prefix=prefix,
+              extra_cols=(1 << 17) // page if wide else 2)
     q = queries(B, Hq, d, dtype)
     out = binding.decode_shared(q, c.k, c.v, c.prefix_table, c.prefix_len, c.table, c.seq_lens)
-    # the prefix's rows come rounded to fp32 only: the same bound as one pass
+    # the two passes' rows are joined in fp32: the same bound as one pass
     check_decode(c, q, out, d ** -0.5, f"prefix {prefix}")
     assert torch.equal(out, binding.decode_shared(q, c.k, c.v, c.prefix_table, c.prefix_len, c.table, c.seq_lens))
 
@@ -233,9 +239,10 @@ def test_workspaces_streams_and_strides():
     assert torch.equal(want, binding.decode_paged(q, k, v, c.table, c.seq_lens))
 
 
-def test_captured_calls_follow_lengths_that_change():
+@pytest.mark.parametrize("wide", [False, True])
+def test_captured_calls_follow_lengths_that_change(wide):
     lens = [300, 5, 0, 129]
-    full = Cache([400, 400, 400, 400], 2, 64, 16, BF16, seed=8, prefix=200)
+    full = Cache([400, 400, 400, 400], 2, 64, 16, BF16, seed=8, prefix=200, extra_cols=8192 if wide else 2)
     q = queries(4, 8, 64, BF16)
     seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
     outs = [torch.empty_like(q) for _ in range(2)]
@@ -263,6 +270,96 @@ def test_captured_calls_follow_lengths_that_change():
             k, v = (torch.cat([f, x]) for f, x in zip(full.front, (k, v)))
             want, _, bound = attend(q[b:b + 1].double(), k, v, 64 ** -0.5, False, BF16)
             assert_rows(outs[1][b:b + 1], want, bound, f"replayed, shared, length {n}")
+
+
+def test_captured_prefill_beside_an_eager_one():
+    """Two graphs, each with scratch of its own, replayed at once on two streams with an eager call between."""
+    c = Cache([3000, 700], 2, 128, 64, F16, seed=12, prefix=900, extra_cols=64)
+    q, qd = queries(500, 16, 128, F16), queries(2, 16, 128, F16, seed=3)
+    cu = torch.tensor([0, 400, 500], dtype=torch.int32, device="cuda")
+    calls = (lambda: binding.prefill_paged(q, c.k, c.v, c.table, c.seq_lens, cu, 400, causal=True),
+             lambda: binding.decode_paged(qd, c.k, c.v, c.table, c.seq_lens),
+             lambda: binding.decode_shared(qd, c.k, c.v, c.prefix_table, c.prefix_len, c.table, c.seq_lens))
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([f() for f in calls])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [f() for f in calls]
+        torch.cuda.synchronize()
+        for got in (*outs, eager):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_the_python_path_makes_the_same_calls(monkeypatch):
+    """What _paged_calls does not take on goes through the checks in Python, to the same result."""
+    c = Cache([90, 5, 300], 2, 64, 16, F16, seed=13, prefix=40)
+    q = queries(3, 8, 64, F16)
+    cu = torch.tensor([0, 1, 1, 3], dtype=torch.int32, device="cuda")
+    calls = (lambda **o: binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens, **o),
+             lambda **o: binding.prefill_paged(q, c.k, c.v, c.table, c.seq_lens, cu, 2, causal=True, **o),
+             lambda **o: binding.decode_shared(q, c.k, c.v, c.prefix_table, c.prefix_len, c.table, c.seq_lens, **o))
+    want = [(f(), f(scale=0.5), f(out=torch.empty_like(q))) for f in calls]
+
+    class Nothing:
+        decode = prefill = shared = append = staticmethod(lambda *a: NotImplemented)
+
+    monkeypatch.setattr(binding, "_calls", Nothing)
+    for f, (plain, scaled, given) in zip(calls, want):
+        assert torch.equal(f(), plain) and torch.equal(f(scale=0.5), scaled) and torch.equal(plain, given)
+        assert torch.equal(f(out_dtype=F16), plain)
+        wide = f(out_dtype=F32)
+        assert wide.dtype == F32 and torch.equal(wide.half(), plain)
+
+
+def test_binding_refusals():
+    c = Cache([90, 5], 2, 64, 16, F16, seed=14, prefix=16)
+    q = queries(2, 8, 64, F16)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    good = dict(q=q, k=c.k, v=c.v, table=c.table, lens=c.seq_lens, cu=cu, out=torch.empty_like(q))
+
+    def decode(a):
+        binding.decode_paged(a["q"], a["k"], a["v"], a["table"], a["lens"], out=a["out"])
+
+    def prefill(a):
+        binding.prefill_paged(a["q"], a["k"], a["v"], a["table"], a["lens"], a["cu"], 1, out=a["out"])
+
+    def shared(a):
+        binding.decode_shared(a["q"], a["k"], a["v"], c.prefix_table, c.prefix_len, a["table"], a["lens"], out=a["out"])
+
+    for call in (decode, prefill, shared):
+        call(good)
+        for change in (dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:1]), dict(q=q[..., :32]), dict(q=q.transpose(0, 1)),
+                       dict(k=c.k.bfloat16()), dict(v=c.v[:-1]), dict(k=c.k[0]), dict(k=c.k.cpu(), v=c.v.cpu()),
+                       dict(table=c.table.long()), dict(table=c.table[:1]), dict(table=c.table[0]),
+                       dict(table=c.table.cpu()), dict(table=c.table.t()), dict(lens=c.seq_lens.long()),
+                       dict(lens=c.seq_lens[:1]), dict(lens=c.seq_lens.cpu()), dict(out=torch.empty_like(q).float()),
+                       dict(out=torch.empty_like(q)[:1])):
+            if call is prefill and "q" in change and change["q"].shape == q[:1].shape and change["q"].dtype == F16 \
+                    and change["q"].is_cuda and change["q"].is_contiguous():
+                continue  # fewer packed tokens than the offsets say are recorded on the device, not refused
+            with pytest.raises((ValueError, TypeError)):
+                call({**good, **change})
+        with pytest.raises(binding.FaError) as e:  # seven query heads over two
+            call({**good, "q": queries(2, 7, 64, F16), "out": None})
+        assert e.value.status == binding.FA_ERR_SHAPE
+    for bad in (cu.long(), cu[:2], cu.cpu()):
+        with pytest.raises(ValueError):
+            prefill({**good, "cu": bad})
+    with pytest.raises(binding.FaError) as e:
+        binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens, scale=float("nan"))
+    assert e.value.status == binding.FA_ERR_SCALE
+    with pytest.raises(binding.FaError) as e:
+        binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens, out=q)
+    assert e.value.status == binding.FA_ERR_ALIAS
 
 
 def test_lengths_and_pages_out_of_range_are_recorded():
