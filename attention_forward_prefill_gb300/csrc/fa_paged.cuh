@@ -753,18 +753,18 @@ struct PagedPass {
     int grid, blocks;  // CTAs; row blocks of the longest sequence, per kv head
     long long units;   // no more units than this exist
     int device, num_sms;
-    bool join;
+    bool early, join;  // see PagedConfig; followed by paged_join_kernel
 };
 
 int launch_paged_tiles(const PagedPass &a, cudaStream_t stream);
 int launch_paged_cluster(const PagedPass &a, int size, cudaStream_t stream);
 
-// Launch attributes of the paged kernels: each may start before the kernels ahead of
+// Launch attributes of the paged kernels; `early`: may start before the kernels ahead of
 // it in the stream have finished (see paged_enter).
 struct PagedConfig {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute attr[1];
-    PagedConfig(dim3 grid, int threads, size_t smem, cudaStream_t stream) {
+    PagedConfig(dim3 grid, int threads, size_t smem, bool early, cudaStream_t stream) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         c.gridDim = grid;
@@ -772,7 +772,7 @@ struct PagedConfig {
         c.dynamicSmemBytes = smem;
         c.stream = stream;
         c.attrs = attr;
-        c.numAttrs = 1;
+        c.numAttrs = early ? 1 : 0;
     }
     PagedConfig(const PagedConfig &) = delete;
 };
@@ -797,7 +797,7 @@ int launch_join(const PagedPass &a, cudaStream_t stream) {
     if (a.grid > kJoinMax) return cuda_fail(cudaErrorInvalidConfiguration);
     const long long rows = std::min<long long>(a.grid, a.units) * std::min<long long>(a.p.block_rows, 1LL * a.p.max_q * a.p.G);
     const int grid = static_cast<int>(std::min<long long>(1LL * kJoinPerSm * a.num_sms, rows));
-    PagedConfig cfg(grid, kJoinThreads, 0, stream);
+    PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, a.p, a.grid);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }

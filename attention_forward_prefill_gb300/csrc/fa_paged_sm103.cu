@@ -225,7 +225,7 @@ int launch_rows(const PagedPass &a, cudaStream_t stream) {
     const auto kernel = paged_rows_kernel<D, RT, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, a.device, ready)) != FA_OK) return rc;
-    PagedConfig cfg(a.grid, kPagedThreads, L::kSmemBytes, stream);
+    PagedConfig cfg(a.grid, kPagedThreads, L::kSmemBytes, a.early, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mk, mv, a.p);
     if (e != cudaSuccess) return cuda_fail(e);
     return a.join ? launch_join<D, L::kRows>(a, stream) : FA_OK;
@@ -283,6 +283,7 @@ PagedPass make_pass(const PagedLaunch &a, const DeviceInfo &dev, void *scratch) 
     x.c = a.c;
     x.device = dev.device;
     x.num_sms = dev.num_sms;
+    x.early = true;
     x.join = true;
     PagedParams &p = x.p;
     p = PagedParams{};
@@ -379,6 +380,9 @@ int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scra
         x.p.unit_note = reinterpret_cast<int2 *>(at);
         at += align256(x.units * sizeof(int2));
         x.join = false;
+        // (One call right behind another: 192 us with the first pass launched when the last
+        // call's join is through, 208 with it waiting on the SMs under that join.)
+        x.early = i == 1;
         x.p.first = i == 0;
         x.p.num_sms = dev.num_sms;
         x.p.per_sm = x.plan.per_sm;
@@ -400,7 +404,7 @@ int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scra
         if ((rc = launch_pass(x, stream)) != FA_OK) return rc;
     constexpr long long kWarps = kJoinThreads / 32;
     const int grid = static_cast<int>(std::min<long long>(2LL * dev.num_sms, (static_cast<long long>(rows) + kWarps - 1) / kWarps));
-    PagedConfig cfg(grid, kJoinThreads, 0, stream);
+    PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, d == 64 ? paged_pair_join_kernel<64> : paged_pair_join_kernel<128>,
                                              pass[0].p, pass[1].p, pass[0].plan.slot_rows, pass[1].plan.slot_rows,
                                              pass[0].blocks, pass[1].blocks);

@@ -583,7 +583,7 @@ int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
     const auto kernel = paged_tiles_kernel<D, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, a.device, ready)) != FA_OK) return rc;
-    PagedConfig cfg(a.grid, kThreads, L::kSmemBytes, stream);
+    PagedConfig cfg(a.grid, kThreads, L::kSmemBytes, a.early, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, tile_tokens, p.scale_log2 < 0.f ? 1 : 0);
     if (e != cudaSuccess) return cuda_fail(e);
     return a.join ? launch_join<D, 2 * kM>(a, stream) : FA_OK;
