@@ -91,9 +91,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
         first = __ldg(p.cu + b);
         last = __ldg(p.cu + b + 1);
     }
-    const int pos = __ldg(p.seq_lens + b) - (last - first) + (t - first);
+    const long long at = static_cast<long long>(__ldg(p.seq_lens + b)) - last + t;
     const long long max_len = static_cast<long long>(p.max_pages) << p.page_shift;
-    bool slot_ok = pos >= 0 && pos < max_len && t >= first && t < last;
+    bool slot_ok = at >= 0 && at < max_len && t >= first && t < last;
+    const int pos = static_cast<int>(min(max(at, -1LL), max_len));
     int status = slot_ok ? 0 : FA_ERR_SEQ_LEN;
     int page = 0;
     if (slot_ok) {

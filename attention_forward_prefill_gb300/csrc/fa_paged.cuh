@@ -29,6 +29,16 @@
 
 namespace fa {
 
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int c0, int c1, int c2, int c3, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "l"(policy)
+        : "memory");
+}
+
 struct PagedParams {
     const uint16_t *q;     // [total_q][Hq][D]
     void *out;             // [total_q][Hq][D]
@@ -246,7 +256,7 @@ struct PagedCursor {
         b = st.b;
         s = paged_seq(p, b);
         blocks = paged_blocks(p, s);
-        const long long per_head = paged_head_steps<TK>(p, s);
+        const long long per_head = max(paged_head_steps<TK>(p, s), 1LL);
         hk = static_cast<int>(st.rem / per_head);
         long long rem = st.rem - hk * per_head;
         if (!p.causal) {
@@ -288,10 +298,12 @@ struct PagedCursor {
                 rb = 0;
                 if (++hk == p.Hkv) {
                     hk = 0;
-                    do {  // steps are left, so a later sequence has rows
+                    blocks = 0;
+                    while (blocks == 0 && b + 1 < p.B) {  // steps are left, so a later sequence has rows
                         s = paged_seq(p, ++b);
                         blocks = paged_blocks(p, s);
-                    } while (blocks == 0);
+                    }
+                    if (blocks == 0) left = 0;
                 }
             }
             if (some) return true;
@@ -319,17 +331,16 @@ __device__ __forceinline__ void paged_note_unit(const PagedParams &p, const Page
                         : make_int2(c, paged_cta_of(st.end + (tiles - u.j1) - 1, st.W, st.G) - c + 1);
 }
 
-// What a CTA notes about the unit it leaves unfinished (or that there is none): u, its
-// last piece, ended where the CTA's range does.
-__device__ __forceinline__ void paged_note_open(const PagedParams &p, const PagedPiece *u, int tiles, long long end,
-                                                long long W, int G) {
+// What a CTA notes about the unit it leaves unfinished: u, its last piece, ended where the
+// CTA's range does.  Without one (and while there is none: a CTA that gives up notes no
+// more) the note says so.
+__device__ __forceinline__ void paged_note_none(const PagedParams &p) {
+    p.open[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+}
+__device__ __forceinline__ void paged_note_open(const PagedParams &p, const PagedPiece &u, int tiles, const PagedStart &st) {
     int4 *o = p.open + 2 * blockIdx.x;
-    if (!u || u->kind != 1) {
-        o[0] = make_int4(-1, 0, 0, 0);
-        return;
-    }
-    o[0] = make_int4(paged_cta_of(end + (tiles - u->j1) - 1, W, G), u->t0, u->hk, u->row0);
-    o[1] = make_int4(u->nq, 0, 0, 0);
+    o[1] = make_int4(u.nq, 0, 0, 0);
+    o[0] = make_int4(paged_cta_of(st.end + (tiles - u.j1) - 1, st.W, st.G), u.t0, u.hk, u.row0);
 }
 
 // ---------------------------------------------------------------- rows out
@@ -631,7 +642,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) paged_join_kernel(co
 // takes R rows at a time; their notes, then their pieces, a's first and in CTA order.
 template <int D, int R, int F>
 __device__ __forceinline__ void paged_pair_rows(const PagedParams &a, const PagedParams &b, int slot_a, int slot_b,
-                                                int blocks_a, int blocks_b, int row0, int rows, int lane) {
+                                                int blocks_a, int blocks_b, int ctas_a, int ctas_b, int row0, int rows,
+                                                int lane) {
     constexpr int N = D / 32;
     // lane 2 r: row r's note in a; lane 2 r + 1: in b
     int2 note = make_int2(0, 0);
@@ -646,6 +658,8 @@ __device__ __forceinline__ void paged_pair_rows(const PagedParams &a, const Page
             note = a.unit_note[static_cast<long long>(hk) * blocks_a + r / a.block_rows];
             off = r % a.block_rows;
         }
+        // (a CTA that gave up has left notes unwritten)
+        if (note.x < 0 || note.y < 1 || note.y > (lane & 1 ? ctas_b : ctas_a) - note.x) note = make_int2(0, 0);
     }
     int ca[R], na[R], oa[R], cb[R], nb[R], ob[R], most = 0;
 #pragma unroll
@@ -696,7 +710,7 @@ __device__ __forceinline__ void paged_pair_rows(const PagedParams &a, const Page
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 2)
     paged_pair_join_kernel(const PagedParams a, const PagedParams b, const int slot_a, const int slot_b,
-                           const int blocks_a, const int blocks_b) {
+                           const int blocks_a, const int blocks_b, const int ctas_a, const int ctas_b) {
     const int lane = threadIdx.x & 31;
     const int rows = b.total_q * b.Hq;
     const int warps = gridDim.x * (kJoinThreads / 32), w = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
@@ -705,10 +719,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     // rows enough for every warp: two at a time, few pieces each; else one with more of its pieces in flight
     if (rows >= 2 * warps)
         for (int r = 2 * w; r < rows; r += 2 * warps)
-            paged_pair_rows<D, 2, 4>(a, b, slot_a, slot_b, blocks_a, blocks_b, r, rows - r, lane);
+            paged_pair_rows<D, 2, 4>(a, b, slot_a, slot_b, blocks_a, blocks_b, ctas_a, ctas_b, r, rows - r, lane);
     else
         for (int r = w; r < rows; r += warps)
-            paged_pair_rows<D, 1, 12>(a, b, slot_a, slot_b, blocks_a, blocks_b, r, 1, lane);
+            paged_pair_rows<D, 1, 12>(a, b, slot_a, slot_b, blocks_a, blocks_b, ctas_a, ctas_b, r, 1, lane);
 }
 
 // ---------------------------------------------------------------- host side

@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         const int my_box = lane % boxes, my_slab = lane / boxes % (D / 64), my_op = lane / boxes / (D / 64);
         bool ok = true;
         PagedCursor<kTile> cur;
+        if (lane == 0) paged_note_none(p);
         cur.begin(p, *start);
         PagedPiece u;
         int unit_tiles = 0;
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             if (more) {
                 if (lane == 0) paged_note_unit(p, u, unit_tiles, *start);
             } else {
-                if (lane == 0) paged_note_open(p, any ? &u : nullptr, unit_tiles, start->end, start->W, start->G);
+                if (lane == 0 && any && u.kind == 1) paged_note_open(p, u, unit_tiles, *start);
                 u.kind = -1;
             }
             any = true;
@@ -407,7 +408,7 @@ int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scra
     PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, d == 64 ? paged_pair_join_kernel<64> : paged_pair_join_kernel<128>,
                                              pass[0].p, pass[1].p, pass[0].plan.slot_rows, pass[1].plan.slot_rows,
-                                             pass[0].blocks, pass[1].blocks);
+                                             pass[0].blocks, pass[1].blocks, pass[0].grid, pass[1].grid);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane -> (half of a group: V_j or K_j+1, slab, page) of its copies: up to 2 x 2 x 8
         const int my_box = lane % boxes, my_slab = lane / boxes % L::kSlabs, my_half = lane / boxes / L::kSlabs;
         PagedCursor<kKeys> cur;
+        if (lane == 0) paged_note_none(p);
         cur.begin(p, *start);
         PagedPiece u;
         int unit_tiles = 0;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) {
                 if (lane == 0) paged_note_unit(p, u, unit_tiles, *start);
             } else {
-                if (lane == 0) paged_note_open(p, any ? &u : nullptr, unit_tiles, start->end, start->W, start->G);
+                if (lane == 0 && any && u.kind == 1) paged_note_open(p, u, unit_tiles, *start);
                 u.kind = -1;
             }
             any = true;

@@ -158,6 +158,15 @@ def test_prefill_lengths(new, had, Hq, Hkv, d, dtype):
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new", [[3, 9], [300, 1], [1, 700]])
+def test_prefill_without_keys(new, causal):
+    """Queries of a sequence whose cache is empty give zero rows."""
+    check_prefill([0, 0], new, 4, 2, 64, 16, F16, causal)
+    check_prefill([0, 40], new, 8, 1, 128, 32, BF16, causal)
+    check_prefill([200, 0], new, 3, 3, 128, 64, F16, causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
 def test_prefill_many_and_long(causal):
     check_prefill([20000], [33], 8, 2, 128, 64, BF16, causal)
     check_prefill([1500] * 9, [1500, 1, 0, 700, 1500, 2, 3, 4, 5], 6, 2, 64, 32, F16, causal)
