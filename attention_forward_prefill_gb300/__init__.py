@@ -1,4 +1,4 @@
-"""GB300-native fused attention forward (prefill + split-K decode).
+"""GB300-native fused attention (prefill, its backward, split-K decode, a paged cache).
 
 The compute path is the CUDA library ``libfa_gb300.so`` built from ``csrc/``
 for sm_103a; ``binding`` is a thin ctypes layer over its C ABI.  Importing this

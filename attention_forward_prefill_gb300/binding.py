@@ -3,7 +3,8 @@
 The ``fa_*`` functions mirror the C entry points one to one (pointers as
 Python ints, streams as ints).  ``prefill`` / ``decode`` are the two calls of
 the flash-attention-cuda README's usage section, taking torch tensors: they
-only check and marshal arguments, allocate the output, and call the library.
+only check and marshal arguments, allocate the output, and call the library; so do the calls
+on a paged cache at the end, whose usual arguments are read by the CPython module _paged_calls.
 Every step of the computation runs in the library's CUDA kernels; if the
 library is missing this module raises -- there is no CPU fallback.
 """

@@ -1,8 +1,9 @@
 """Build libfa_gb300.so in-tree from csrc/*.cu with nvcc for sm_103a.
 
 One translation unit per kernel family, compiled in parallel, then linked
-into a shared library next to this file.  No torch C++ ABI is involved, so the
-same sources build on x86 and Arm hosts.
+into a shared library next to this file; and the CPython module _paged_calls, with the
+host's C compiler.  No torch C++ ABI is involved, so the same sources build on x86 and
+Arm hosts.
 """
 from __future__ import annotations
 

@@ -1,6 +1,7 @@
 /*
- * fa.h -- C ABI of libfa_gb300.so: fused scaled-dot-product attention forward
- * (prefill and split-K decode) for one NVIDIA GB300 (sm_103a).
+ * fa.h -- C ABI of libfa_gb300.so: fused scaled-dot-product attention (prefill,
+ * its backward, split-K decode, and a paged key/value cache) for one NVIDIA GB300
+ * (sm_103a).
  *
  * What is computed (flash-attention-cuda README, "What is Attention?", "What is
  * Flash Attention?" and the "Kernel design" table):
