@@ -242,6 +242,14 @@ struct PagedPiece {
     int kind;       // 0 whole unit, 1 opens a unit that the next CTA continues, 2 continues one, -1 no more work
 };
 
+// True never, and known only when a piece is in registers, in every lane: what hands its
+// place back hangs on it (see PagedRows::loads_pending).  zero: a mask that is zero, which the
+// compiler does not know.
+__device__ __forceinline__ bool paged_pending(const PagedPiece &u, int zero) {
+    const int x = u.b | u.t0 | u.nq | u.len | u.hk | u.row0 | u.j0 | u.j1 | u.end0 | u.end1 | u.kind;
+    return __any_sync(0xffffffffu, (x & zero) != 0);
+}
+
 // Walks a CTA's pieces in order.  A unit's steps are its unit_steps, then its key
 // tiles: a range that ends among the former leaves the whole unit to the next CTA.
 template <int TK>

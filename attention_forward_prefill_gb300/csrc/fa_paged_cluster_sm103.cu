@@ -183,8 +183,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                     const int k0 = (j - pre_tiles) * kTile;
                     r.tile(ring + st * L::kStage, lim0 - k0, lim1 - k0, u.len - k0, p.scale_log2);
                 }
+                const bool pending = r.loads_pending(static_cast<uint32_t>(p.unit_steps) >> 30);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty + st);
+                if (lane == 0) mbar_arrive(empty + st + pending);
             }
         }
         if (ok) {

@@ -65,6 +65,7 @@ struct PagedRows {
     // once a key has been seen (0 before, when masked scores of -inf still give weight 0)
     float m0, m1, l0, l1, n0, n1;
     uint32_t joins;
+    uint32_t loads;  // of begin() or tile(): a register of each, or-ed
 
     __device__ __forceinline__ explicit PagedRows(int warp, int lane_)
         : lane(lane_), quad(lane_ & 3), qrow(lane_ >> 2), rw(warp % RT), kw(warp / RT), joins(0) {}
@@ -80,6 +81,19 @@ struct PagedRows {
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
         m0 = m1 = -INFINITY;
         l0 = l1 = n0 = n1 = 0.f;
+        loads = 0;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) loads |= qf[kk][0];
+    }
+
+    // True never, and known only when the shared-memory loads of begin() or tile() have
+    // arrived in every lane: what hands their place back hangs on it.  (zero: a mask that
+    // is zero, which the compiler does not know.)  A barrier arrival alone comes after the
+    // loads' issue, not their end, and nothing else binds the copy engine that writes the
+    // place next: without this, one call in two of many short units of 32 rows took a query
+    // row, and one in a thousand a piece of a V tile, from the data that came behind.
+    __device__ __forceinline__ bool loads_pending(uint32_t zero) const {
+        return __any_sync(0xffffffffu, (loads & zero) != 0);
     }
 
     // One tile: K at shared address kt, V behind it (128-byte swizzled slabs of 64
@@ -163,6 +177,7 @@ struct PagedRows {
             pf[nb >> 1][(nb & 1) * 2] = lo;
             pf[nb >> 1][(nb & 1) * 2 + 1] = hi;
         }
+        loads = 0;  // (those of K are through: the weights come from them)
         // ---- O += P V.  Slots behind the last key hold anything at all, so their V
         // rows are read as zero (0 x NaN would be NaN).
 #pragma unroll
@@ -178,6 +193,7 @@ struct PagedRows {
                 uint32_t vb[4];
                 const int chunk = (c & 3) * 2 + (lane >> 4);
                 ldmatrix4_trans(vt + (c >> 2) * kSlab + kb * 2048 + v_row + ((chunk ^ (lane & 7)) << 4), vb);
+                loads |= vb[0];
                 mma_16816<BF16>(o[2 * c], pf[kb], vb[0] & mask0, vb[1] & mask1);
                 mma_16816<BF16>(o[2 * c + 1], pf[kb], vb[2] & mask0, vb[3] & mask1);
             }

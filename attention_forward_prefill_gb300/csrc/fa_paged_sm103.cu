@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         PagedCursor<kTile> cur;
         if (lane == 0) paged_note_none(p);
         cur.begin(p, *start);
-        PagedPiece u;
+        PagedPiece u = {};
         int unit_tiles = 0;
         bool any = false;
         while (ok) {
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     } else {
         // ------------------------------------------------------------ consumers
         R rows(warp, lane);
+        const uint32_t zero = static_cast<uint32_t>(p.unit_steps) >> 30;
         const uint32_t ring = smem_u32(smem);
         bool ok = true;
         while (ok) {
@@ -166,8 +167,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             const PagedPiece u = *piece;
             if (u.kind < 0) break;
             rows.begin(smem_u32(smem + L::kQOff), L::kQPitch);
+            const bool pending = rows.loads_pending(zero) || paged_pending(u, static_cast<int>(zero));
             __syncwarp();
-            if (lane == 0) mbar_arrive(u_empty);
+            if (lane == 0) mbar_arrive(u_empty + pending);
             // the last key that each of this thread's two rows sees
             int lim0 = u.len - 1, lim1 = u.len - 1;
             if (p.causal) {
@@ -180,8 +182,9 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                 if (!lanes_wait(full + st, (tiles / L::kStages) & 1, abort_flag)) { ok = false; break; }
                 ++tiles;
                 rows.tile(ring + st * L::kStage, lim0 - j * kTile, lim1 - j * kTile, u.len - j * kTile, p.scale_log2);
+                const bool pending = rows.loads_pending(zero);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty + st);
+                if (lane == 0) mbar_arrive(empty + st + pending);
             }
             if (!ok) break;
             rows.end();

@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         u.kind = -1;
         if (lanes_wait(u_full + slot, (pieces >> 1) & 1, abort_flag)) {
             u = *piece_at(pieces);
+            const bool pending = paged_pending(u, p.unit_steps >> 30);
             __syncwarp();
-            if (lane == 0) mbar_arrive(u_empty + slot);
+            if (lane == 0) mbar_arrive(u_empty + slot + pending);
             ++pieces;
         } else {
             ok = false;
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         PagedCursor<kKeys> cur;
         if (lane == 0) paged_note_none(p);
         cur.begin(p, *start);
-        PagedPiece u;
+        PagedPiece u = {};
         int unit_tiles = 0;
         bool any = false;
         while (ok) {

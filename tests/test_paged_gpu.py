@@ -98,6 +98,18 @@ def test_decode_is_the_same_bits_every_time_and_follows_the_contiguous_cache():
     assert (first.float() - other.float()).abs().max() <= 3 * 2.0 ** -11 * float(flat[1].abs().max())
 
 
+@pytest.mark.parametrize("G,d,dtype", [(32, 128, BF16), (17, 128, F16), (16, 128, BF16), (64, 128, F16), (32, 64, F16)])
+def test_many_short_units_keep_their_own_queries(G, d, dtype):
+    """Unit after unit through the same shared memory: each one's rows are its own, call after call."""
+    lens = [(i * 61) % 450 for i in range(40)]
+    c = Cache(lens, 8, d, 64, dtype, seed=21)
+    q = queries(40, G * 8, d, dtype)
+    out = binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens)
+    check_decode(c, q, out, d ** -0.5, "short units")
+    for _ in range(200):
+        assert torch.equal(out, binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens))
+
+
 def test_offsets_past_32_bits():
     """Pages whose element and byte offsets pass 2^31 and 2^32."""
     Hkv, d, page = 8, 128, 64
