@@ -327,3 +327,48 @@ def test_serving_loop(shared):
             K[b].append(turned(k[b:b + 1].double(), pos, d, False).to(dtype).double())
             V[b].append(v[b:b + 1].double())
             check(q, out, b, slice(b, b + 1), pos, f"step {i}, sequence {b}")
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("wide", [1, 400])
+def test_a_chain_of_dependent_calls_needs_no_waiting(shared, wide):
+    """Each step's queries, keys and values come from the last step's rows, nothing waits on the host, and kernels
+    start under the tail of those before them: the same bits as with a wait after every call."""
+    Hq, Hkv, d, page, B, steps, front = 16, 4, 128, 32, 6, 40, 300
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cols = -(-(steps + 60) // page)
+    start = torch.randn(B, Hq, d, generator=g, device="cuda").to(BF16)
+    pre = [torch.randn(front, Hkv, d, generator=g, device="cuda").to(BF16) for _ in range(2)]
+    rope = binding.rope_table(1024, d)
+    table = torch.full((B, cols * wide), -1, dtype=torch.int32, device="cuda")
+    table[:, :cols] = torch.randperm(B * cols, generator=g, device="cuda").view(B, cols).int()
+    front_table = (B * cols + torch.arange(-(-front // page), device="cuda")).int()
+
+    def run(wait):
+        kp, vp = (torch.zeros(B * cols + 10, Hkv, page, d, dtype=BF16, device="cuda") for _ in range(2))
+        seq = torch.arange(B, dtype=torch.int32, device="cuda") * 9
+        x, rows = start.clone(), []
+
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+
+        binding.cache_append(None, *pre, kp, vp, front_table[None].contiguous(), ints([front]), cu_seqlens=ints([0, front]))
+        done()
+        for _ in range(steps):
+            seq.add_(1)
+            q = binding.cache_append(x, x[:, :Hkv], x[:, Hkv:2 * Hkv], kp, vp, table, seq, rope=rope)
+            done()
+            if shared:
+                x = binding.decode_shared(q, kp, vp, front_table, ints([front]), table, seq)
+            else:
+                x = binding.decode_paged(q, kp, vp, table, seq)
+            done()
+            x = x + start * 0.5
+            rows.append(x)
+        torch.cuda.synchronize()
+        return torch.stack(rows), kp, vp
+
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
