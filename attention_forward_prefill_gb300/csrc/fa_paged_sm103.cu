@@ -92,6 +92,10 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     }
     paged_enter(p);
     paged_plan<kTile, kPagedThreads>(p, *start, warp_sum, &g_paged_status);
+    if (static_cast<int>(blockIdx.x) >= start->G) {  // no work: makes room for a CTA that has some
+        if (threadIdx.x == 0) paged_note_none(p);
+        return;
+    }
     uint32_t units = 0, tiles = 0;  // handed over / taken so far
 
     if (warp == kConsumers) {
@@ -202,8 +206,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         }
         __syncwarp();
     }
-    // Whoever waits for this grid also waits for the grids before it.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    paged_leave(p);
     __syncthreads();
     if (*abort_flag && warp == kConsumers && lane == 0) {
         // let every copy already issued land before the CTA goes away
