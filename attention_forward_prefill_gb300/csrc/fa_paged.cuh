@@ -437,7 +437,9 @@ __device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiec
 // (one long sequence: 300 pieces of 64 rows took 26 us a warp per row).  8 us for 303 units
 // of 4 rows, 13 us for 151 of 256 (39 MB of pieces, out of L2).
 constexpr int kJoinThreads = 256;
-constexpr int kJoinPerSm = 2;
+// CTAs per SM (d = 64: 3 take 2.5 us less than 2 for 151 units of 256 rows; d = 128 at 3: spills, 7 us more)
+template <int D>
+constexpr int kJoinPerSm = D == 64 ? 3 : 2;
 constexpr int kJoinMax = 512;  // CTAs of the main kernel
 
 // The sums of R rows over n pieces, F pieces at a time: ml_at(k, r) and row_at(k, r)
@@ -546,7 +548,7 @@ __device__ __forceinline__ void paged_join_few(const PagedParams &p, int c, cons
 __device__ __forceinline__ int join_rows_each(int pieces) { return pieces <= 2 ? 4 : (pieces <= 4 ? 2 : 1); }
 
 template <int D, int RB>
-__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) paged_join_kernel(const PagedParams p, const int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm<D>) paged_join_kernel(const PagedParams p, const int ctas) {
     __shared__ int4 note[kJoinMax];
     __shared__ int first[kJoinMax];  // items before CTA c's unit
     __shared__ int rows_of[kJoinMax];
@@ -829,7 +831,7 @@ template <int D, int RB>
 int launch_join(const PagedPass &a, cudaStream_t stream) {
     if (a.grid > kJoinMax) return cuda_fail(cudaErrorInvalidConfiguration);
     const long long rows = std::min<long long>(a.grid, a.units) * std::min<long long>(a.p.block_rows, 1LL * a.p.max_q * a.p.G);
-    const int grid = static_cast<int>(std::min<long long>(1LL * kJoinPerSm * a.num_sms, rows));
+    const int grid = static_cast<int>(std::min<long long>(1LL * kJoinPerSm<D> * a.num_sms, rows));
     PagedConfig cfg(grid, kJoinThreads, 0, true, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, paged_join_kernel<D, RB>, a.p, a.grid);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
