@@ -7,8 +7,8 @@
 // sequence with nq query tokens gives each kv head nq * G query rows
 // (G = query heads per kv head), row r = (token r / G, head r % G), cut into
 // blocks of block_rows.  A unit = (sequence, kv head, row block); it costs
-// unit_steps for its own start and end and a step per key tile its rows can see
-// (at least one, so that a unit without keys still writes its rows).  The W
+// unit_steps for its own start and end and a step per key tile its rows can see,
+// or a few (PagedCut; at least one tile, so that a unit without keys still writes its rows).  The W
 // steps of the whole call, in the order (sequence, kv head, block), are cut
 // into gridDim.x equal ranges, one per CTA, whatever the lengths are: they live
 // on the device, so the cut is made there, by every CTA for itself (1 to 2 us,
@@ -54,6 +54,7 @@ struct PagedParams {
     int num_pages, page_shift;
     int block_rows;         // query rows of a unit
     int unit_steps;         // what a unit costs besides its key tiles, in steps
+    int tile_tokens;        // paged_tiles_kernel: tokens of a query tile, of which a block has two
     int causal;             // query token i of nq sees keys j <= len - nq + i
     float scale_log2;       // scale * log2(e)
     int out_dtype;
@@ -70,7 +71,7 @@ struct PagedParams {
     int2 *unit_note;            // [B][Hkv][row blocks]: the CTA that opened the unit, its pieces (1: dense)
     // Such a pass also leaves SMs to the other one, in proportion to their work.
     const int *peer_lens;       // the other pass's seq_lens
-    int peer_B, peer_max_len, peer_blocks, peer_tile, peer_unit_steps;
+    int peer_B, peer_max_len, peer_blocks, peer_tile, peer_tile_steps, peer_unit_steps;
     int step_ns, peer_step_ns;  // SM time of a step of this pass, and of the other
     int num_sms, per_sm, first; // first: the pass that is launched first
 };
@@ -111,8 +112,8 @@ __device__ __forceinline__ bool paged_seq_bad(const PagedParams &p, int b) {
     return bad;
 }
 
-// Key tiles (TK keys each) that rows up to last_row of a sequence, or row block rb, must
-// visit: at least one.
+// Key tiles (TK keys each) that rows up to last_row of a sequence must visit:
+// at least one.
 template <int TK>
 __device__ __forceinline__ int paged_tiles_to_row(const PagedParams &p, const SeqView &s, int last_row) {
     int seen = s.len;
@@ -120,23 +121,67 @@ __device__ __forceinline__ int paged_tiles_to_row(const PagedParams &p, const Se
     return max(1, (seen + TK - 1) / TK);
 }
 
-template <int TK>
-__device__ __forceinline__ int paged_tiles(const PagedParams &p, const SeqView &s, int rb) {
-    return paged_tiles_to_row<TK>(p, s, rb * p.block_rows + p.block_rows - 1);
-}
-
 __device__ __forceinline__ int paged_blocks(const PagedParams &p, const SeqView &s) {
     return (s.nq * p.G + p.block_rows - 1) / p.block_rows;
 }
 
+// How a kernel's work is cut: keys of a tile, and what a key tile costs in steps.  Of
+// paged_tiles_kernel's two query tiles (KEYS = 128) a causal or short block has key tiles
+// that one alone visits, ONE steps against BOTH.
+template <int KEYS, int BOTH, int ONE>
+struct PagedCut {
+    static constexpr int kKeys = KEYS, kBoth = BOTH, kOne = ONE;
+};
+
+using RowsCut = PagedCut<64, 1, 1>;
+// (Per CTA of 4 chunks of 700 to 2048 tokens at d = 128 and 3 prompts of 3500 to 5000 at d = 64,
+// fitted: a key tile 1.80 us for both and 1.60 for one, and 1.60 and 1.10; a piece 2.64 and 2.39.)
+template <int D>
+using TilesCut = PagedCut<128, D == 64 ? 3 : 1, D == 64 ? 2 : 1>;
+
+// What row block rb costs, in steps: its unit_steps, then its key tiles in order, those
+// that both query tiles visit first.
+template <typename C>
+struct UnitSteps {
+    int tiles, both;  // key tiles, and those for both query tiles
+    int total;
+
+    __device__ __forceinline__ UnitSteps(const PagedParams &p, const SeqView &s, int rb) {
+        if constexpr (C::kKeys == 128) {
+            // (no division by G: the plan goes through all blocks of a causal sequence, and with
+            // two divisions each its CTAs started 5 us later for 32 blocks)
+            const int tok1 = (2 * rb + 1) * p.tile_tokens;  // the second query tile's first token
+            const int past = s.len - s.nq;
+            auto tiles_to = [&](int tok) {  // that tokens before tok visit: at least one
+                return max(1, ((p.causal ? max(0, past + min(s.nq, tok)) : s.len) + C::kKeys - 1) / C::kKeys);
+            };
+            tiles = tiles_to(tok1 + p.tile_tokens);
+            both = C::kBoth == C::kOne ? tiles : (tok1 < s.nq ? tiles_to(tok1) : 0);
+        } else {
+            tiles = both = paged_tiles_to_row<C::kKeys>(p, s, rb * p.block_rows + p.block_rows - 1);
+        }
+        total = before(p, tiles);
+    }
+    // Steps before key tile j.
+    __device__ __forceinline__ int before(const PagedParams &p, int j) const {
+        return p.unit_steps + j * C::kOne + min(j, both) * (C::kBoth - C::kOne);
+    }
+    // Key tiles that start before step v: a range has those that start in it.
+    __device__ __forceinline__ int tiles_before(const PagedParams &p, int v) const {
+        const int e = max(0, v - p.unit_steps), b = both * C::kBoth;
+        return e <= b ? (e + C::kBoth - 1) / C::kBoth : min(tiles, both + (e - b + C::kOne - 1) / C::kOne);
+    }
+};
+
 // Steps of one kv head of a sequence.
-template <int TK>
+template <typename C>
 __device__ __forceinline__ long long paged_head_steps(const PagedParams &p, const SeqView &s) {
     const int n = paged_blocks(p, s);
     if (n == 0) return 0;
-    long long sum = static_cast<long long>(n) * p.unit_steps;
-    if (!p.causal || n == 1) return sum + static_cast<long long>(n) * paged_tiles<TK>(p, s, n - 1);
-    for (int rb = 0; rb < n; ++rb) sum += paged_tiles<TK>(p, s, rb);
+    long long sum = UnitSteps<C>(p, s, n - 1).total;
+    if (n == 1) return sum;
+    if (!p.causal) return sum + static_cast<long long>(n - 1) * UnitSteps<C>(p, s, 0).total;
+    for (int rb = 0; rb < n - 1; ++rb) sum += UnitSteps<C>(p, s, rb).total;
     return sum;
 }
 
@@ -169,7 +214,7 @@ struct PagedStart {
 };
 
 // The whole CTA (NT threads) adds up the sequences' steps and finds its range.
-template <int TK, int NT>
+template <typename C, int NT>
 __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st, long long *warp_sum, int *status) {
     constexpr int NW = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -178,7 +223,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
     long long mine = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
-        mine += paged_head_steps<TK>(p, paged_seq(p, b)) * p.Hkv;
+        mine += paged_head_steps<C>(p, paged_seq(p, b)) * p.Hkv;
         bad |= paged_seq_bad(p, b);
     }
     if (bad && blockIdx.x == 0) atomicCAS(status, 0, static_cast<int>(FA_ERR_SEQ_LEN));
@@ -202,7 +247,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
         long long theirs = 0;
         for (int b = tid; b < p.peer_B; b += NT) {
             const int len = min(max(__ldg(p.peer_lens + b), 0), p.peer_max_len);
-            theirs += max(1, (len + p.peer_tile - 1) / p.peer_tile) + p.peer_unit_steps;
+            theirs += max(1, (len + p.peer_tile - 1) / p.peer_tile) * p.peer_tile_steps + p.peer_unit_steps;
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) theirs += __shfl_xor_sync(0xffffffffu, theirs, off);
@@ -219,7 +264,8 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
         most = min(most, p.per_sm * (p.first ? first_sms : max(p.num_sms - first_sms, 1)));
     }
     const int c = blockIdx.x;
-    const int G = static_cast<int>(min(static_cast<long long>(most), max(W, 1LL)));
+    // (a range holds a key tile at least, but for those in a unit's first steps)
+    const int G = static_cast<int>(min(static_cast<long long>(most), max(W / C::kBoth, 1LL)));
     const long long first = c < G ? c * W / G : W;
     const long long end = c < G ? (c + 1) * W / G : W;
     if (tid == 0) {
@@ -232,7 +278,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
         long long rem = first - before;
         int b = b0;
         for (; b < b1 - 1; ++b) {
-            const long long c = paged_head_steps<TK>(p, paged_seq(p, b)) * p.Hkv;
+            const long long c = paged_head_steps<C>(p, paged_seq(p, b)) * p.Hkv;
             if (rem < c) break;
             rem -= c;
         }
@@ -259,9 +305,9 @@ __device__ __forceinline__ bool paged_pending(const PagedPiece &u, int zero) {
     return __any_sync(0xffffffffu, (x & zero) != 0);
 }
 
-// Walks a CTA's pieces in order.  A unit's steps are its unit_steps, then its key
-// tiles: a range that ends among the former leaves the whole unit to the next CTA.
-template <int TK>
+// Walks a CTA's pieces in order (UnitSteps: a range that ends among a unit's unit_steps
+// leaves the whole unit to the next CTA).
+template <typename C>
 struct PagedCursor {
     SeqView s;
     int b, hk, rb, blocks, v;  // v: the next step of unit (b, hk, rb)
@@ -273,32 +319,33 @@ struct PagedCursor {
         b = st.b;
         s = paged_seq(p, b);
         blocks = paged_blocks(p, s);
-        const long long per_head = max(paged_head_steps<TK>(p, s), 1LL);
+        const long long per_head = max(paged_head_steps<C>(p, s), 1LL);
         hk = static_cast<int>(st.rem / per_head);
         long long rem = st.rem - hk * per_head;
         if (!p.causal) {
-            const int c = paged_tiles<TK>(p, s, 0) + p.unit_steps;
+            const int c = UnitSteps<C>(p, s, 0).total;  // (the last block's may be less)
             rb = static_cast<int>(rem / c);
             v = static_cast<int>(rem - static_cast<long long>(rb) * c);
             return;
         }
         for (rb = 0; rb < blocks - 1; ++rb) {
-            const int c = paged_tiles<TK>(p, s, rb) + p.unit_steps;
+            const int c = UnitSteps<C>(p, s, rb).total;
             if (rem < c) break;
             rem -= c;
         }
         v = static_cast<int>(rem);
     }
 
-    // The next piece with key tiles; false when the range is used up.  tiles: the whole unit's.
-    __device__ __forceinline__ bool next(const PagedParams &p, PagedPiece &u, int &tiles) {
+    // The next piece with key tiles; false when the range is used up.  to_last: steps from
+    // the piece's end to the start of the unit's last tile (of a piece that opens a unit).
+    __device__ __forceinline__ bool next(const PagedParams &p, PagedPiece &u, int &to_last) {
         while (left > 0) {
-            const int t = paged_tiles<TK>(p, s, rb), cost = t + p.unit_steps;
-            const int end = static_cast<int>(min(static_cast<long long>(cost), v + left));
-            const int j0 = max(0, v - p.unit_steps), j1 = max(0, end - p.unit_steps);
+            const UnitSteps<C> c(p, s, rb);
+            const int end = static_cast<int>(min(static_cast<long long>(c.total), v + left));
+            const int j0 = c.tiles_before(p, v), j1 = c.tiles_before(p, end);
             const bool some = j1 > j0;
             if (some) {
-                tiles = t;
+                to_last = c.before(p, c.tiles - 1) - end;
                 u.b = b;
                 u.t0 = s.t0;
                 u.nq = s.nq;
@@ -307,7 +354,7 @@ struct PagedCursor {
                 u.row0 = rb * p.block_rows;
                 u.j0 = j0;
                 u.j1 = j1;
-                u.kind = j0 > 0 ? 2 : (j1 < t ? 1 : 0);
+                u.kind = j0 > 0 ? 2 : (j1 < c.tiles ? 1 : 0);
             }
             left -= end - v;
             v = 0;
@@ -339,13 +386,13 @@ __device__ __forceinline__ int paged_cta_of(long long step, long long W, int G) 
 }
 
 // Where a unit's pieces are, for paged_pair_join_kernel: noted by the CTA whose piece starts it.
-__device__ __forceinline__ void paged_note_unit(const PagedParams &p, const PagedPiece &u, int tiles, const PagedStart &st) {
+__device__ __forceinline__ void paged_note_unit(const PagedParams &p, const PagedPiece &u, int to_last, const PagedStart &st) {
     if (!p.unit_note || u.kind == 2) return;
     const int blocks = (u.nq * p.G + p.block_rows - 1) / p.block_rows;
     int2 *note = p.unit_note + (static_cast<long long>(u.b) * p.Hkv + u.hk) * blocks + u.row0 / p.block_rows;
     const int c = blockIdx.x;
     *note = u.kind == 0 ? make_int2(c, 1)
-                        : make_int2(c, paged_cta_of(st.end + (tiles - u.j1) - 1, st.W, st.G) - c + 1);
+                        : make_int2(c, paged_cta_of(st.end + to_last, st.W, st.G) - c + 1);
 }
 
 // What a CTA notes about the unit it leaves unfinished: u, its last piece, ended where the
@@ -354,10 +401,10 @@ __device__ __forceinline__ void paged_note_unit(const PagedParams &p, const Page
 __device__ __forceinline__ void paged_note_none(const PagedParams &p) {
     p.open[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
-__device__ __forceinline__ void paged_note_open(const PagedParams &p, const PagedPiece &u, int tiles, const PagedStart &st) {
+__device__ __forceinline__ void paged_note_open(const PagedParams &p, const PagedPiece &u, int to_last, const PagedStart &st) {
     int4 *o = p.open + 2 * blockIdx.x;
     o[1] = make_int4(u.nq, 0, 0, 0);
-    o[0] = make_int4(paged_cta_of(st.end + (tiles - u.j1) - 1, st.W, st.G), u.t0, u.hk, u.row0);
+    o[0] = make_int4(paged_cta_of(st.end + to_last, st.W, st.G), u.t0, u.hk, u.row0);
 }
 
 // ---------------------------------------------------------------- rows out
@@ -775,9 +822,10 @@ struct PagedPlan {
     bool tiles;      // 128-row tensor-memory tiles (paged_tiles_kernel), else paged_rows_kernel
     int block_rows;  // query rows of a unit
     int slot_rows;   // rows of a partial slot
-    int tile;        // keys per step
+    int tile;        // keys of a tile
     int per_sm;      // CTAs per SM
-    int unit_steps;  // what a unit costs besides its key tiles, in steps
+    int tile_steps;  // what a key tile costs, in steps (PagedCut: of both query tiles)
+    int unit_steps;  // what a unit costs besides its key tiles
 };
 
 // One launch of a main kernel, with its join or without.

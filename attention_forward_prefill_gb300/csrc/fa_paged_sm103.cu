@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         prefetch_tensormap(&map_v);
     }
     paged_enter(p);
-    paged_plan<kTile, kPagedThreads>(p, *start, warp_sum, &g_paged_status);
+    paged_plan<RowsCut, kPagedThreads>(p, *start, warp_sum, &g_paged_status);
     if (static_cast<int>(blockIdx.x) >= start->G) {  // no work: makes room for a CTA that has some
         if (threadIdx.x == 0) paged_note_none(p);
         return;
@@ -106,18 +106,18 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         // lane -> (operand, slab, box) of a tile's copies
         const int my_box = lane % boxes, my_slab = lane / boxes % (D / 64), my_op = lane / boxes / (D / 64);
         bool ok = true;
-        PagedCursor<kTile> cur;
+        PagedCursor<RowsCut> cur;
         if (lane == 0) paged_note_none(p);
         cur.begin(p, *start);
         PagedPiece u = {};
-        int unit_tiles = 0;
+        int to_last = 0;
         bool any = false;
         while (ok) {
-            const bool more = cur.next(p, u, unit_tiles);
+            const bool more = cur.next(p, u, to_last);
             if (more) {
-                if (lane == 0) paged_note_unit(p, u, unit_tiles, *start);
+                if (lane == 0) paged_note_unit(p, u, to_last, *start);
             } else {
-                if (lane == 0 && any && u.kind == 1) paged_note_open(p, u, unit_tiles, *start);
+                if (lane == 0 && any && u.kind == 1) paged_note_open(p, u, to_last, *start);
                 u.kind = -1;
             }
             any = true;
@@ -220,11 +220,15 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
 }
 
 // How a call runs, from its sizes alone.
-PagedPlan plan_paged(int max_q, int group) {
+PagedPlan plan_paged(int max_q, int group, int d) {
     const long long rows = static_cast<long long>(max_q) * group;
-    if (rows > 64 && group <= 128) return {true, 2 * (128 / group) * group, 256, 128, 1, 2};
+    if (rows > 64 && group <= 128) {
+        const int block = 2 * (128 / group) * group;
+        return d == 64 ? PagedPlan{true, block, 256, 128, 1, TilesCut<64>::kBoth, 5}
+                       : PagedPlan{true, block, 256, 128, 1, TilesCut<128>::kBoth, 2};
+    }
     const int rb = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    return {false, rb, rb, kTile, 2, 2};
+    return {false, rb, rb, kTile, 2, RowsCut::kBoth, 2};
 }
 
 template <int D, int RT, bool BF16>
@@ -263,7 +267,7 @@ int launch_pass(const PagedPass &a, cudaStream_t stream) {
 // the ratio of two passes counts.  (Shared prefix of 16500 tokens for 256 sequences of
 // 16 to 1024 own ones, 64 query heads: 202 us with the SMs split so, 228 one after the other.)
 int step_ns(const PagedPlan &pl, int d) {
-    if (pl.tiles) return d == 128 ? 1900 : 1400;
+    if (pl.tiles) return (d == 128 ? 1900 : 1400) / pl.tile_steps;
     const int ns = pl.block_rows == 16 ? 420 : (pl.block_rows == 32 ? 800 : 1150);
     return d == 128 ? ns : ns * 5 / 6;
 }
@@ -320,9 +324,10 @@ PagedPass make_pass(const PagedLaunch &a, const DeviceInfo &dev, void *scratch) 
     p.causal = a.causal;
     p.scale_log2 = a.scale * kLog2e;
     p.out_dtype = a.out_dtype;
-    const PagedPlan pl = x.plan = plan_paged(a.max_q, p.G);
+    const PagedPlan pl = x.plan = plan_paged(a.max_q, p.G, a.c.head_dim);
     p.block_rows = pl.block_rows;
     p.unit_steps = pl.unit_steps;
+    p.tile_tokens = pl.tiles ? pl.block_rows / p.G / 2 : 0;
     const int most = pl.per_sm * dev.num_sms;
     const size_t slots = static_cast<size_t>(most) * 2, rec = slots * pl.slot_rows;
     p.part_o = static_cast<float *>(scratch);
@@ -339,7 +344,7 @@ PagedPass make_pass(const PagedLaunch &a, const DeviceInfo &dev, void *scratch) 
 }  // namespace
 
 size_t paged_scratch_bytes(int max_q, int group, int d, int num_sms) {
-    return pass_bytes(plan_paged(max_q, group), d, num_sms);
+    return pass_bytes(plan_paged(max_q, group, d), d, num_sms);
 }
 
 bool paged_needs_scratch(const PagedLaunch &a, const DeviceInfo &dev) {
@@ -360,7 +365,7 @@ size_t paged_pair_scratch_bytes(int B, int Hq, int Hkv, int d, int num_sms) {
     const size_t rows = static_cast<size_t>(B) * Hq;
     size_t total = 0;
     for (int i = 0; i < 2; ++i) {
-        const PagedPlan pl = plan_paged(i ? 1 : B, Hq / Hkv);
+        const PagedPlan pl = plan_paged(i ? 1 : B, Hq / Hkv, d);
         const size_t per = static_cast<size_t>(i ? 1 : B) * (Hq / Hkv);
         const size_t units = static_cast<size_t>(i ? B : 1) * Hkv * ((per + pl.block_rows - 1) / pl.block_rows);
         total += align256(pass_bytes(pl, d, num_sms)) + align256(rows * d * 4) + align256(rows * 8) +
@@ -408,6 +413,7 @@ int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scra
         p.peer_max_len = o.p.max_len;
         p.peer_blocks = o.blocks;
         p.peer_tile = o.plan.tile;
+        p.peer_tile_steps = o.plan.tile_steps;
         p.peer_unit_steps = o.plan.unit_steps;
         p.peer_step_ns = o.p.step_ns;
     }

@@ -90,8 +90,7 @@ __device__ __forceinline__ bool has_tail(const PagedPiece &u) { return u.j1 * kK
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const PagedParams p, const int tile_tokens,
-                       const int scale_neg) {
+                       const __grid_constant__ CUtensorMap map_v, const PagedParams p, const int scale_neg) {
     using L = TilesLayout<D>;
     constexpr float kShift = BF16 ? 0.f : 7.f;  // fp16 weights: as in paged_rows_kernel
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -107,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return reinterpret_cast<PagedPiece *>(smem + L::kPieceOff + (i & 1) * (((int)sizeof(PagedPiece) + 7) / 8 * 8));
     };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile_rows = tile_tokens * p.G;
+    const int tile_tokens = p.tile_tokens, tile_rows = tile_tokens * p.G;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     paged_enter(p);
-    paged_plan<kKeys, kThreads>(p, *start, warp_sum, &g_tiles_status);
+    paged_plan<TilesCut<D>, kThreads>(p, *start, warp_sum, &g_tiles_status);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     uint32_t pieces = 0;  // handed over / taken so far
@@ -172,18 +171,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int box = min(page, kKeys), boxes = kKeys / box;
         // lane -> (half of a group: V_j or K_j+1, slab, page) of its copies: up to 2 x 2 x 8
         const int my_box = lane % boxes, my_slab = lane / boxes % L::kSlabs, my_half = lane / boxes / L::kSlabs;
-        PagedCursor<kKeys> cur;
+        PagedCursor<TilesCut<D>> cur;
         if (lane == 0) paged_note_none(p);
         cur.begin(p, *start);
         PagedPiece u = {};
-        int unit_tiles = 0;
+        int to_last = 0;
         bool any = false;
         while (ok) {
-            const bool more = cur.next(p, u, unit_tiles);
+            const bool more = cur.next(p, u, to_last);
             if (more) {
-                if (lane == 0) paged_note_unit(p, u, unit_tiles, *start);
+                if (lane == 0) paged_note_unit(p, u, to_last, *start);
             } else {
-                if (lane == 0 && any && u.kind == 1) paged_note_open(p, u, unit_tiles, *start);
+                if (lane == 0 && any && u.kind == 1) paged_note_open(p, u, to_last, *start);
                 u.kind = -1;
             }
             any = true;
@@ -567,7 +566,6 @@ int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
     PagedParams p = a.p;
     using L = TilesLayout<D>;
     static_assert(L::kSmemBytes <= 227 * 1024, "shared memory budget");
-    const int tile_tokens = kM / p.G;
     CUtensorMap mq, mk, mv;
     int rc;
     // queries [token][head][d], a box of the G heads of a kv head and tile_tokens tokens
@@ -575,7 +573,7 @@ int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
     if (!enc) return cuda_fail(cudaErrorNotSupported);
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.total_q};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * p.Hq};
-    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tile_tokens};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.tile_tokens};
     const cuuint32_t estr[3] = {1, 1, 1};
     if (enc(&mq, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t *>(p.q),
             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -590,7 +588,7 @@ int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, a.device, ready)) != FA_OK) return rc;
     PagedConfig cfg(a.grid, kThreads, L::kSmemBytes, a.early, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, tile_tokens, p.scale_log2 < 0.f ? 1 : 0);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, p.scale_log2 < 0.f ? 1 : 0);
     if (e != cudaSuccess) return cuda_fail(e);
     return a.join ? launch_join<D, 2 * kM>(a, stream) : FA_OK;
 }

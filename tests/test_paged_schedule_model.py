@@ -25,6 +25,42 @@ def units_of(seqs, Hkv, G, rows, TK, causal):
             for rb in range(-(-s[0] * G // rows))]
 
 
+def both_of(seq, rb, rows, G, causal, tiles):
+    """Key tiles of 128 that both query tiles of a block visit."""
+    if rb * rows + rows // 2 >= seq[0] * G:
+        return 0
+    return min(tiles, tiles_of(seq, 2 * rb, rows // 2, G, 128, causal))
+
+
+def weighted_pieces_of(units, unit_steps, both_steps, one_steps, grid):
+    """pieces_of for units (sequence, head, block, tiles, both) whose key tiles cost both_steps for both query
+    tiles (they come first) and one_steps for one: a range has the tiles that start in it."""
+    def start(t, both, j):
+        return unit_steps + min(j, both) * both_steps + max(0, j - both) * one_steps
+
+    def starts_before(t, both, v):
+        return sum(start(t, both, j) < v for j in range(t))
+
+    W = sum(start(t, both, t) for *_, t, both in units)
+    G = min(grid, max(W // both_steps, 1))
+    ranges = [(c * W // G, (c + 1) * W // G) if c < G else (W, W) for c in range(grid)]
+    out = [([], None) for _ in range(grid)]
+    at = 0
+    for i, (*_, t, both) in enumerate(units):
+        cost = start(t, both, t)
+        for c, (first, end) in enumerate(ranges):
+            lo, hi = max(first, at), min(end, at + cost)
+            if lo < hi:
+                j0, j1 = starts_before(t, both, lo - at), starts_before(t, both, hi - at)
+                if j1 > j0:
+                    kind = 2 if j0 > 0 else (1 if j1 < t else 0)
+                    out[c][0].append((i, j0, j1, kind))
+                    if kind == 1:
+                        out[c] = (out[c][0], cta_of(end + start(t, both, t - 1) - (hi - at), W, G))
+        at += cost
+    return out
+
+
 def cta_of(step, W, G):
     c = min(((step + 1) * G - 1) // W, G - 1)
     while c > 0 and c * W // G > step:
@@ -69,6 +105,27 @@ def test_every_tile_once_and_every_note_right(seed):
     units = units_of(seqs, Hkv, G, rows, TK, rng.random() < 0.6)
     grid = rng.choice([1, 2, 7, 152, 304])
     cut = pieces_of(units, rng.choice([0, 1, 2, 3]), grid)
+    check_cut(units, cut)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_every_tile_once_when_tiles_cost_more_or_less(seed):
+    rng = random.Random(2000 + seed)
+    Hkv, G = rng.choice([1, 2, 4]), rng.choice([1, 2, 3, 7, 16, 65, 100, 128])
+    rows, causal = 2 * (128 // G) * G, rng.random() < 0.7
+    seqs = [(rng.choice([0, 1, rng.randint(1, 300), rng.randint(1, 1200)]) // max(1, G // 16), rng.choice([0, 1, rng.randint(1, 3000)]))
+            for _ in range(rng.randint(1, 6))]
+    units = [(b, hk, rb, t, both_of(seqs[b], rb, rows, G, causal, t))
+             for b, hk, rb, t in units_of(seqs, Hkv, G, rows, 128, causal)]
+    both_steps, one_steps, unit_steps = rng.choice([(3, 2, 5), (3, 2, 5), (1, 1, 2), (4, 1, 0), (5, 5, 7)])
+    grid = rng.choice([1, 2, 7, 40, 152])
+    cut = weighted_pieces_of(units, unit_steps, both_steps, one_steps, grid)
+    check_cut([u[:4] for u in units], cut)
+    if (both_steps, one_steps) == (1, 1):
+        assert cut == pieces_of([u[:4] for u in units], unit_steps, grid)
+
+
+def check_cut(units, cut):
     done = {}
     for c, (pieces, closes) in enumerate(cut):
         for n, (i, j0, j1, kind) in enumerate(pieces):
