@@ -413,6 +413,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2_from(float m, float M) { return m == -INFINITY ? 0.f : ex2_approx(m - M); }
 
+// Whether a row has seen a key, by its sum, to which the key whose score is m added 1 or more.
+// (m does not tell: a maximum passes NaN over, so a row of NaN scores has m = -inf like one without
+// keys.  Its l is NaN, as is that of a row with a score of +inf, and has to reach the output.)
+__device__ __forceinline__ bool saw_key(float l) { return l != 0.f; }
+
 // N consecutive columns of a finished row at element offset `off`.
 template <int N>
 __device__ __forceinline__ void paged_store(const PagedParams &p, long long off, const float (&v)[N]) {
@@ -435,10 +440,10 @@ __device__ __forceinline__ void paged_store(const PagedParams &p, long long off,
 template <int N>
 __device__ __forceinline__ void paged_finish(const PagedParams &p, int D, long long row, int col, float (&acc)[N],
                                              float m, float l) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = saw_key(l) ? 1.f / l : 0.f;
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] *= inv;
-    if (p.lse && col == 0) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && col == 0) p.lse[row] = saw_key(l) ? (m + __log2f(l)) * kLn2 : -INFINITY;
     paged_store<N>(p, row * D + col, acc);
 }
 
@@ -530,7 +535,7 @@ __device__ __forceinline__ void paged_add_pieces(int n, int rows, int lane, MlAt
 #pragma unroll
             for (int i = 0; i < F; ++i) {
                 const float w = ex2_from(mi[i], next), li = __shfl_sync(0xffffffffu, ml.y, i * R + r);
-                if (w > 0.f) {  // 0: the row saw no key in this piece, whose columns may be unwritten
+                if (saw_key(li)) {  // else the piece's columns may be unwritten
                     const float *xv = reinterpret_cast<const float *>(&x[r][i]);
                     L[r] = fmaf(w, li, L[r]);
 #pragma unroll
@@ -581,12 +586,12 @@ __device__ __forceinline__ void paged_join_few(const PagedParams &p, int c, cons
         for (int k = 0; k < F; ++k) M = fmaxf(M, ml[r][k].x);
 #pragma unroll
         for (int k = 0; k < F; ++k) {
-            const float w = k < n ? ex2_from(ml[r][k].x, M) : 0.f;
+            const float w = ex2_from(ml[r][k].x, M);
             const float *xv = reinterpret_cast<const float *>(&x[r][k]);
-            L = fmaf(w, ml[r][k].y, L);
+            const bool adds = k < n && saw_key(ml[r][k].y);  // else the piece's columns may be unwritten
+            L += adds ? w * ml[r][k].y : 0.f;
 #pragma unroll
-            for (int e = 0; e < N; ++e)  // no weight: the row saw no key in this piece, whose columns may be unwritten
-                acc[e] += w > 0.f ? w * xv[e] : 0.f;
+            for (int e = 0; e < N; ++e) acc[e] += adds ? w * xv[e] : 0.f;
         }
         paged_finish<N>(p, D, paged_noted_row(p, a, r0 + r), lane * N, acc, M, L);
     }

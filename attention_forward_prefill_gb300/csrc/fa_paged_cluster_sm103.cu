@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {
-            const float w = ex2_from(ml[k].x, M);
-            if (w > 0.f) {  // 0: no key seen, the columns may be unwritten
+            if (saw_key(ml[k].y)) {  // else the columns may be unwritten
+                const float w = ex2_from(ml[k].x, M);
                 sum = fmaf(w, ml[k].y, sum);
                 acc[0] = fmaf(w, v[k].x, acc[0]);
                 acc[1] = fmaf(w, v[k].y, acc[1]);

@@ -465,12 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const float m = m_ref - kShift;  // (-inf stays)
-            const float inv = keep ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+            const float inv = keep ? 1.f : (saw_key(l) ? 1.f / l : 0.f);
             if (row_ok) {
                 if (keep)
                     *reinterpret_cast<float2 *>((u.kind == 0 ? p.dense_ml : p.part_ml) + rec * 2) = make_float2(m, l);
                 else if (p.lse)
-                    p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                    p.lse[row] = saw_key(l) ? (m + __log2f(l)) * kLn2 : -INFINITY;
             }
             // A lane holds a row, and a row's neighbours in memory are its columns: 32 rows x 32
             // words at a time turn in shared memory, so that eight lanes write a row's 128 bytes.

@@ -436,6 +436,9 @@ size_t fa_decode_noalloc_max_bytes(void);
  *   lengths : device int32, clamped to [0, max_pages * page_size] and recorded
  *     as FA_ERR_SEQ_LEN when they were outside.
  * Slots behind a sequence's last token may hold anything, NaN included.
+ * A row with a score of NaN or +inf comes out NaN, its log-sum-exp too, as the
+ * softmax of such scores is; one whose scores are all -inf counts as a row
+ * without keys.
  */
 typedef struct {
     void *k_pages, *v_pages;
