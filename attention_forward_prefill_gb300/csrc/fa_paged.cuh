@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "fa_internal.h"
+#include "fa_status.cuh"
 #include "fa_tiles.cuh"
 #include "sm103_ptx.cuh"
 
@@ -226,7 +227,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
         mine += paged_head_steps<C>(p, paged_seq(p, b)) * p.Hkv;
         bad |= paged_seq_bad(p, b);
     }
-    if (bad && blockIdx.x == 0) atomicCAS(status, 0, static_cast<int>(FA_ERR_SEQ_LEN));
+    if (bad && blockIdx.x == 0) record_status(status, FA_ERR_SEQ_LEN);
     long long incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {

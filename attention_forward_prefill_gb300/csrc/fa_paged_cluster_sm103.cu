@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     if (p.pre_lens) prefix = min(max(__ldg(p.pre_lens), 0), p.pre_max_len);
     if (threadIdx.x == 0 && rank == 0 && u.hk == 0 && u.row0 == 0 &&
         (paged_seq_bad(p, u.b) || (p.pre_lens && __ldg(p.pre_lens) != prefix)))
-        atomicCAS(&g_cluster_status, 0, static_cast<int>(FA_ERR_SEQ_LEN));
+        record_status(&g_cluster_status, FA_ERR_SEQ_LEN);
     const int rows = min(RB, u.nq * p.G - u.row0);
     if (rows <= 0) return;  // (the whole cluster)
     // key tiles: the prefix's, then the sequence's own that the rows can see
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             __syncwarp();
             if (live) {
                 if (id < 0 || id >= p.num_pages) {
-                    atomicCAS(&g_cluster_status, 0, static_cast<int>(FA_ERR_PAGE));
+                    record_status(&g_cluster_status, FA_ERR_PAGE);
                     id = p.num_pages;  // outside the tensor: the copy writes zeros
                 }
                 tma_load_4d(smem + st * L::kStage + my_op * R::kOperand + my_slab * R::kSlab + my_box * box * 128,
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         if (j1 > j0) mbar_wait(q_full, 0, &dummy, kDrainNs);
         for (uint32_t i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
             mbar_wait(full + i % L::kStages, (i / L::kStages) & 1, &dummy, kDrainNs);
-        atomicCAS(&g_cluster_status, 0, static_cast<int>(FA_ERR_WATCHDOG));
+        record_status(&g_cluster_status, FA_ERR_WATCHDOG);
     }
     __syncwarp();
     cluster_sync();  // nobody leaves while its rows are read

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                 __syncwarp();
                 if (live) {
                     if (id < 0 || id >= p.num_pages) {
-                        atomicCAS(&g_paged_status, 0, static_cast<int>(FA_ERR_PAGE));
+                        record_status(&g_paged_status, FA_ERR_PAGE);
                         id = p.num_pages;  // outside the tensor: the copy writes zeros
                     }
                     tma_load_4d(smem + st * L::kStage + my_op * R::kOperand + my_slab * R::kSlab + my_box * box * 128,
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         if (units > 0) mbar_wait(u_full, (units - 1) & 1, &dummy, kDrainNs);
         for (uint32_t i = tiles > L::kStages ? tiles - L::kStages : 0; i < tiles; ++i)
             mbar_wait(full + i % L::kStages, (i / L::kStages) & 1, &dummy, kDrainNs);
-        atomicCAS(&g_paged_status, 0, static_cast<int>(FA_ERR_WATCHDOG));
+        record_status(&g_paged_status, FA_ERR_WATCHDOG);
     }
 }
 

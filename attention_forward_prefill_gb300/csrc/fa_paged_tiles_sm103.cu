@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (live) {
                     if (id < 0 || id >= p.num_pages) {
-                        atomicCAS(&g_tiles_status, 0, static_cast<int>(FA_ERR_PAGE));
+                        record_status(&g_tiles_status, FA_ERR_PAGE);
                         id = p.num_pages;  // outside the tensor: the copy writes zeros
                     }
                     // slot 2 st: V_j (or the first K); slot 2 st + 1: K_j+1
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (qc > 0) mbar_wait(q_full, (qc - 1) & 1, &dummy, kDrainNs);
         for (uint32_t i = gc > L::kGroups ? gc - L::kGroups : 0; i < gc; ++i)
             mbar_wait(kv_full + i % L::kGroups, (i / L::kGroups) & 1, &dummy, kDrainNs);
-        atomicCAS(&g_tiles_status, 0, static_cast<int>(FA_ERR_WATCHDOG));
+        record_status(&g_tiles_status, FA_ERR_WATCHDOG);
     }
     if (warp == kMmaWarp) {
         tc_fence_after();
