@@ -33,6 +33,7 @@
 #include <cuda_fp16.h>
 
 #include "fa_internal.h"
+#include "fa_status.cuh"
 #include "fa_tiles.cuh"
 #include "sm103_ptx.cuh"
 
@@ -205,7 +206,7 @@ __device__ __forceinline__ void check_seq(const Params &p, const Work &w) {
     const int k0 = __ldg(p.cu_k + w.b), k1 = __ldg(p.cu_k + w.b + 1);
     const bool bad = q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.Nq || k0 < 0 || k1 < k0 ||
                      k1 > p.total_k || k1 - k0 > p.Nk;
-    if (bad) atomicCAS(&g_prefill_status, 0, static_cast<int>(FA_ERR_SEQ_LEN));
+    if (bad) record_status(&g_prefill_status, FA_ERR_SEQ_LEN);
 }
 
 template <int SCHED>
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-    if (threadIdx.x == 0 && *abort_flag) atomicCAS(&g_prefill_status, 0, (int)FA_ERR_WATCHDOG);
+    if (threadIdx.x == 0 && *abort_flag) record_status(&g_prefill_status, FA_ERR_WATCHDOG);
 }
 
 // ---------------------------------------------------------------- stream-K fixup
@@ -963,7 +964,7 @@ __global__ void __launch_bounds__(64, 1) watchdog_selftest_kernel(long long limi
         result[2 + warp] = static_cast<long long>(t1 - t0);
     }
     __syncthreads();
-    if (threadIdx.x == 0 && *abort_flag) atomicCAS(&g_prefill_status, 0, (int)FA_ERR_WATCHDOG);
+    if (threadIdx.x == 0 && *abort_flag) record_status(&g_prefill_status, FA_ERR_WATCHDOG);
 }
 
 // ---------------------------------------------------------------- host side

@@ -42,11 +42,11 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # digits of the sha256 of the listed source files, in order.
 NCU_TRAFFIC = {
     # one prefill_kernel<128> launch of each of the step's problems (B=1, H=16,
-    # d=128, bf16): --set full at N=8192, the two DRAM counters alone at 4096 and
-    # 16384 (one pass each, on the full-size problem).
+    # d=128, bf16): the two DRAM counters alone (one pass each, on the full-size
+    # problem).
     "prefill": {"src": ["fa_prefill_sm103.cu", "fa_tiles.cuh", "sm103_ptx.cuh"],
-                "src_sha": "e952fd9eb477dd27",
-                "bytes_per_launch": {"4096": 50.46e6, "8192": 114.69e6, "16384": 253.71e6}},
+                "src_sha": "e5e3c4e06c5d754f",
+                "bytes_per_launch": {"4096": 50.45e6, "8192": 114.96e6, "16384": 253.82e6}},
     # one decode_split_kernel<64> launch of the step's decode problem (B=32, H=14)
     "decode": {"src": ["fa_decode_sm103.cu", "sm103_ptx.cuh"], "src_sha": "9066595177c6f87f",
                "bytes_per_launch": 263.58e6},

@@ -23,12 +23,12 @@ def records(text):
 def test_a_watchdog_report_is_never_the_second_of_two_compare_and_swaps():
     seen = 0
     for name, text in sources():
-        if not name.startswith("fa_paged"):
+        if not name.startswith(("fa_paged", "fa_prefill")):
             continue
         for how, status in records(text):
             seen += 1
             assert status != "FA_ERR_WATCHDOG" or how != "atomicCAS", name
-    assert seen >= 8
+    assert seen >= 11
 
 
 HARNESS = """
