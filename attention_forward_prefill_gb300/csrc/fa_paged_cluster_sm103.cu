@@ -45,7 +45,9 @@ struct ClusterLayout {
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
+// (.aligned: all lanes of a warp at once, whatever branch they come from)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, int rank) {
@@ -204,7 +206,6 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                     if (col == 0) out_ml[row] = make_float2(m, l);
                 });
         }
-        __syncwarp();
     }
 
     cluster_sync();
@@ -244,7 +245,6 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             mbar_wait(full + i % L::kStages, (i / L::kStages) & 1, &dummy, kDrainNs);
         record_status(&g_cluster_status, FA_ERR_WATCHDOG);
     }
-    __syncwarp();
     cluster_sync();  // nobody leaves while its rows are read
 }
 
