@@ -192,9 +192,13 @@ __device__ __forceinline__ long long paged_head_steps(const PagedParams &p, cons
 // early behind it may read what was complete before it.  The second of two passes
 // over the same rows is the exception: it reads nothing that the first one writes,
 // and the first one has been through here.
-__device__ __forceinline__ void paged_enter(const PagedParams &p) {
+__device__ __forceinline__ void paged_wait(const PagedParams &p) {
     if (!p.peer_lens || p.first) asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void paged_let_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void paged_enter(const PagedParams &p) {
+    paged_wait(p);
+    paged_let_go();
 }
 
 // Whoever waits for the second of two passes also waits for the first: one CTA of it stays

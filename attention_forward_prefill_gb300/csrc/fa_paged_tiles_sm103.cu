@@ -128,17 +128,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
-        tmem_alloc(tmem_slot, kTmemCols);
-        tmem_relinquish();
-    }
     if (warp == kTmaWarp && lane == 0) {
         prefetch_tensormap(&map_q);
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
+    paged_wait(p);
+    if (warp == kMmaWarp) {
+        // behind the wait and before followers start: a kernel ahead of this one, or this one, may
+        // still need columns that a kernel which waits for it would hold
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+        paged_let_go();
+    }
     tc_fence_before();
-    paged_enter(p);
     paged_plan<TilesCut<D>, kThreads>(p, *start, warp_sum, &g_tiles_status);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;

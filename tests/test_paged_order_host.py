@@ -18,3 +18,13 @@ def test_aligned_cluster_barriers_see_whole_warps():
     assert helper.group(1).lstrip().startswith("__syncwarp();")
     outside = text[:helper.start()] + text[helper.end():]
     assert "barrier.cluster" not in outside and outside.count("cluster_sync();") == 2
+
+
+def test_tensor_memory_is_taken_behind_the_wait_and_before_followers_start():
+    """A kernel that takes columns and then waits for one that still needs some would wait forever, and so would this
+    one if what follows it took them first."""
+    text = source("fa_paged_tiles_sm103.cu")
+    order = [text.index(x) for x in ("paged_wait(p);", "tmem_alloc(", "paged_let_go();", "paged_plan<")]
+    assert order == sorted(order)
+    assert "paged_enter" not in text and "launch_dependents" not in text and text.count("paged_let_go();") == 1
+    assert text.count("tmem_alloc(") == 1
