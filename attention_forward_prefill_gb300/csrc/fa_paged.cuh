@@ -1,21 +1,5 @@
-// fa_paged.cuh -- what the paged-attention kernels share: the launch
-// parameters, the cut of the work into equal ranges of key tiles, and the
-// writing and joining of rows.
-//
-// Work.  The cache keeps K and V as [page][kv head][slot][d]; sequence b's
-// token j lives in page page_table[b][j / page_size], slot j % page_size.  A
-// sequence with nq query tokens gives each kv head nq * G query rows
-// (G = query heads per kv head), row r = (token r / G, head r % G), cut into
-// blocks of block_rows.  A unit = (sequence, kv head, row block); it costs
-// unit_steps for its own start and end and a step per key tile its rows can see,
-// or a few (PagedCut; at least one tile, so that a unit without keys still writes its rows).  The W
-// steps of the whole call, in the order (sequence, kv head, block), are cut
-// into gridDim.x equal ranges, one per CTA, whatever the lengths are: they live
-// on the device, so the cut is made there, by every CTA for itself (1 to 2 us,
-// under the launch of what comes before).  A unit inside one range is written
-// directly; the pieces of a unit that ranges cut keep (O, m, l) in fp32 and
-// paged_join_kernel adds them in a fixed order, so a given shape and set of
-// lengths gives the same bits on every run.
+// fa_paged.cuh -- what the paged-attention kernels share: a CTA's walk through
+// its range of the work (fa_paged_cut.cuh), and the writing and joining of rows.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,6 +9,7 @@
 #include <cstdint>
 
 #include "fa_internal.h"
+#include "fa_paged_cut.cuh"
 #include "fa_status.cuh"
 #include "fa_tiles.cuh"
 #include "sm103_ptx.cuh"
@@ -41,149 +26,11 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
-struct PagedParams {
-    const uint16_t *q;     // [total_q][Hq][D]
-    void *out;             // [total_q][Hq][D]
-    float *lse;            // optional [total_q][Hq]: natural-log row log-sum-exp, -inf for a row without keys
-    const int *page_table;  // [B][max_pages]
-    const int *seq_lens;    // [B] keys of each sequence
-    const int *cu_q;        // [B + 1] query token offsets, or null: nq_each tokens per sequence
-    int nq_each;
-    int B, Hq, Hkv, G;
-    int total_q, max_q;
-    int max_pages, max_len;
-    int num_pages, page_shift;
-    int block_rows;         // query rows of a unit
-    int unit_steps;         // what a unit costs besides its key tiles, in steps
-    int tile_tokens;        // paged_tiles_kernel: tokens of a query tile, of which a block has two
-    int causal;             // query token i of nq sees keys j <= len - nq + i
-    float scale_log2;       // scale * log2(e)
-    int out_dtype;
-    // paged_cluster_kernel alone: keys that every sequence has in front of its own
-    const int *pre_table, *pre_lens;
-    int pre_max_len;
-    float *part_o;          // [gridDim.x][2][RB][D], RB >= block_rows the kernel's slot size
-    float *part_ml;         // [gridDim.x][2][RB][2]: m (log2 units), l
-    int4 *open;             // [gridDim.x][2]: the unit a CTA leaves unfinished
-    // One of two passes over the same query rows, each over keys of its own (a shared
-    // prefix, then the sequences'), that paged_pair_join_kernel joins: whole units'
-    // rows go to dense_* as pieces do, and unit_note says where a unit's pieces are.
-    float *dense_o, *dense_ml;  // [total_q][Hq][D] and [total_q][Hq][2], or null: rows go to out
-    int2 *unit_note;            // [B][Hkv][row blocks]: the CTA that opened the unit, its pieces (1: dense)
-    // Such a pass also leaves SMs to the other one, in proportion to their work.
-    const int *peer_lens;       // the other pass's seq_lens
-    int peer_B, peer_max_len, peer_blocks, peer_tile, peer_tile_steps, peer_unit_steps;
-    int step_ns, peer_step_ns;  // SM time of a step of this pass, and of the other
-    int num_sms, per_sm, first; // first: the pass that is launched first
-};
-
 // Bounded wait in which every lane polls the barrier itself, so that every lane's
 // loads come after the phase it waited for (one lane's wait and a shuffle order
 // nothing for the loads of the other lanes).
 __device__ __forceinline__ bool lanes_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWatchdogNs));
-}
-
-struct SeqView {
-    int t0, nq, len;
-};
-
-__device__ __forceinline__ SeqView paged_seq(const PagedParams &p, int b) {
-    SeqView s;
-    const int raw = __ldg(p.seq_lens + b);
-    s.len = min(max(raw, 0), p.max_len);
-    if (p.cu_q) {
-        s.t0 = min(max(__ldg(p.cu_q + b), 0), p.total_q);
-        s.nq = min(min(max(__ldg(p.cu_q + b + 1), s.t0), p.total_q) - s.t0, p.max_q);
-    } else {
-        s.t0 = b * p.nq_each;
-        s.nq = p.nq_each;
-    }
-    return s;
-}
-
-// Whether paged_seq had to clamp sequence b's length or offsets.
-__device__ __forceinline__ bool paged_seq_bad(const PagedParams &p, int b) {
-    const int raw = __ldg(p.seq_lens + b);
-    bool bad = raw < 0 || raw > p.max_len;
-    if (p.cu_q) {
-        const int lo = __ldg(p.cu_q + b), hi = __ldg(p.cu_q + b + 1);
-        bad |= lo < 0 || hi < lo || hi > p.total_q || hi - lo > p.max_q;
-    }
-    return bad;
-}
-
-// Key tiles (TK keys each) that rows up to last_row of a sequence must visit:
-// at least one.
-template <int TK>
-__device__ __forceinline__ int paged_tiles_to_row(const PagedParams &p, const SeqView &s, int last_row) {
-    int seen = s.len;
-    if (p.causal) seen = max(0, s.len - s.nq + min(s.nq - 1, last_row / p.G) + 1);
-    return max(1, (seen + TK - 1) / TK);
-}
-
-__device__ __forceinline__ int paged_blocks(const PagedParams &p, const SeqView &s) {
-    return (s.nq * p.G + p.block_rows - 1) / p.block_rows;
-}
-
-// How a kernel's work is cut: keys of a tile, and what a key tile costs in steps.  Of
-// paged_tiles_kernel's two query tiles (KEYS = 128) a causal or short block has key tiles
-// that one alone visits, ONE steps against BOTH.
-template <int KEYS, int BOTH, int ONE>
-struct PagedCut {
-    static constexpr int kKeys = KEYS, kBoth = BOTH, kOne = ONE;
-};
-
-using RowsCut = PagedCut<64, 1, 1>;
-// (Per CTA of 4 chunks of 700 to 2048 tokens at d = 128 and 3 prompts of 3500 to 5000 at d = 64,
-// fitted: a key tile 1.80 us for both and 1.60 for one, and 1.60 and 1.10; a piece 2.64 and 2.39.)
-template <int D>
-using TilesCut = PagedCut<128, D == 64 ? 3 : 1, D == 64 ? 2 : 1>;
-
-// What row block rb costs, in steps: its unit_steps, then its key tiles in order, those
-// that both query tiles visit first.
-template <typename C>
-struct UnitSteps {
-    int tiles, both;  // key tiles, and those for both query tiles
-    int total;
-
-    __device__ __forceinline__ UnitSteps(const PagedParams &p, const SeqView &s, int rb) {
-        if constexpr (C::kKeys == 128) {
-            // (no division by G: the plan goes through all blocks of a causal sequence, and with
-            // two divisions each its CTAs started 5 us later for 32 blocks)
-            const int tok1 = (2 * rb + 1) * p.tile_tokens;  // the second query tile's first token
-            const int past = s.len - s.nq;
-            auto tiles_to = [&](int tok) {  // that tokens before tok visit: at least one
-                return max(1, ((p.causal ? max(0, past + min(s.nq, tok)) : s.len) + C::kKeys - 1) / C::kKeys);
-            };
-            tiles = tiles_to(tok1 + p.tile_tokens);
-            both = C::kBoth == C::kOne ? tiles : (tok1 < s.nq ? tiles_to(tok1) : 0);
-        } else {
-            tiles = both = paged_tiles_to_row<C::kKeys>(p, s, rb * p.block_rows + p.block_rows - 1);
-        }
-        total = before(p, tiles);
-    }
-    // Steps before key tile j.
-    __device__ __forceinline__ int before(const PagedParams &p, int j) const {
-        return p.unit_steps + j * C::kOne + min(j, both) * (C::kBoth - C::kOne);
-    }
-    // Key tiles that start before step v: a range has those that start in it.
-    __device__ __forceinline__ int tiles_before(const PagedParams &p, int v) const {
-        const int e = max(0, v - p.unit_steps), b = both * C::kBoth;
-        return e <= b ? (e + C::kBoth - 1) / C::kBoth : min(tiles, both + (e - b + C::kOne - 1) / C::kOne);
-    }
-};
-
-// Steps of one kv head of a sequence.
-template <typename C>
-__device__ __forceinline__ long long paged_head_steps(const PagedParams &p, const SeqView &s) {
-    const int n = paged_blocks(p, s);
-    if (n == 0) return 0;
-    long long sum = UnitSteps<C>(p, s, n - 1).total;
-    if (n == 1) return sum;
-    if (!p.causal) return sum + static_cast<long long>(n - 1) * UnitSteps<C>(p, s, 0).total;
-    for (int rb = 0; rb < n - 1; ++rb) sum += UnitSteps<C>(p, s, rb).total;
-    return sum;
 }
 
 // Every paged kernel may be launched while the kernels ahead of it in the stream
@@ -251,8 +98,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
     if (p.peer_lens) {  // SMs in proportion to the two passes' work, at least one each
         long long theirs = 0;
         for (int b = tid; b < p.peer_B; b += NT) {
-            const int len = min(max(__ldg(p.peer_lens + b), 0), p.peer_max_len);
-            theirs += max(1, (len + p.peer_tile - 1) / p.peer_tile) * p.peer_tile_steps + p.peer_unit_steps;
+            theirs += paged_peer_steps(p, b);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) theirs += __shfl_xor_sync(0xffffffffu, theirs, off);
@@ -262,10 +108,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams &p, PagedStart &st,
         theirs = 0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) theirs += warp_sum[w];
-        const long long mine_ns = W * p.step_ns, their_ns = theirs * p.peer_blocks * p.Hkv * p.peer_step_ns;
-        const long long first_ns = p.first ? mine_ns : their_ns;
-        const int first_sms = static_cast<int>(min(max(p.num_sms * first_ns / (mine_ns + their_ns), 1LL),
-                                                   static_cast<long long>(max(p.num_sms - 1, 1))));
+        const int first_sms = paged_first_sms(p, W, theirs * p.Hkv);
         most = min(most, p.per_sm * (p.first ? first_sms : max(p.num_sms - first_sms, 1)));
     }
     const int c = blockIdx.x;
@@ -826,17 +669,6 @@ inline int make_page_map(CUtensorMap *map, const void *base, const fa_paged_cach
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
     return FA_OK;
 }
-
-// How a call runs, from its sizes alone.
-struct PagedPlan {
-    bool tiles;      // 128-row tensor-memory tiles (paged_tiles_kernel), else paged_rows_kernel
-    int block_rows;  // query rows of a unit
-    int slot_rows;   // rows of a partial slot
-    int tile;        // keys of a tile
-    int per_sm;      // CTAs per SM
-    int tile_steps;  // what a key tile costs, in steps (PagedCut: of both query tiles)
-    int unit_steps;  // what a unit costs besides its key tiles
-};
 
 // One launch of a main kernel, with its join or without.
 struct PagedPass {

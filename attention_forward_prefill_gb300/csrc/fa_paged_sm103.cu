@@ -219,18 +219,6 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     }
 }
 
-// How a call runs, from its sizes alone.
-PagedPlan plan_paged(int max_q, int group, int d) {
-    const long long rows = static_cast<long long>(max_q) * group;
-    if (rows > 64 && group <= 128) {
-        const int block = 2 * (128 / group) * group;
-        return d == 64 ? PagedPlan{true, block, 256, 128, 1, TilesCut<64>::kBoth, 5}
-                       : PagedPlan{true, block, 256, 128, 1, TilesCut<128>::kBoth, 2};
-    }
-    const int rb = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    return {false, rb, rb, kTile, 2, RowsCut::kBoth, 2};
-}
-
 template <int D, int RT, bool BF16>
 int launch_rows(const PagedPass &a, cudaStream_t stream) {
     using L = PagedLayout<D, RT>;
@@ -261,15 +249,6 @@ int launch_pass(const PagedPass &a, cudaStream_t stream) {
     const bool bf16 = a.c.dtype == FA_BF16;
     if (a.c.head_dim == 64) return bf16 ? launch_rows_d<64, true>(a, stream) : launch_rows_d<64, false>(a, stream);
     return bf16 ? launch_rows_d<128, true>(a, stream) : launch_rows_d<128, false>(a, stream);
-}
-
-// What a step of a pass costs an SM, in ns, measured on runs confined to a few SMs; only
-// the ratio of two passes counts.  (Shared prefix of 16500 tokens for 256 sequences of
-// 16 to 1024 own ones, 64 query heads: 202 us with the SMs split so, 228 one after the other.)
-int step_ns(const PagedPlan &pl, int d) {
-    if (pl.tiles) return (d == 128 ? 1900 : 1400) / pl.tile_steps;
-    const int ns = pl.block_rows == 16 ? 420 : (pl.block_rows == 32 ? 800 : 1150);
-    return d == 128 ? ns : ns * 5 / 6;
 }
 
 // CTAs per cluster for calls that paged_cluster_kernel serves best, or 0.  Against the
@@ -403,20 +382,9 @@ int launch_paged_pair(const PagedLaunch &pre, const PagedLaunch &own, void *scra
         x.p.first = i == 0;
         x.p.num_sms = dev.num_sms;
         x.p.per_sm = x.plan.per_sm;
-        x.p.step_ns = step_ns(x.plan, d);
+        x.p.step_ns = paged_step_ns(x.plan, d);
     }
-    for (int i = 0; i < 2; ++i) {
-        const PagedPass &o = pass[1 - i];
-        PagedParams &p = pass[i].p;
-        p.peer_lens = o.p.seq_lens;
-        p.peer_B = o.p.B;
-        p.peer_max_len = o.p.max_len;
-        p.peer_blocks = o.blocks;
-        p.peer_tile = o.plan.tile;
-        p.peer_tile_steps = o.plan.tile_steps;
-        p.peer_unit_steps = o.plan.unit_steps;
-        p.peer_step_ns = o.p.step_ns;
-    }
+    for (int i = 0; i < 2; ++i) paged_set_peer(pass[i].p, pass[1 - i].p, pass[1 - i].plan);
     int rc;
     for (const PagedPass &x : pass)
         if ((rc = launch_pass(x, stream)) != FA_OK) return rc;
