@@ -769,7 +769,9 @@ def decode_paged(q, k_pages, v_pages, page_table, seq_lens, scale: float | None 
     """One query token per sequence over the first seq_lens[b] tokens of its pages.
 
     q [B, Hq, d] or [B, Hq, 1, d]; k_pages, v_pages [pages, Hkv, slots, d], any strides;
-    page_table int32 [B, max_pages]; seq_lens int32 [B].  Returns rows shaped as q.
+    page_table int32 [B, max_pages]; seq_lens int32 [B].  Returns rows shaped as q.  The table's
+    width bounds the lengths that the call is laid out for: a short call is some 5 us faster with
+    one no wider than it needs.
     """
     if out_dtype is None and workspace is None:
         done = (_calls or _fast()).decode(q, k_pages, v_pages, page_table, seq_lens, scale, out)

@@ -10,7 +10,7 @@
 // graph), of which the launch and four loads that wait for one another (length, page
 // id, tile, the other CTAs' rows) are most.  The balance is only as good as the lengths
 // are alike, and a cluster has no more than eight CTAs, so launch_paged takes this
-// form by a rule on the sizes (cluster_size).
+// form only where no sequence can be long (paged_cluster_size).
 //
 // A shared prefix is read by every sequence's clusters in front of its own keys: at
 // these sizes its keys come from L2, and one kernel replaces three (four sequences

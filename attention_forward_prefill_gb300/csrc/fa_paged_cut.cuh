@@ -204,6 +204,37 @@ inline PagedPlan plan_paged(int max_q, int group, int d) {
     return {false, rb, rb, RowsCut::kKeys, 2, RowsCut::kBoth, RowsCut::kOne, 2};
 }
 
+// CTAs per cluster for a call of `units` units that paged_cluster_kernel serves best, or 0 for
+// the split form.  The sizes are bounds: lengths are known on the device only.
+//
+// A cluster's CTAs take their unit's key tiles one after another, and no other CTA helps them,
+// so that the longest sequence sets the time alone, where the split form shares it among all
+// SMs but costs a plan and a join (7 us more, and 12 to 17 us with a prefix, whose two passes
+// and join it replaces).  So the bound is on the tiles in a row, whatever the number of units, by
+// what one takes: at most 10 us, 12 with a prefix, which loses 3 us when one sequence has the
+// bound's length and gains 5 when none comes near it.  Measured on 32 units, one sequence of that
+// length among short ones, clusters against split: 16 rows of 128, 12 tiles in a row 12.8 us
+// against 12.6 and 16 tiles 15.4 against 13.3; 32 rows of 128, 4 tiles 11.8 against 14.5 and 8
+// tiles 16.6 against 15.1; 64 rows of 64, 8 tiles 12.5 against 12.2 and 10 tiles 14.3 against
+// 12.4.  All of that length: 18.2 against 22.6, 25.5 against 26.3, 12.9 against 18.3, 17.9 against
+// 24.2, 15.8 against 20.5, 18.2 against 22.8.  None: 4 sequences of 1000 tokens, 8 kv heads of
+// 128, in tables of 8192, 7.0 against 11.9.
+inline int paged_cluster_size(const PagedPlan &pl, int d, long long units, long long max_len, long long prefix_max,
+                              int num_sms) {
+    if (pl.tiles) return 0;
+    const long long tiles = (max_len + pl.tile - 1) / pl.tile + (prefix_max + pl.tile - 1) / pl.tile;
+    const long long all = static_cast<long long>(pl.per_sm) * num_sms;  // CTAs at a time
+    // Clusters of 8 or 4 do not fill the last SMs of every group of SMs: 36 and 74 ran at a time
+    // on 152 SMs, and one more made a second wave (16 rows of 128: 8.7 to 13.1 us).
+    auto fit = [&](int size) { return units * size <= (size > 2 ? all - all / 16 : all); };
+    int size = 8;
+    while (size > 1 && (size / 2 >= tiles || !fit(size))) size /= 2;
+    if (!fit(size)) return 0;
+    const long long tile_ns = pl.block_rows == 16 ? (d == 128 ? 580 : 450) : pl.block_rows == 32 ? (d == 128 ? 950 : 580)
+                                                                                               : (d == 128 ? 1700 : 870);
+    return (tiles + size - 1) / size * tile_ns <= (prefix_max ? 12000 : 10000) ? size : 0;
+}
+
 // What a step of a pass costs an SM, in ns, measured on runs confined to a few SMs; only
 // the ratio of two passes counts.  (Shared prefix of 16500 tokens for 256 sequences of
 // 16 to 1024 own ones, 64 query heads: 202 us with the SMs split so, 228 one after the other.)

@@ -251,18 +251,9 @@ int launch_pass(const PagedPass &a, cudaStream_t stream) {
     return bf16 ? launch_rows_d<128, true>(a, stream) : launch_rows_d<128, false>(a, stream);
 }
 
-// CTAs per cluster for calls that paged_cluster_kernel serves best, or 0.  Against the
-// split form it saves a kernel and a scratch allocation (about 3 us) and loses where its
-// eight CTAs per unit get more tiles each than an even share of the whole GPU would be
-// (0.5 to 0.7 us a tile).  The sizes are bounds: lengths are known on the device only.
+// CTAs per cluster when the call (prefix_max: and the keys in front of it) goes to paged_cluster_kernel, or 0.
 int cluster_size(const PagedPass &x, long long prefix_max) {
-    if (x.plan.tiles) return 0;
-    const long long tiles = (x.p.max_len + kTile - 1) / kTile + (prefix_max + kTile - 1) / kTile;
-    const long long all = 2LL * x.num_sms;  // CTAs at a time
-    int size = 8;
-    while (size > 1 && (size / 2 >= tiles || x.units * size > all)) size /= 2;
-    if (x.units * size > all) return 0;
-    return (tiles + size - 1) / size - x.units * tiles / all <= (prefix_max ? 6 : 4) ? size : 0;
+    return paged_cluster_size(x.plan, x.c.head_dim, x.units, x.p.max_len, prefix_max, x.num_sms);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }

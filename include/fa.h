@@ -495,7 +495,10 @@ int fa_cache_append(const fa_paged_cache *cache, const void *q, const void *k,
  *     at a time may use
  * The lengths are read on the device and the work is cut there, so a captured
  * call follows lengths and tables that change between replays.  The same
- * arguments and lengths give the same bits on every run.
+ * arguments and lengths give the same bits on every run.  How the work is laid
+ * out goes by the sizes, max_pages among them, as the longest that a sequence
+ * may be: a table that is no wider than the sequences need saves a short call
+ * some 5 us.
  */
 int fa_decode_paged(const fa_paged_cache *cache, const void *q, void *out,
                     const int32_t *page_table, int max_pages,

@@ -1,5 +1,6 @@
-"""How the two passes of a shared-prefix call share the SMs (csrc/fa_paged_cut.cuh compiled for the host, no GPU): each
-pass adds up its own steps and the other one's, from the lengths, and both have to come to the same split."""
+"""How a paged call is cut (csrc/fa_paged_cut.cuh compiled for the host, no GPU).  The two passes of a shared-prefix call
+share the SMs: each adds up its own steps and the other one's, from the lengths, and both have to come to the same
+split.  A call runs in clusters only where the longest sequence that its table allows stays short."""
 import os
 import random
 import subprocess
@@ -9,6 +10,7 @@ import pytest
 from attention_forward_prefill_gb300 import build
 
 HARNESS = r"""
+// arguments: none, shared-prefix calls; "form", sizes of calls that may run in clusters
 #include <algorithm>
 #include <cstdio>
 #include <vector>
@@ -64,7 +66,14 @@ long long peer_of(const Pass &x) {
     return sum * x.p.Hkv;
 }
 
-int main() {
+int main(int argc, char **) {
+    if (argc > 1) {
+        long long units, max_len, prefix;
+        int rows, d, sms;
+        while (std::scanf("%d %d %lld %lld %lld %d", &rows, &d, &units, &max_len, &prefix, &sms) == 6)
+            std::printf("%d\n", paged_cluster_size(plan_paged(1, rows, d), d, units, max_len, prefix, sms));
+        return 0;
+    }
     int B, G, Hkv, d, prefix, max_len, sms;
     while (std::scanf("%d %d %d %d %d %d %d", &B, &G, &Hkv, &d, &prefix, &max_len, &sms) == 7) {
         std::vector<int> front{prefix}, lens(B);
@@ -88,7 +97,11 @@ def split(tmp_path_factory):
     subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-O1", "-I", build.CSRC, str(at / "split.cpp"), "-o",
                     str(at / "split")], check=True)
 
-    def run(cases):
+    def run(cases, *how):
+        if how:
+            out = subprocess.run([str(at / "split"), *how], input="\n".join(" ".join(map(str, c)) for c in cases),
+                                 capture_output=True, text=True, check=True).stdout
+            return [int(line) for line in out.split()]
         text = "\n".join(" ".join(map(str, [B, G, Hkv, d, prefix, max_len, sms, *lens]))
                          for B, G, Hkv, d, prefix, max_len, sms, lens in cases)
         out = subprocess.run([str(at / "split")], input=text, capture_output=True, text=True, check=True).stdout
@@ -136,3 +149,29 @@ def test_both_passes_come_to_the_same_split(split):
         assert wa == wa_seen == steps(1, B, G, Hkv, d, [prefix])
         assert wb == wb_seen == steps(B, 1, G, Hkv, d, clamped)
         assert mine == theirs and 1 <= mine <= max(sms - 1, 1)
+
+
+def test_clusters_are_kept_for_short_sequences_whatever_the_number_of_units(split):
+    """No CTA of a cluster may be given more than a few microseconds of tiles in a row: a batch whose units times the
+    cluster's size nearly fill the GPU is no exception, as its longest sequence would set the time alone."""
+    cases = [(rows, d, units, max_len, prefix, sms) for rows in (1, 8, 16, 32, 64) for d in (64, 128)
+             for units in (1, 8, 30, 35, 36, 38, 70, 72, 76, 144, 150, 151, 152, 153, 160, 296, 303, 304, 305, 312)
+             for max_len in (16, 64, 200, 1008, 2000, 4112, 8192, 131072) for prefix in (0, 64, 784, 8192, 65536)
+             for sms in (148, 152)]
+    seen = set()
+    for (rows, d, units, max_len, prefix, sms), size in zip(cases, split(cases, "form")):
+        if size == 0:
+            continue
+        seen.add(size)
+        in_a_row = -(-(-(-max_len // 64) + -(-prefix // 64)) // size)
+        assert in_a_row <= (27 if prefix else 22) and units * size <= 2 * sms
+        if rows == 64 and d == 128:
+            assert in_a_row <= (7 if prefix else 5)
+        if size > 2:  # clusters that all run at once
+            assert units * size <= 2 * sms * 15 / 16
+    assert seen == {1, 2, 4, 8}
+    # 8 kv heads and a table of 8192 tokens: neighbouring batch sizes take the same form
+    assert split([(4, 128, 8 * B, 8192, 0, 152) for B in (9, 18, 19, 20, 37, 38, 39)], "form") == [0] * 7
+    assert split([(4, 128, 8 * B, 131072, 0, 152) for B in (1, 19, 38)], "form") == [0] * 3
+    # short tables stay in clusters
+    assert split([(1, 64, 12, 1008, 0, 152), (1, 64, 48, 64, 784, 152), (42, 64, 32, 4128, 0, 152)], "form") == [8, 4, 8]
