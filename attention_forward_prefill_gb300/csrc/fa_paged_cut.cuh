@@ -211,7 +211,7 @@ inline PagedPlan plan_paged(int max_q, int group, int d) {
 // so that the longest sequence sets the time alone, where the split form shares it among all
 // SMs but costs a plan and a join (7 us more, and 12 to 17 us with a prefix, whose two passes
 // and join it replaces).  So the bound is on the tiles in a row, whatever the number of units, by
-// what one takes: at most 10 us, 12 with a prefix, which loses 3 us when one sequence has the
+// what one takes: at most 10 us, which loses 3 us when one sequence has the
 // bound's length and gains 5 when none comes near it.  Measured on 32 units, one sequence of that
 // length among short ones, clusters against split: 16 rows of 128, 12 tiles in a row 12.8 us
 // against 12.6 and 16 tiles 15.4 against 13.3; 32 rows of 128, 4 tiles 11.8 against 14.5 and 8
@@ -226,20 +226,27 @@ inline int paged_cluster_size(const PagedPlan &pl, int d, long long units, long 
     const long long all = static_cast<long long>(pl.per_sm) * num_sms;  // CTAs at a time
     // Clusters of 8 or 4 do not fill the last SMs of every group of SMs: 36 and 74 ran at a time
     // on 152 SMs, and one more made a second wave (16 rows of 128: 8.7 to 13.1 us).
-    auto fit = [&](int size) { return units * size <= (size > 2 ? all - all / 16 : all); };
+    auto fit = [&](int size) { return units * size <= (size > 2 ? all - all / 20 : all); };
     int size = 8;
     while (size > 1 && (size / 2 >= tiles || !fit(size))) size /= 2;
     if (!fit(size)) return 0;
     const long long tile_ns = pl.block_rows == 16 ? (d == 128 ? 580 : 450) : pl.block_rows == 32 ? (d == 128 ? 950 : 580)
                                                                                                : (d == 128 ? 1700 : 870);
-    return (tiles + size - 1) / size * tile_ns <= (prefix_max ? 12000 : 10000) ? size : 0;
+    const long long in_a_row = (tiles + size - 1) / size;
+    if (in_a_row * tile_ns <= (prefix_max ? 12000 : 10000)) return size;
+    // A prefix is as long for every unit, so that its tiles are shared evenly where the units fill
+    // the GPU: up to 18 us of them (36 units of 40 tiles in a row: 20 us, 30 in two passes).
+    return prefix_max && in_a_row - units * tiles / all <= 6 && in_a_row * tile_ns <= 18000 ? size : 0;
 }
 
-// What a step of a pass costs an SM, in ns, measured on runs confined to a few SMs; only
-// the ratio of two passes counts.  (Shared prefix of 16500 tokens for 256 sequences of
-// 16 to 1024 own ones, 64 query heads: 202 us with the SMs split so, 228 one after the other.)
+// What a step of a pass costs an SM, in ns; only the ratio of two passes counts.  At d = 128
+// measured on runs confined to a few SMs (shared prefix of 16500 tokens for 256 sequences of
+// 16 to 1024 own ones, 64 query heads: 202 us with the SMs split so, 228 one after the other).
+// At d = 64 what 11 calls of 18 to 256 sequences behind 500 to 30000 tokens took least with:
+// 128 sequences of 500 behind 16000, 12 heads: 73 us with 1400, 58 with 2400, 52 with 2600, 54
+// with 3000; 256 of them behind 16500, 64 over 8 heads: 165, 145, 152 and 166.
 inline int paged_step_ns(const PagedPlan &pl, int d) {
-    if (pl.tiles) return (d == 128 ? 1900 : 1400) / pl.both_steps;
+    if (pl.tiles) return (d == 128 ? 1900 : 2400) / pl.both_steps;
     const int ns = pl.block_rows == 16 ? 420 : (pl.block_rows == 32 ? 800 : 1150);
     return d == 128 ? ns : ns * 5 / 6;
 }
