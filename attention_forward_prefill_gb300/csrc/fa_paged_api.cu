@@ -33,6 +33,50 @@ size_t strided(long long rows, long long stride, int H, int d) {
     return rows < 1 || H < 1 ? 0 : static_cast<size_t>(rows - 1) * stride + static_cast<size_t>(H) * d;
 }
 
+struct Dim {
+    long long n, stride;
+};
+
+// The dimensions of a page tensor that are stepped over, shortest stride first; how many.
+int page_dims(const fa_paged_cache &c, Dim (&dims)[3]) {
+    int n = 0;
+    for (const Dim &m : {Dim{c.page_size, c.slot_stride}, Dim{c.num_heads, c.head_stride}, Dim{c.num_pages, c.page_stride}})
+        if (m.n > 1) dims[n++] = m;  // (the stride of an extent of one may be anything)
+    std::sort(dims, dims + n, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    return n;
+}
+
+long long floor_div(long long a, long long b) { return a / b - (a % b < 0 ? 1 : 0); }
+
+// Whether two tensors of these dimensions over rows of `row` elements, `delta` elements apart, share a
+// place.  Every stride is at least what the dimensions below it span, so two steps of one come into question.
+bool share_place(const Dim *dims, int n, long long row, long long delta) {
+    if (n == 0) return delta > -row && delta < row;
+    const Dim &m = dims[n - 1];
+    const long long step = floor_div(delta, m.stride);
+    for (long long i = step; i <= step + 1; ++i)
+        if (i > -m.n && i < m.n && share_place(dims, n - 1, row, delta - i * m.stride)) return true;
+    return false;
+}
+
+// `row` elements every `stride`.
+struct Rows {
+    const void *base;
+    long long row, stride;
+};
+// Whether any of `total` rows of either meet.  (At different strides: whether their spans do.)
+bool rows_meet(const Rows &a, const Rows &b, long long total) {
+    const auto span = [&](const Rows &r) {
+        return Span{r.base, static_cast<size_t>((total < 1 ? 0 : (total - 1) * r.stride + r.row) * 2)};
+    };
+    if (total < 1 || !meet(span(a), span(b))) return false;
+    if (total < 2 || a.stride != b.stride) return true;
+    const long long delta = (reinterpret_cast<intptr_t>(b.base) - reinterpret_cast<intptr_t>(a.base)) / 2;
+    const long long step = floor_div(delta, a.stride), off = delta - step * a.stride;
+    return (off < a.row && step > -total && step < total) ||
+           (off + b.row > a.stride && step + 1 > -total && step + 1 < total);
+}
+
 // The pages themselves; *elements: from the first to the last element of either tensor.
 int check_cache(const fa_paged_cache *c, size_t *elements) {
     if (!c || !c->k_pages || !c->v_pages) return FA_ERR_NULL;
@@ -41,18 +85,16 @@ int check_cache(const fa_paged_cache *c, size_t *elements) {
     if (c->head_dim != 64 && c->head_dim != 128) return FA_ERR_HEAD_DIM;
     if (c->dtype != FA_F16 && c->dtype != FA_BF16) return FA_ERR_DTYPE;
     if (off16(c->k_pages) || off16(c->v_pages)) return FA_ERR_ALIGN;
-    struct Dim {
-        long long n, stride;
-    } dims[3] = {{c->page_size, c->slot_stride}, {c->num_heads, c->head_stride}, {c->num_pages, c->page_stride}};
-    for (const Dim &m : dims) {
-        if (m.n == 1) continue;  // never stepped over
+    Dim dims[3];
+    const int n = page_dims(*c, dims);
+    for (int i = 0; i < n; ++i) {
+        const Dim &m = dims[i];
         if (m.stride < c->head_dim || m.stride >= (1LL << 39)) return FA_ERR_SHAPE;
         if (m.stride % 8) return FA_ERR_ALIGN;
     }
-    std::sort(dims, dims + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
     unsigned long long span = c->head_dim;  // no two elements share a place
-    for (const Dim &m : dims) {
-        if (m.n == 1) continue;
+    for (int i = 0; i < n; ++i) {
+        const Dim &m = dims[i];
         if (static_cast<unsigned long long>(m.stride) < span) return FA_ERR_SHAPE;
         span += static_cast<unsigned long long>(m.n - 1) * m.stride;
         if (span > (1ULL << 46)) return FA_ERR_SHAPE;
@@ -241,9 +283,20 @@ int fa_cache_append(const fa_paged_cache *cache, const void *q, const void *k, c
         for (const Span &x : aux)
             if (meet(w, x)) return FA_ERR_ALIAS;
     }
-    if (!in_place)
+    if (in_place) {  // (k and v may lie between q's rows, as in a fused projection)
+        const Rows rq = {q, 1LL * Hq * d, q_stride};
+        if (rows_meet(rq, {k, 1LL * Hkv * d, k_stride}, q ? total : 0) ||
+            rows_meet(rq, {v, 1LL * Hkv * d, v_stride}, q ? total : 0))
+            return FA_ERR_ALIAS;
+    } else {
         for (const Span &i : in)
             if (meet(qo, i)) return FA_ERR_ALIAS;
+    }
+    // a slot's key and its value are two places
+    Dim dims[3];
+    const int n = page_dims(*cache, dims);
+    if (share_place(dims, n, d, (reinterpret_cast<intptr_t>(cache->v_pages) - reinterpret_cast<intptr_t>(cache->k_pages)) / 2))
+        return FA_ERR_ALIAS;
     for (const Span &x : aux)
         if (meet(qo, x)) return FA_ERR_ALIAS;
     DeviceInfo dev;

@@ -473,7 +473,8 @@ typedef struct {
  * outside [0, max_pages * page_size) is not written (FA_ERR_SEQ_LEN recorded).
  * Two tokens with the same slot are the caller's error.
  * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEAD_DIM, FA_ERR_DTYPE, FA_ERR_ALIGN,
- * FA_ERR_ALIAS (the pages, or q_out other than q, overlap an input), FA_ERR_ARCH,
+ * FA_ERR_ALIAS (the pages, or q_out other than q, overlap an input; k_pages and
+ * v_pages share a slot's place; in place, k or v shares q's rows), FA_ERR_ARCH,
  * FA_ERR_CUDA.
  */
 int fa_cache_append(const fa_paged_cache *cache, const void *q, const void *k,
