@@ -29,6 +29,7 @@
 // weights overwrite S, at d = 64 they have columns of their own and the next
 // S starts as soon as the last one is in registers.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fa_paged.cuh"
@@ -586,7 +587,9 @@ int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
     if ((rc = make_page_map(&mv, a.c.v_pages, a.c, kKeys)) != FA_OK) return rc;
     // scale == 0 runs as 2^-100: every weight is then exactly 1 as well, and masked
     // scores (+-inf) never meet a zero multiplier
+    // (below 2^-126 the packed products would take it for 0)
     if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-100f;
+    else if (std::fabs(p.scale_log2) < 0x1p-126f) p.scale_log2 = std::copysign(0x1p-126f, p.scale_log2);
     const auto kernel = paged_tiles_kernel<D, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, a.device, ready)) != FA_OK) return rc;
