@@ -11,6 +11,7 @@ namespace fa {
 namespace {
 
 constexpr int kMaxPageSize = 1 << 20;
+constexpr float kLog2eHost = 1.4426950408889634f;
 
 bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
@@ -132,7 +133,7 @@ int check_attention(const Attention &a) {
     if (off16(a.q) || off16(a.out) || off4(a.lse) || off4(a.page_table) || off4(a.seq_lens) || off4(a.cu) ||
         off16(a.workspace))
         return FA_ERR_ALIGN;
-    if (!std::isfinite(a.scale)) return FA_ERR_SCALE;
+    if (!std::isfinite(a.scale * kLog2eHost)) return FA_ERR_SCALE;  // (the kernels' scores are in log2 units)
     const size_t rows = static_cast<size_t>(a.total) * a.Hq;
     const Span outs[2] = {{a.out, rows * a.c->head_dim * out_size(a.out_dtype)}, {a.lse, a.lse ? rows * 4 : 0}};
     const Span ins[6] = {{a.q, rows * a.c->head_dim * 2},

@@ -50,7 +50,8 @@ typedef enum {
     FA_ERR_HEAD_DIM = 3,   /* d is not a supported head dimension                 */
     FA_ERR_DTYPE = 4,      /* unsupported input/output dtype combination          */
     FA_ERR_ALIGN = 5,      /* a pointer is not 16-byte aligned                    */
-    FA_ERR_SCALE = 6,      /* scale is NaN or infinite                            */
+    FA_ERR_SCALE = 6,      /* scale is NaN or infinite (over pages: or scale x
+                              log2 e is)                                          */
     FA_ERR_ARCH = 7,       /* current device is not compute capability 10.3       */
     FA_ERR_WORKSPACE = 8,  /* caller workspace too small, or allocation failed    */
     FA_ERR_CUDA = 9,       /* a CUDA runtime call failed: see fa_last_cuda_error  */
