@@ -11,6 +11,7 @@ library is missing this module raises -- there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import struct
@@ -125,12 +126,21 @@ def load(build_if_missing: bool = False):
 _calls = None
 
 
+class _InPython:
+    """In the place of _paged_calls where it is not built: every call goes through the checks in Python."""
+    append = decode = prefill = shared = staticmethod(lambda *args: NotImplemented)
+
+
 def _fast():
     """The module _paged_calls over the loaded library."""
     global _calls
     if _calls is None:
         lib = load()
-        from . import _paged_calls
+        try:
+            _paged_calls = importlib.import_module("._paged_calls", __package__)
+        except ModuleNotFoundError:
+            _calls = _InPython
+            return _calls
         _paged_calls.init(_torch(), FaError, *(ctypes.cast(getattr(lib, n), _vp).value for n in (
             "fa_cache_append", "fa_decode_paged", "fa_prefill_paged", "fa_decode_shared")))
         _calls = _paged_calls

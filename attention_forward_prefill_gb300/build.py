@@ -1,8 +1,8 @@
 """Build libfa_gb300.so in-tree from csrc/*.cu with nvcc for sm_103a.
 
 One translation unit per kernel family, compiled in parallel, then linked
-into a shared library next to this file; and the CPython module _paged_calls, with the
-host's C compiler.  No torch C++ ABI is involved, so the same sources build on x86 and
+into a shared library next to this file; and, where Python's headers are, the CPython
+module _paged_calls, with the host's C compiler.  No torch C++ ABI is involved, so the same sources build on x86 and
 Arm hosts.
 """
 from __future__ import annotations
@@ -45,11 +45,18 @@ def _inputs_mtime() -> float:
 
 
 def _build_calls(verbose: bool) -> None:
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        # (the library needs none of it, and binding.py makes the same calls in Python)
+        if os.path.exists(CALLS_PATH):
+            os.remove(CALLS_PATH)  # of older sources
+        sys.stderr.write(f"no Python.h in {include}: paged-cache calls stay in Python, some 3 us slower each\n")
+        return
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
     if cc is None:
         raise RuntimeError("a C compiler is required to build _paged_calls")
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
-    r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+    r = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", include,
                         os.path.join(CSRC, CALLS_SOURCE), "-o", tmp, "-lm"], capture_output=True, text=True)
     if verbose or r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
@@ -61,10 +68,15 @@ def _build_calls(verbose: bool) -> None:
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the path of libfa_gb300.so."""
     newest = _inputs_mtime()
+    _build_library(force, verbose, ptxas_info, newest)
     if force or not os.path.exists(CALLS_PATH) or os.path.getmtime(CALLS_PATH) < newest:
         _build_calls(verbose)
+    return LIB_PATH
+
+
+def _build_library(force: bool, verbose: bool, ptxas_info: bool, newest: float) -> None:
     if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= newest:
-        return LIB_PATH
+        return
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
@@ -90,7 +102,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking libfa_gb300.so failed")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
