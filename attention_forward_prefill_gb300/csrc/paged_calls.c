@@ -73,8 +73,10 @@ static int read_tensor(PyObject *o, Tensor *t) {
     return ok;
 }
 
-static int contiguous(const Tensor *t) {
+static int contiguous(const Tensor *t) { /* (a tensor without elements is) */
     long long want = 1;
+    for (int i = 0; i < t->nd; ++i)
+        if (t->size[i] == 0) return 1;
     for (int i = t->nd - 1; i >= 0; --i) {
         if (t->size[i] != 1 && t->stride[i] != want) return 0;
         want *= t->size[i];
