@@ -188,14 +188,15 @@ static int scale_of(PyObject *o, int d, float *scale) {
 /* append(q, k, v, k_pages, v_pages, page_table, seq_lens, cu_seqlens, rope, interleaved, positions, out) */
 static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
-    if (n != 12 || a[0] == Py_None) GIVE_UP;
+    const int keys_alone = n == 12 && a[0] == Py_None;
+    if (n != 12 || (keys_alone && a[11] != Py_None)) GIVE_UP;
     fa_paged_cache c;
     Tensor kp, q, k, v, table, lens, cu, pos, rope, to;
     if (!cache_of(a[3], a[4], &c, &kp)) GIVE_UP;
     const long long d = c.head_dim;
-    if (!rows(a[0], &q, &kp, d) || !rows(a[1], &k, &kp, d) || !rows(a[2], &v, &kp, d)) GIVE_UP;
+    if ((!keys_alone && !rows(a[0], &q, &kp, d)) || !rows(a[1], &k, &kp, d) || !rows(a[2], &v, &kp, d)) GIVE_UP;
     const long long total = k.size[0];
-    if (total < 1 || q.size[0] != total || v.size[0] != total || k.size[1] != c.num_heads || v.size[1] != c.num_heads) GIVE_UP;
+    if (total < 1 || (!keys_alone && q.size[0] != total) || v.size[0] != total || k.size[1] != c.num_heads || v.size[1] != c.num_heads) GIVE_UP;
     if (!ints(a[5], &table, 2, kp.device) || !ints(a[6], &lens, 1, kp.device) || table.size[0] != lens.size[0]) GIVE_UP;
     cu.ptr = pos.ptr = rope.ptr = NULL;
     if (a[7] != Py_None && (!ints(a[7], &cu, 1, kp.device) || cu.size[0] != lens.size[0] + 1)) GIVE_UP;
@@ -211,11 +212,18 @@ static PyObject *py_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     }
     void *stream;
     if (!stream_of(kp.device, &stream)) GIVE_UP;
-    PyObject *out = output(a[11], a[0], &q, &to);
-    if (!out) GIVE_UP;
-    if (to.stride[2] != 1 || (to.stride[1] != d && to.size[1] != 1)) {
-        Py_DECREF(out);
-        GIVE_UP;
+    PyObject *out;
+    if (keys_alone) {
+        q.ptr = to.ptr = NULL;
+        q.stride[0] = to.stride[0] = q.size[1] = 0;
+        out = Py_NewRef(Py_None);
+    } else {
+        out = output(a[11], a[0], &q, &to);
+        if (!out) GIVE_UP;
+        if (to.stride[2] != 1 || (to.stride[1] != d && to.size[1] != 1)) {
+            Py_DECREF(out);
+            GIVE_UP;
+        }
     }
     int rc;
     Py_BEGIN_ALLOW_THREADS

@@ -49,3 +49,22 @@ def test_ordinary_calls(c_path_only):
     assert torch.equal(out, binding.prefill_paged(turned, kp, vp, table, lens, cu, 1))
     empty = torch.zeros(1, dtype=torch.int32, device="cuda")
     binding.decode_shared(turned, kp, vp, empty, empty, table, lens)
+
+
+def test_keys_alone(c_path_only):
+    _, k, v, kp, vp, table, lens = operands()
+    assert binding.cache_append(None, k, v, kp, vp, table, lens) is None
+    assert torch.equal(kp[:3, :, 4], k) and torch.equal(vp[:3, :, 4], v)
+
+
+def test_refusals_of_keys_alone_are_those_of_python():
+    q, k, v, kp, vp, table, lens = operands()
+    with pytest.raises(ValueError, match="out without q"):
+        binding.cache_append(None, k, v, kp, vp, table, lens, out=q)
+    with pytest.raises(ValueError):
+        binding.cache_append(None, k[:2], v, kp, vp, table, lens)
+    with pytest.raises(ValueError):
+        binding.cache_append(None, k.float(), v, kp, vp, table, lens)
+    with pytest.raises(binding.FaError) as e:
+        binding.cache_append(None, k, v, kp, kp, table, lens)
+    assert e.value.status == binding.FA_ERR_ALIAS
