@@ -67,3 +67,20 @@ def test_units_that_nearly_fill_the_gpu(units, G, d, dtype):
     out = binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens)
     check(c, q, out, f"{units} units")
     assert torch.equal(out, binding.decode_paged(q, c.k, c.v, c.table, c.seq_lens))
+
+
+# 65 to 128 query heads per kv head: the pass over the sequences' own keys runs on tensor-memory tiles too
+@pytest.mark.parametrize("cols", [2, 2048])
+@pytest.mark.parametrize("prefix", [0, 333, 5000])
+@pytest.mark.parametrize("B,G,Hkv,d,dtype", [(5, 65, 1, 64, BF16), (9, 71, 2, 128, F16), (40, 128, 1, 64, F16),
+                                             (3, 128, 2, 128, BF16), (1, 100, 1, 128, F16)])
+def test_shared_prefix_of_many_heads(B, G, Hkv, d, dtype, prefix, cols):
+    lens = [(i * 37) % 200 if i % 3 else 0 for i in range(B)]
+    if B > 2:
+        lens[-1] = 3000
+    c = Cache(lens, Hkv, d, 64, dtype, slots_first=prefix == 333, seed=G, prefix=prefix, extra_cols=cols)
+    q = queries(B, G * Hkv, d, dtype)
+    out = binding.decode_shared(q, c.k, c.v, c.prefix_table, c.prefix_len, c.table, c.seq_lens)
+    check(c, q, out, f"prefix {prefix}")
+    for _ in range(20):
+        assert torch.equal(out, binding.decode_shared(q, c.k, c.v, c.prefix_table, c.prefix_len, c.table, c.seq_lens))
