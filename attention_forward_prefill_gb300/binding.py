@@ -834,8 +834,9 @@ def prefill_paged(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_s
 def decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens,
                   scale: float | None = None, out_dtype=None, workspace=None, out=None):
     """decode_paged for a batch that shares a prefix: every row sees the first prefix_len tokens
-    (int32 [1], on the device) of prefix_table's pages (int32 [n]), then its own.  The prefix is
-    read once for the whole batch.
+    (int32 [1], on the device) of prefix_table's pages (int32 [n]), then its own.  A tile of the
+    prefix is loaded once for up to 256 query rows of a kv head; a small call loads it once per
+    sequence and kv head, out of L2.
     """
     if out_dtype is None and workspace is None:
         done = (_calls or _fast()).shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq_lens, scale, out)

@@ -14,7 +14,7 @@
 // of the table in registers while it walks over the heads, D / 16 lanes a head,
 // 32 bytes a lane: a pair's two halves are then always in one lane.  38 thousand
 // tokens of 32 + 8 + 8 heads of 128: 141 us, 6.4 TB/s of DRAM traffic (95% of the copy
-// rate); 256 single tokens: 3.2 us, one token 2.1 us (back to back in a graph).
+// rate); 256 single tokens: 3.3 us, one token 2.2 us (back to back in a graph).
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -335,7 +335,7 @@ __device__ __forceinline__ void paged_emit(const PagedParams &p, const PagedPiec
 // loads (4 rows x 2 pieces, 2 x 4, or 8 pieces) are in flight together.  Where the items
 // leave most warps idle, a CTA takes an item and its warps a share of the pieces each
 // (one long sequence: 300 pieces of 64 rows took 26 us a warp per row).  8 us for 303 units
-// of 4 rows, 13 us for 151 of 256 (39 MB of pieces, out of L2).
+// of 4 rows, 13.5 us for 151 of 256 (39 MB of pieces, out of L2).
 constexpr int kJoinThreads = 256;
 // CTAs per SM (d = 64: 3 take 2.5 us less than 2 for 151 units of 256 rows; d = 128 at 3: spills, 7 us more)
 template <int D>
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm<D>) paged_join_kernel
 // Joins two passes over the same rows, one query token per sequence: a over keys that
 // all sequences share (one sequence of B tokens), b over each sequence's own.  A warp
 // takes R rows at a time; their notes, then their pieces, a's first and in CTA order.
-// 7.5 us for 2048 rows of 20 and 1 to 2 pieces, 13.5 us for 16384 of 2 to 4 and 1 to 2 (d = 128).
+// 8 us for 2048 rows of 20 and 1 to 2 pieces, 15.5 us for 16384 of 2 to 4 and 1 to 2 (d = 128).
 template <int D, int R, int F>
 __device__ __forceinline__ void paged_pair_rows(const PagedParams &a, const PagedParams &b, int slot_a, int slot_b,
                                                 int blocks_a, int blocks_b, int ctas_a, int ctas_b, int row0, int rows,

@@ -90,8 +90,8 @@ struct PagedRows {
     // arrived in every lane: what hands their place back hangs on it.  (zero: a mask that
     // is zero, which the compiler does not know.)  A barrier arrival alone comes after the
     // loads' issue, not their end, and nothing else binds the copy engine that writes the
-    // place next: without this, one call in two of many short units of 32 rows took a query
-    // row, and one in a thousand a piece of a V tile, from the data that came behind.
+    // place next: without this, most calls of many short units of 32 rows took a query
+    // row, and a few in thousands a piece of a V tile, from the data that came behind.
     __device__ __forceinline__ bool loads_pending(uint32_t zero) const {
         return __any_sync(0xffffffffu, (loads & zero) != 0);
     }

@@ -23,8 +23,8 @@
 // While the softmax of one query tile works on its weights, the tensor core
 // runs the other tile's products.  (A unit's start and end cost 2.7 to 3.5 us at
 // d = 128, a step 1.75 us.)  Measured: 4 chunks of 700 to 2048 tokens on up to 12048, 32
-// heads over 8 of 128, bf16, causal: 281 us, 1231 TFLOP/s, tensor pipe 54% active, and
-// 13 us of join; 8192 tokens, 16 heads, full: 421 us against the dense kernel's 410.
+// heads over 8 of 128, bf16, causal: 287 us, 1205 TFLOP/s, tensor pipe 54% active, and
+// 13.5 us of join; 8192 tokens, 16 heads, full: 421 us against the dense kernel's 410.
 // TMEM: S0 | S1 | O0 | O1; at d = 128 the
 // weights overwrite S, at d = 64 they have columns of their own and the next
 // S starts as soon as the last one is in registers.

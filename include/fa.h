@@ -439,7 +439,11 @@ size_t fa_decode_noalloc_max_bytes(void);
  * Slots behind a sequence's last token may hold anything, NaN included.
  * A row with a score of NaN or +inf comes out NaN, its log-sum-exp too, as the
  * softmax of such scores is; one whose scores are all -inf counts as a row
- * without keys.
+ * without keys.  A NaN or an infinity among the values of a token reaches the rows
+ * that see the token, and may reach rows of its sequence that a causal mask keeps
+ * from it.
+ * Scores, sums and joins are fp32.  The weights are rounded to the cache's type for
+ * the product with the values, and the sum adds the rounded weights.
  */
 typedef struct {
     void *k_pages, *v_pages;
@@ -531,8 +535,10 @@ int fa_prefill_paged(const fa_paged_cache *cache, const void *q, void *out,
 /*
  * Decode of a batch that shares a prefix: row b attends to the first
  * *prefix_len tokens of prefix_table's pages and then to its own seq_lens[b]
- * tokens in page_table[b] (either may be 0).  The prefix's keys and values are
- * read once for the whole batch.  prefix_table : int32 [max_prefix_pages];
+ * tokens in page_table[b] (either may be 0).  A tile of the prefix's keys and
+ * values is loaded once for up to 256 query rows of a kv head (B * Hq / num_heads
+ * of them), and by a call small enough for one kernel once per sequence and kv
+ * head, out of L2.  prefix_table : int32 [max_prefix_pages];
  * prefix_len : device int32; workspace : NULL or
  * fa_shared_workspace_bytes(B, Hq, num_heads, d, -1); the rest as fa_decode_paged.
  */
