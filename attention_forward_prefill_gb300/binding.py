@@ -29,11 +29,11 @@ STATUS_NAMES = {
     4: "FA_ERR_DTYPE", 5: "FA_ERR_ALIGN", 6: "FA_ERR_SCALE", 7: "FA_ERR_ARCH",
     8: "FA_ERR_WORKSPACE", 9: "FA_ERR_CUDA", 10: "FA_ERR_WATCHDOG",
     11: "FA_ERR_SEQ_LEN", 12: "FA_ERR_ALIAS", 13: "FA_ERR_SPLITS",
-    14: "FA_ERR_PAGE",
+    14: "FA_ERR_PAGE", 15: "FA_ERR_INDEX",
 }
 (FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEAD_DIM, FA_ERR_DTYPE, FA_ERR_ALIGN, FA_ERR_SCALE, FA_ERR_ARCH,
  FA_ERR_WORKSPACE, FA_ERR_CUDA, FA_ERR_WATCHDOG, FA_ERR_SEQ_LEN, FA_ERR_ALIAS,
- FA_ERR_SPLITS, FA_ERR_PAGE) = range(1, 15)
+ FA_ERR_SPLITS, FA_ERR_PAGE, FA_ERR_INDEX) = range(1, 16)
 
 _lock = threading.Lock()
 _lib = None
@@ -74,6 +74,13 @@ _SIGNATURES = {
                               _vp]),
     "fa_paged_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "fa_shared_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_tree_mask": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "fa_prefill_tree": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i,
+                             _vp, _sz, _vp]),
+    "fa_cache_weigh": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _f, _vp, _i,
+                            _vp]),
+    "fa_cache_select": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "fa_cache_keep": (_i, [_vp, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _i, _i, _vp]),
     "fa_status_string": (ctypes.c_char_p, [_i]),
     "fa_last_cuda_error": (_i, []),
     "fa_device_status": (_i, [_i]),
@@ -295,6 +302,39 @@ def fa_paged_workspace_bytes(Hq, Hkv, max_seqlen_q, d, device=-1) -> int:
 
 def fa_shared_workspace_bytes(B, Hq, Hkv, d, device=-1) -> int:
     return load().fa_shared_workspace_bytes(B, Hq, Hkv, d, device)
+
+
+def fa_tree_mask(parents, mask, mask_words, positions, seq_lens, cu_seqlens_q, B, total_q, max_seqlen_q,
+                 stream=0) -> int:
+    return load().fa_tree_mask(parents, mask, mask_words, positions, seq_lens, cu_seqlens_q, B, total_q,
+                               max_seqlen_q, stream)
+
+
+def fa_prefill_tree(cache, q, out, lse, page_table, max_pages, seq_lens, cu_seqlens_q, mask, mask_words, B,
+                    Hq, total_q, max_seqlen_q, scale, out_dtype, workspace=None, workspace_bytes=0,
+                    stream=0) -> int:
+    return load().fa_prefill_tree(ctypes.byref(cache), q, out, lse, page_table, max_pages, seq_lens,
+                                  cu_seqlens_q, mask, mask_words, B, Hq, total_q, max_seqlen_q, scale,
+                                  out_dtype, workspace, workspace_bytes, stream)
+
+
+def fa_cache_weigh(cache, q, lse, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq, total_q, max_seqlen_q,
+                   causal, scale, weights, decay, out, weights_len, stream=0) -> int:
+    return load().fa_cache_weigh(ctypes.byref(cache), q, lse, page_table, max_pages, seq_lens, cu_seqlens_q, B,
+                                 Hq, total_q, max_seqlen_q, int(causal), scale, weights, decay, out,
+                                 weights_len, stream)
+
+
+def fa_cache_select(weights, seq_lens, B, heads, weights_len, budget, sink, recent, keep, counts, kept=None,
+                    stream=0) -> int:
+    return load().fa_cache_select(weights, seq_lens, B, heads, weights_len, budget, sink, recent, keep, counts,
+                                  kept, stream)
+
+
+def fa_cache_keep(cache, page_table, max_pages, seq_lens, keep, heads, keep_len, counts, first, out_table,
+                  out_max_pages, B, stream=0) -> int:
+    return load().fa_cache_keep(ctypes.byref(cache), page_table, max_pages, seq_lens, keep, heads, keep_len,
+                                counts, first, out_table, out_max_pages, B, stream)
 
 
 def status_string(status: int) -> str:
@@ -854,3 +894,177 @@ def decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, page_table, seq
          prefix_table.numel(), prefix_len.data_ptr(), page_table.data_ptr(), max_pages, seq_lens.data_ptr(),
          B, _decode_rows(q, B, d), scale, code, ws, ws_bytes)
     return out
+
+
+# ---------------------------------------------------------------- drafted trees
+def tree_mask(parents, cu_seqlens_q, max_seqlen_q: int, seq_lens=None):
+    """What the drafted tokens (nodes) of every sequence see of each other, and their rotary positions.
+
+    parents int32 [T]: the index among its sequence's nodes of the node that each one follows,
+    below its own, or -1 for one that follows the tokens in the cache; sequence b's nodes are
+    cu_seqlens_q[b] .. cu_seqlens_q[b + 1] (int32 [B + 1]), at most max_seqlen_q.  Returns the
+    mask, int32 [T, ceil(max_seqlen_q / 32)], bit j of a row saying that the node sees node j of
+    its sequence (itself and its ancestors), and with seq_lens (int32 [B], the nodes in) the
+    nodes' positions, int32 [T], as cache_append takes them; None without.  Rows outside every
+    sequence are not written.
+    """
+    torch = _torch()
+    device = parents.device
+    if not parents.is_cuda:
+        raise ValueError("parents must be a CUDA tensor")
+    _check_ints(device, "parents", parents, (None,))
+    _check_ints(device, "cu_seqlens_q", cu_seqlens_q, (None,))
+    total, B = parents.numel(), cu_seqlens_q.numel() - 1
+    lens_ptr = None
+    if seq_lens is not None:
+        _check_ints(device, "seq_lens", seq_lens, (B,))
+        lens_ptr = seq_lens.data_ptr()
+    words = max(1, -(-int(max_seqlen_q) // 32))
+    mask = torch.empty((total, words), dtype=torch.int32, device=device)
+    positions = None if seq_lens is None else torch.empty_like(parents)
+    if total:
+        _run("fa_tree_mask", device, parents.data_ptr(), mask.data_ptr(), words,
+             None if positions is None else positions.data_ptr(), lens_ptr, cu_seqlens_q.data_ptr(), B, total,
+             int(max_seqlen_q))
+    return mask, positions
+
+
+def prefill_tree(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q: int, mask,
+                 scale: float | None = None, out_dtype=None, workspace=None, out=None, lse=None):
+    """prefill_paged for drafted trees: every query token sees its sequence's tokens in front of the
+    sequence's query tokens, and of the query tokens those whose bits are set in its row of the mask
+    (int32 [T, words], as tree_mask makes them; any bits will do).
+
+    The rest as prefill_paged; the keys and values of the query tokens are in the cache already.
+    """
+    cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
+                                                                   out_dtype, out)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, Hq, {d}]")
+    total, Hq, _ = q.shape
+    int32 = _torch().int32
+    if not (_is_ints(cu_seqlens_q, device, int32, 1) and cu_seqlens_q.numel() == B + 1):
+        _check_ints(device, "cu_seqlens_q", cu_seqlens_q, (B + 1,))
+    if not (_is_ints(mask, device, int32, 2) and mask.shape[0] == total):
+        _check_ints(device, "mask", mask, (total, None))
+    lse_ptr = None
+    if lse is not None:
+        _check_cuda("lse", lse, (total, Hq), _torch().float32)
+        if lse.device != device:
+            raise ValueError("lse must be on the device of the cache")
+        lse_ptr = lse.data_ptr()
+    if total:
+        ws, ws_bytes = _workspace(workspace, device)
+        _run("fa_prefill_tree", device, cache, q.data_ptr(), out.data_ptr(), lse_ptr, page_table.data_ptr(), max_pages,
+             seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), mask.data_ptr(), mask.shape[1], B, Hq, total,
+             int(max_seqlen_q), scale, code, ws, ws_bytes)
+    return out
+
+
+# ---------------------------------------------------------------- eviction
+def _check_weights(name, t, device, shape):
+    """fp32 [B, heads, width] beside the cache, contiguous; a None in `shape` is any size."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype is not _torch().float32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor")
+    if t.dim() != 3 or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"[{', '.join('any' if n is None else str(n) for n in shape)}]")
+
+
+def cache_weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q: int = 1,
+                causal: bool = True, scale: float | None = None, weights=None, decay: float = 1.0, out=None):
+    """What every token of a paged cache got of the attention of q, added to what it had:
+    out = decay * weights + the sum over the query rows that see the token of exp(scale q.k - lse).
+
+    q [T, Hq, d] and lse fp32 [T, Hq] as in prefill_paged(..., causal, scale, lse=lse) over the same
+    cache; cu_seqlens_q None: one token per sequence.  weights fp32 [B, Hkv, width] or None (nothing
+    so far); out: the same sizes, weights itself for in place, or None for a new array of the width
+    of weights or of the page table.  Places behind a sequence's last token are neither read nor
+    written (zeros in a new array).  A sequence without query tokens keeps its weights.
+    """
+    torch = _torch()
+    cache, Hkv, d = _pages(k_pages, v_pages)
+    device = k_pages.device
+    if not (q.dtype == k_pages.dtype and q.device == device and q.is_contiguous() and q.dim() == 3 and q.shape[2] == d):
+        raise ValueError(f"q must be a contiguous [tokens, Hq, {d}] tensor of the dtype and device of the cache")
+    total, Hq, _ = q.shape
+    _check_cuda("lse", lse, (total, Hq), torch.float32)
+    if lse.device != device:
+        raise ValueError("lse must be on the device of the cache")
+    B, max_pages = _tables(device, page_table, seq_lens)
+    cu_ptr = None
+    if cu_seqlens_q is not None:
+        _check_ints(device, "cu_seqlens_q", cu_seqlens_q, (B + 1,))
+        cu_ptr = cu_seqlens_q.data_ptr()
+    elif total != B * int(max_seqlen_q):
+        raise ValueError(f"q has {total} tokens, expected {max_seqlen_q} for each of {B} sequences")
+    width = None
+    if weights is not None:
+        _check_weights("weights", weights, device, (B, Hkv, None))
+        width = weights.shape[2]
+    if out is None:
+        width = max_pages * k_pages.shape[2] if width is None else width
+        out = torch.zeros((B, Hkv, width), dtype=torch.float32, device=device)
+    else:
+        _check_weights("out", out, device, (B, Hkv, width))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _run("fa_cache_weigh", device, cache, q.data_ptr(), lse.data_ptr(), page_table.data_ptr(), max_pages,
+         seq_lens.data_ptr(), cu_ptr, B, Hq, total, int(max_seqlen_q), 1 if causal else 0, scale,
+         None if weights is None else weights.data_ptr(), decay, out.data_ptr(), out.shape[2])
+    return out
+
+
+def cache_select(weights, seq_lens, budget: int, sink: int = 0, recent: int = 0):
+    """Which tokens stay when every sequence and head may keep `budget`: the first `sink`, the last
+    `recent` and the heaviest of the others (of equal weights the first; NaN counts as the largest);
+    all of them where there are no more than budget.
+
+    weights fp32 [B, heads, width] (heads: the cache's, or 1 for the same choice in all of them),
+    seq_lens int32 [B].  Returns keep, int32 [B, heads, budget], the tokens that stay in rising
+    order, then -1; counts, int32 [B], the new lengths; and the weights of those tokens in the same
+    order, zeros behind, in the shape of weights.
+    """
+    torch = _torch()
+    if not weights.is_cuda:
+        raise ValueError("weights must be a CUDA tensor")
+    device = weights.device
+    _check_weights("weights", weights, device, (None, None, None))
+    B, heads, width = weights.shape
+    _check_ints(device, "seq_lens", seq_lens, (B,))
+    keep = torch.empty((B, heads, max(int(budget), 0)), dtype=torch.int32, device=device)
+    counts = torch.empty_like(seq_lens)
+    kept = torch.empty_like(weights)
+    _run("fa_cache_select", device, weights.data_ptr(), seq_lens.data_ptr(), B, heads, width, int(budget), int(sink),
+         int(recent), keep.data_ptr(), counts.data_ptr(), kept.data_ptr())
+    return keep, counts, kept
+
+
+def cache_keep(k_pages, v_pages, page_table, seq_lens, keep, counts, first=None, out_table=None):
+    """Move the tokens that stay: token keep[b, h, i] of sequence b and kv head h goes to place
+    first[b] + i (first int32 [B], None: 0), for i < counts[b]; returns (k_pages, v_pages).
+
+    keep int32 [B, Hkv, n], or [B, 1, n] for the same tokens in all heads; counts int32 [B].
+    In place by default: a token must lie at or behind the place that it goes to, as those of
+    rising lists do.  out_table int32 [B, pages]: into these pages instead, none of which holds
+    a token that is read.  The new lengths (first + counts) are the caller's to set.
+    """
+    cache, Hkv, _ = _pages(k_pages, v_pages)
+    device = k_pages.device
+    B, max_pages = _tables(device, page_table, seq_lens)
+    _check_ints(device, "keep", keep, (B, None, None))
+    heads, n = keep.shape[1], keep.shape[2]
+    if heads not in (1, Hkv):
+        raise ValueError(f"keep has shape {tuple(keep.shape)}, expected [{B}, {Hkv} or 1, any]")
+    _check_ints(device, "counts", counts, (B,))
+    if first is not None:
+        _check_ints(device, "first", first, (B,))
+    if out_table is not None:
+        _check_ints(device, "out_table", out_table, (B, None))
+    if n:
+        _run("fa_cache_keep", device, cache, page_table.data_ptr(), max_pages, seq_lens.data_ptr(), keep.data_ptr(), heads,
+             n, counts.data_ptr(), None if first is None else first.data_ptr(),
+             None if out_table is None else out_table.data_ptr(), 0 if out_table is None else out_table.shape[1], B)
+    return k_pages, v_pages

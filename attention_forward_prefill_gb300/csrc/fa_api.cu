@@ -137,6 +137,7 @@ const char *fa_status_string(int status) {
         case FA_ERR_ALIAS: return "output overlaps an input";
         case FA_ERR_SPLITS: return "num_splits out of range";
         case FA_ERR_PAGE: return "a page table entry in use was outside the cache";
+        case FA_ERR_INDEX: return "a device-resident index was out of range";
         default: return "unknown status";
     }
 }
@@ -145,8 +146,9 @@ int fa_last_cuda_error(void) { return t_last_cuda_error; }
 
 int fa_device_status(int reset) {
     if (cudaDeviceSynchronize() != cudaSuccess) return -1;
-    const int words[7] = {read_prefill_status(reset), read_decode_status(reset), read_backward_status(reset),
-                          read_paged_status(reset), read_tiles_status(reset), read_cluster_status(reset), read_append_status(reset)};
+    const int words[10] = {read_prefill_status(reset), read_decode_status(reset), read_backward_status(reset),
+                          read_paged_status(reset), read_tiles_status(reset), read_cluster_status(reset), read_append_status(reset),
+                           read_tree_status(reset), read_weigh_status(reset), read_evict_status(reset)};
     int first = 0;
     for (int v : words) {
         if (v < 0) return -1;

@@ -114,6 +114,8 @@ struct PagedLaunch {
     const int32_t *cu_q;        // [B + 1], or null: max_q tokens for every sequence
     int B, Hq, total_q, max_q, max_pages;
     int causal;
+    const uint32_t *tree;       // drafted trees: [total_q][tree_words], see PagedParams; or null
+    int tree_words;
     float scale;
     int out_dtype;
     void *scratch;              // paged_scratch_bytes(...), 16-byte aligned
@@ -142,6 +144,53 @@ struct AppendLaunch {
 
 int launch_append(const AppendLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
 
+struct TreeLaunch {
+    const int32_t *parents;     // [total_q]
+    uint32_t *mask;             // [total_q][mask_words]
+    int32_t *positions;         // [total_q], or null
+    const int32_t *seq_lens, *cu_seqlens_q;
+    int mask_words, B, total_q, max_q;
+};
+
+int launch_tree_mask(const TreeLaunch &a, cudaStream_t stream);
+
+// What the cached tokens got of the attention of some queries.
+struct WeighLaunch {
+    fa_paged_cache c;
+    const void *q;              // [total_q][Hq][d]
+    const float *lse;           // [total_q][Hq]
+    const int32_t *page_table, *seq_lens;
+    const int32_t *cu_q;        // [B + 1], or null: max_q tokens for every sequence
+    int B, Hq, total_q, max_q, max_pages;
+    int causal;
+    float scale, decay;
+    const float *weights;       // [B][heads][weights_len], or null: nothing
+    float *out;                 // the same sizes
+    int weights_len;
+};
+
+int launch_weigh(const WeighLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
+
+struct SelectLaunch {
+    const float *weights;       // [B][heads][weights_len]
+    const int32_t *seq_lens;    // [B]
+    int B, heads, weights_len, budget, sink, recent;
+    int32_t *keep;              // [B][heads][budget]
+    int32_t *counts;            // [B]
+    float *kept;                // [B][heads][weights_len], or null
+};
+
+int launch_select(const SelectLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
+
+struct KeepLaunch {
+    fa_paged_cache c;
+    const int32_t *page_table, *seq_lens, *keep, *counts, *first, *out_table;
+    int max_pages, out_max_pages, heads, keep_len, B;
+    bool in_place;
+};
+
+int launch_keep(const KeepLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
+
 // Device-side watchdog words (one per kernel translation unit).
 int read_prefill_status(int reset);
 int read_decode_status(int reset);
@@ -150,5 +199,8 @@ int read_paged_status(int reset);
 int read_tiles_status(int reset);
 int read_cluster_status(int reset);
 int read_append_status(int reset);
+int read_tree_status(int reset);
+int read_weigh_status(int reset);
+int read_evict_status(int reset);
 
 }  // namespace fa

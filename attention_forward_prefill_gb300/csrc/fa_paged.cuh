@@ -255,6 +255,32 @@ __device__ __forceinline__ void paged_note_open(const PagedParams &p, const Page
     o[0] = make_int4(paged_cta_of(st.end + to_last, st.W, st.G), u.t0, u.hk, u.row0);
 }
 
+// ---------------------------------------------------------------- drafted trees
+// Which of a sequence's keys k0 .. k0 + 31 query token `token` sees, as bits; bits of nodes behind
+// the sequence's last one count for nothing.
+__device__ __forceinline__ uint32_t tree_seen32(const PagedParams &p, const SeqView &s, const uint32_t *row, int k0) {
+    const int n = k0 - (s.len - s.nq);  // the node whose key is k0; below 0 lies the context
+    if (n <= -32) return 0xffffffffu;
+    const int w = n >> 5;
+    const uint32_t lo = w >= 0 && w < p.tree_words ? __ldg(row + w) : 0u;
+    const uint32_t hi = w + 1 < p.tree_words ? __ldg(row + w + 1) : 0u;
+    uint32_t seen = __funnelshift_r(lo, hi, n & 31);
+    if (n < 0) seen |= (1u << -n) - 1u;
+    const int left = s.nq - n;
+    if (left < 32) seen &= left <= 0 ? 0u : (1u << left) - 1u;
+    return seen;
+}
+// The mask row of query row rr of a sequence (rows behind its last token: that token's).
+__device__ __forceinline__ const uint32_t *tree_row(const PagedParams &p, const SeqView &s, int rr) {
+    return p.tree + static_cast<long long>(s.t0 + min(rr / p.G, s.nq - 1)) * p.tree_words;
+}
+// The same for keys k0 .. k0 + 63 and query row rr.
+__device__ __forceinline__ uint64_t tree_seen64(const PagedParams &p, const SeqView &s, int rr, int k0) {
+    if (k0 + 64 <= s.len - s.nq) return ~0ull;  // context alone
+    const uint32_t *row = tree_row(p, s, rr);
+    return tree_seen32(p, s, row, k0) | static_cast<uint64_t>(tree_seen32(p, s, row, k0 + 32)) << 32;
+}
+
 // ---------------------------------------------------------------- rows out
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;

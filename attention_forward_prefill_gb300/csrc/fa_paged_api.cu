@@ -104,6 +104,13 @@ int check_cache(const fa_paged_cache *c, size_t *elements) {
     return FA_OK;
 }
 
+// Whether k_pages and v_pages share a place: a slot's key and its value are two, where either is written.
+bool slots_share(const fa_paged_cache &c) {
+    Dim dims[3];
+    const int n = page_dims(c, dims);
+    return share_place(dims, n, c.head_dim, (reinterpret_cast<intptr_t>(c.v_pages) - reinterpret_cast<intptr_t>(c.k_pages)) / 2);
+}
+
 struct Attention {
     const fa_paged_cache *c;
     const void *q;
@@ -146,6 +153,34 @@ int check_attention(const Attention &a) {
         for (const Span &i : ins)
             if (meet(o, i)) return FA_ERR_ALIAS;
     if (meet(outs[0], outs[1])) return FA_ERR_ALIAS;
+    return FA_OK;
+}
+
+// a: the attention whose weights are counted, without its output (no rows).
+int check_weigh(const Attention &a, const float *lse, int total_q, const float *weights, float decay, const float *out,
+                int weights_len) {
+    int rc = check_attention(a);
+    if (rc != FA_OK) return rc;
+    if (total_q < 0 || static_cast<long long>(total_q) * a.Hq > INT_MAX / 2 || weights_len < 1 || weights_len > INT_MAX / 2 ||
+        (!a.cu && total_q != static_cast<long long>(a.B) * a.max_q))
+        return FA_ERR_SHAPE;
+    const size_t heads = static_cast<size_t>(a.B) * a.c->num_heads;
+    if (heads > (size_t(1) << 40) / weights_len) return FA_ERR_SHAPE;
+    if (off4(lse) || off4(weights) || off4(out)) return FA_ERR_ALIGN;
+    if (!std::isfinite(decay)) return FA_ERR_SCALE;
+    size_t elements = 0;
+    if ((rc = check_cache(a.c, &elements)) != FA_OK) return rc;
+    const size_t rows = static_cast<size_t>(total_q) * a.Hq;
+    const Span o = {out, heads * weights_len * 4};
+    const Span ins[7] = {{a.q, rows * a.c->head_dim * 2},
+                         {lse, rows * 4},
+                         {a.c->k_pages, elements * 2},
+                         {a.page_table, static_cast<size_t>(a.B) * a.max_pages * 4},
+                         {a.seq_lens, static_cast<size_t>(a.B) * 4},
+                         {a.cu, (static_cast<size_t>(a.B) + 1) * 4},
+                         {weights == out ? nullptr : weights, heads * weights_len * 4}};
+    for (const Span &i : ins)
+        if (meet(o, i)) return FA_ERR_ALIAS;
     return FA_OK;
 }
 
@@ -199,12 +234,15 @@ struct Scratch {
     }
 };
 
-int run_attention(const Attention &a, int causal, void *workspace, size_t workspace_bytes, void *stream) {
+int run_attention(const Attention &a, int causal, void *workspace, size_t workspace_bytes, void *stream,
+                  const uint32_t *tree = nullptr, int tree_words = 0) {
     DeviceInfo dev;
     int rc = current_device_info(&dev);
     if (rc != FA_OK) return rc;
     if (a.total == 0) return FA_OK;
     PagedLaunch l = launch_of(a, causal);
+    l.tree = tree;
+    l.tree_words = tree_words;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Scratch s(st);
     // (a workspace is sized for max_seqlen_q, which fewer tokens than that do not change)
@@ -293,11 +331,7 @@ int fa_cache_append(const fa_paged_cache *cache, const void *q, const void *k, c
         for (const Span &i : in)
             if (meet(qo, i)) return FA_ERR_ALIAS;
     }
-    // a slot's key and its value are two places
-    Dim dims[3];
-    const int n = page_dims(*cache, dims);
-    if (share_place(dims, n, d, (reinterpret_cast<intptr_t>(cache->v_pages) - reinterpret_cast<intptr_t>(cache->k_pages)) / 2))
-        return FA_ERR_ALIAS;
+    if (slots_share(*cache)) return FA_ERR_ALIAS;
     for (const Span &x : aux)
         if (meet(qo, x)) return FA_ERR_ALIAS;
     DeviceInfo dev;
@@ -358,6 +392,144 @@ int fa_decode_paged(const fa_paged_cache *cache, const void *q, void *out, const
                          out_dtype, workspace};
     const int rc = check_attention(a);
     return rc != FA_OK ? rc : run_attention(a, 0, workspace, workspace_bytes, stream);
+}
+
+int fa_tree_mask(const int32_t *parents, uint32_t *mask, int mask_words, int32_t *positions, const int32_t *seq_lens,
+                 const int32_t *cu_seqlens_q, int B, int total_q, int max_seqlen_q, void *stream) {
+    if (!parents || !mask || !cu_seqlens_q || (positions && !seq_lens)) return FA_ERR_NULL;
+    if (B < 1 || total_q < 0 || max_seqlen_q < 1 || mask_words < 1 || 32LL * mask_words < max_seqlen_q ||
+        total_q > INT_MAX / 2 || max_seqlen_q > INT_MAX / 2 || (max_seqlen_q + 127LL) / 128 * B > INT_MAX)
+        return FA_ERR_SHAPE;
+    if (off4(parents) || off4(mask) || off4(positions) || off4(seq_lens) || off4(cu_seqlens_q)) return FA_ERR_ALIGN;
+    const size_t rows = static_cast<size_t>(total_q);
+    const Span outs[2] = {{mask, rows * mask_words * 4}, {positions, rows * 4}};
+    const Span ins[3] = {{parents, rows * 4}, {seq_lens, static_cast<size_t>(B) * 4}, {cu_seqlens_q, (static_cast<size_t>(B) + 1) * 4}};
+    for (const Span &o : outs)
+        for (const Span &i : ins)
+            if (meet(o, i)) return FA_ERR_ALIAS;
+    if (meet(outs[0], outs[1])) return FA_ERR_ALIAS;
+    DeviceInfo dev;
+    const int rc = current_device_info(&dev);
+    if (rc != FA_OK) return rc;
+    if (total_q == 0) return FA_OK;
+    return launch_tree_mask({parents, mask, positions, seq_lens, cu_seqlens_q, mask_words, B, total_q, max_seqlen_q},
+                            static_cast<cudaStream_t>(stream));
+}
+
+int fa_prefill_tree(const fa_paged_cache *cache, const void *q, void *out, float *lse, const int32_t *page_table,
+                    int max_pages, const int32_t *seq_lens, const int32_t *cu_seqlens_q, const uint32_t *mask,
+                    int mask_words, int B, int Hq, int total_q, int max_seqlen_q, float scale, fa_dtype out_dtype,
+                    void *workspace, size_t workspace_bytes, void *stream) {
+    if (!cu_seqlens_q || !mask) return FA_ERR_NULL;
+    const Attention a = {cache,        q, out, lse, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq, total_q,
+                         max_seqlen_q, scale, out_dtype, workspace};
+    const int rc = check_attention(a);
+    if (rc != FA_OK) return rc;
+    if (mask_words < 1 || 32LL * mask_words < max_seqlen_q) return FA_ERR_SHAPE;
+    if (off4(mask)) return FA_ERR_ALIGN;
+    const Span bits = {mask, static_cast<size_t>(total_q) * mask_words * 4};
+    const size_t rows = static_cast<size_t>(total_q) * Hq;
+    if (meet({out, rows * cache->head_dim * out_size(out_dtype)}, bits) || meet({lse, rows * 4}, bits)) return FA_ERR_ALIAS;
+    return run_attention(a, 0, workspace, workspace_bytes, stream, mask, mask_words);
+}
+
+int fa_cache_weigh(const fa_paged_cache *cache, const void *q, const float *lse, const int32_t *page_table, int max_pages,
+                   const int32_t *seq_lens, const int32_t *cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q,
+                   int causal, float scale, const float *weights, float decay, float *out, int weights_len, void *stream) {
+    if (!lse || !out) return FA_ERR_NULL;
+    // (no attention output here: q stands in for one of no rows)
+    const Attention a = {cache, q, const_cast<void *>(q), nullptr, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq, 0,
+                         max_seqlen_q, scale, FA_F32, nullptr};
+    int rc = check_weigh(a, lse, total_q, weights, decay, out, weights_len);
+    if (rc != FA_OK) return rc;
+    DeviceInfo dev;
+    if ((rc = current_device_info(&dev)) != FA_OK) return rc;
+    WeighLaunch l;
+    l.c = *cache;
+    l.q = q;
+    l.lse = lse;
+    l.page_table = page_table;
+    l.seq_lens = seq_lens;
+    l.cu_q = cu_seqlens_q;
+    l.B = B;
+    l.Hq = Hq;
+    l.total_q = total_q;
+    l.max_q = max_seqlen_q;
+    l.max_pages = max_pages;
+    l.causal = causal ? 1 : 0;
+    l.scale = scale;
+    l.decay = decay;
+    l.weights = weights;
+    l.out = out;
+    l.weights_len = weights_len;
+    return launch_weigh(l, dev, static_cast<cudaStream_t>(stream));
+}
+
+int fa_cache_select(const float *weights, const int32_t *seq_lens, int B, int heads, int weights_len, int budget, int sink,
+                    int recent, int32_t *keep, int32_t *counts, float *kept, void *stream) {
+    if (!weights || !seq_lens || !keep || !counts) return FA_ERR_NULL;
+    if (B < 1 || heads < 1 || weights_len < 1 || budget < 1 || sink < 0 || recent < 0 ||
+        static_cast<long long>(sink) + recent > budget || weights_len > INT_MAX / 2 || budget > INT_MAX / 2 ||
+        static_cast<long long>(B) * heads > INT_MAX / 16)
+        return FA_ERR_SHAPE;
+    if (off4(weights) || off4(seq_lens) || off4(keep) || off4(counts) || off4(kept)) return FA_ERR_ALIGN;
+    const size_t rows = static_cast<size_t>(B) * heads;
+    const Span outs[3] = {{keep, rows * budget * 4}, {counts, static_cast<size_t>(B) * 4}, {kept, rows * weights_len * 4}};
+    const Span ins[2] = {{weights, rows * weights_len * 4}, {seq_lens, static_cast<size_t>(B) * 4}};
+    for (int o = 0; o < 3; ++o) {
+        for (const Span &i : ins)
+            if (meet(outs[o], i)) return FA_ERR_ALIAS;
+        if (meet(outs[o], outs[(o + 1) % 3])) return FA_ERR_ALIAS;
+    }
+    DeviceInfo dev;
+    const int rc = current_device_info(&dev);
+    if (rc != FA_OK) return rc;
+    return launch_select({weights, seq_lens, B, heads, weights_len, budget, sink, recent, keep, counts, kept}, dev,
+                         static_cast<cudaStream_t>(stream));
+}
+
+int fa_cache_keep(const fa_paged_cache *cache, const int32_t *page_table, int max_pages, const int32_t *seq_lens,
+                  const int32_t *keep, int heads, int keep_len, const int32_t *counts, const int32_t *first,
+                  const int32_t *out_table, int out_max_pages, int B, void *stream) {
+    if (!page_table || !seq_lens || !keep || !counts) return FA_ERR_NULL;
+    size_t elements = 0;
+    int rc = check_cache(cache, &elements);
+    if (rc != FA_OK) return rc;
+    const bool in_place = !out_table || out_table == page_table;
+    if (!out_table) {
+        out_table = page_table;
+        out_max_pages = max_pages;
+    }
+    if (B < 1 || max_pages < 1 || out_max_pages < 1 || keep_len < 1 || (heads != 1 && heads != cache->num_heads) ||
+        static_cast<long long>(max_pages) * cache->page_size > INT_MAX / 2 ||
+        static_cast<long long>(out_max_pages) * cache->page_size > INT_MAX / 2 || keep_len > INT_MAX / 2 ||
+        static_cast<long long>(B) * cache->num_heads > INT_MAX / 64 || (out_table == page_table && out_max_pages != max_pages))
+        return FA_ERR_SHAPE;
+    if (off4(page_table) || off4(seq_lens) || off4(keep) || off4(counts) || off4(first) || off4(out_table)) return FA_ERR_ALIGN;
+    const size_t batch = static_cast<size_t>(B);
+    const Span ins[6] = {{page_table, batch * max_pages * 4}, {seq_lens, batch * 4}, {keep, batch * heads * keep_len * 4},
+                         {counts, batch * 4},                 {first, batch * 4},    {out_table, batch * out_max_pages * 4}};
+    for (const void *pages : {cache->k_pages, cache->v_pages})
+        for (const Span &i : ins)
+            if (meet({pages, elements * 2}, i)) return FA_ERR_ALIAS;
+    if (slots_share(*cache)) return FA_ERR_ALIAS;
+    DeviceInfo dev;
+    if ((rc = current_device_info(&dev)) != FA_OK) return rc;
+    KeepLaunch l;
+    l.c = *cache;
+    l.page_table = page_table;
+    l.seq_lens = seq_lens;
+    l.keep = keep;
+    l.counts = counts;
+    l.first = first;
+    l.out_table = out_table;
+    l.max_pages = max_pages;
+    l.out_max_pages = out_max_pages;
+    l.heads = heads;
+    l.keep_len = keep_len;
+    l.B = B;
+    l.in_place = in_place;
+    return launch_keep(l, dev, static_cast<cudaStream_t>(stream));
 }
 
 int fa_decode_shared(const fa_paged_cache *cache, const void *q, void *out, const int32_t *prefix_table,

@@ -67,7 +67,7 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t a) {
     return v;
 }
 
-template <int D, int RT, bool BF16>
+template <int D, int RT, bool BF16, bool TREE>
 __global__ void __launch_bounds__(kPagedThreads, 2)
     paged_cluster_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                          const PagedParams p, const int blocks, const int size) {
@@ -173,15 +173,18 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
         if (ok) {
             r.begin(smem_u32(smem + L::kQOff), L::kQPitch);
             int lim0 = u.len - 1, lim1 = u.len - 1;  // last own key of this thread's two rows
-            if (p.causal) {
-                const int r0 = u.row0 + r.rw * 16 + r.qrow;
+            const int r0 = u.row0 + r.rw * 16 + r.qrow;
+            if (!TREE && p.causal) {
                 lim0 = min(lim0, u.len - u.nq + r0 / p.G);
                 lim1 = min(lim1, u.len - u.nq + (r0 + 8) / p.G);
             }
             for (int j = j0; j < j1; ++j) {
                 const int i = j - j0, st = i % L::kStages;
                 if (!lanes_wait(full + st, (i / L::kStages) & 1, abort_flag)) { ok = false; break; }
-                if (j < pre_tiles) {
+                if constexpr (TREE) {  // (trees have no prefix)
+                    r.tile_seen(ring + st * L::kStage, tree_seen64(p, s, r0, j * kTile), tree_seen64(p, s, r0 + 8, j * kTile),
+                                u.len - j * kTile, p.scale_log2);
+                } else if (j < pre_tiles) {
                     const int keys = prefix - j * kTile;
                     r.tile(ring + st * L::kStage, keys - 1, keys - 1, keys, p.scale_log2);
                 } else {
@@ -248,14 +251,14 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     cluster_sync();  // nobody leaves while its rows are read
 }
 
-template <int D, int RT, bool BF16>
+template <int D, int RT, bool BF16, bool TREE>
 int launch_cluster(const PagedPass &a, int size, cudaStream_t stream) {
     using L = ClusterLayout<D, RT>;
     CUtensorMap mk, mv;
     int rc;
     if ((rc = make_page_map(&mk, a.c.k_pages, a.c, kTile)) != FA_OK) return rc;
     if ((rc = make_page_map(&mv, a.c.v_pages, a.c, kTile)) != FA_OK) return rc;
-    const auto kernel = paged_cluster_kernel<D, RT, BF16>;
+    const auto kernel = paged_cluster_kernel<D, RT, BF16, TREE>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, a.device, ready)) != FA_OK) return rc;
     cudaLaunchConfig_t cfg = {};
@@ -276,12 +279,17 @@ int launch_cluster(const PagedPass &a, int size, cudaStream_t stream) {
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
+template <int D, int RT, bool BF16>
+int launch_cluster_m(const PagedPass &a, int size, cudaStream_t stream) {
+    return a.p.tree ? launch_cluster<D, RT, BF16, true>(a, size, stream) : launch_cluster<D, RT, BF16, false>(a, size, stream);
+}
+
 template <int D, bool BF16>
 int launch_cluster_d(const PagedPass &a, int size, cudaStream_t stream) {
     switch (a.plan.block_rows) {
-        case 16: return launch_cluster<D, 1, BF16>(a, size, stream);
-        case 32: return launch_cluster<D, 2, BF16>(a, size, stream);
-        default: return launch_cluster<D, 4, BF16>(a, size, stream);
+        case 16: return launch_cluster_m<D, 1, BF16>(a, size, stream);
+        case 32: return launch_cluster_m<D, 2, BF16>(a, size, stream);
+        default: return launch_cluster_m<D, 4, BF16>(a, size, stream);
     }
 }
 

@@ -38,6 +38,10 @@ struct PagedParams {
     int unit_steps;         // what a unit costs besides its key tiles, in steps
     int tile_tokens;        // paged_tiles_kernel: tokens of a query tile, of which a block has two
     int causal;             // query token i of nq sees keys j <= len - nq + i
+    // Drafted trees (not causal): a row per query token, bit j: the token sees the sequence's
+    // query token j, whose key is len - nq + j; the keys before len - nq every row sees.  Or null.
+    const uint32_t *tree;   // [total_q][tree_words]
+    int tree_words;
     float scale_log2;       // scale * log2(e)
     int out_dtype;
     // paged_cluster_kernel alone: keys that every sequence has in front of its own

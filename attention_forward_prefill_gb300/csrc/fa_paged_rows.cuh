@@ -100,10 +100,27 @@ struct PagedRows {
     // columns); the rows see keys up to lim0 and lim1 of the tile, of which the first
     // `keys` exist.
     __device__ __forceinline__ void tile(uint32_t kt, int lim0, int lim1, int keys, float scale_log2) {
-        kt += kw * NK * 128;
-        const uint32_t vt = kt + kOperand;
         lim0 -= kw * NK;
         lim1 -= kw * NK;
+        products(kt, keys, scale_log2, min(lim0, lim1) < NK - 1, [&](int key) { return key > lim0; },
+                 [&](int key) { return key > lim1; });
+    }
+    // The same where the rows see the keys whose bits are set.
+    __device__ __forceinline__ void tile_seen(uint32_t kt, uint64_t see0, uint64_t see1, int keys, float scale_log2) {
+        constexpr uint64_t kAll = NK == 64 ? ~0ull : (1ull << (NK & 63)) - 1;
+        see0 >>= kw * NK;
+        see1 >>= kw * NK;
+        products(kt, keys, scale_log2, (see0 & see1 & kAll) != kAll, [&](int key) { return !(see0 >> key & 1); },
+                 [&](int key) { return !(see1 >> key & 1); });
+    }
+
+    // hidden0 and hidden1: whether this thread's two rows do not see one of its group's keys, asked
+    // where `tail` says that any is hidden.
+    template <typename Hidden0, typename Hidden1>
+    __device__ __forceinline__ void products(uint32_t kt, int keys, float scale_log2, bool tail, Hidden0 hidden0,
+                                             Hidden1 hidden1) {
+        kt += kw * NK * 128;
+        const uint32_t vt = kt + kOperand;
         keys -= kw * NK;
         // K fragments: lane = key row lane % 8 of an 8-key block, 16-byte chunk lane / 8 of four
         const uint32_t k_row = (lane & 7) * 128;
@@ -125,7 +142,6 @@ struct PagedRows {
             }
         }
         // ---- scores in log2 units, masked; the tile's row maxima
-        const bool tail = min(lim0, lim1) < NK - 1;
         float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
         for (int nb = 0; nb < NK / 8; ++nb)
@@ -135,8 +151,8 @@ struct PagedRows {
                 s[nb][e] *= scale_log2;
                 s[nb][2 + e] *= scale_log2;
                 if (tail) {
-                    if (key > lim0) s[nb][e] = -INFINITY;
-                    if (key > lim1) s[nb][2 + e] = -INFINITY;
+                    if (hidden0(key)) s[nb][e] = -INFINITY;
+                    if (hidden1(key)) s[nb][2 + e] = -INFINITY;
                 }
                 x0 = fmaxf(x0, s[nb][e]);
                 x1 = fmaxf(x1, s[nb][2 + e]);

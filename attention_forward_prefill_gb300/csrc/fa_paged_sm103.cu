@@ -53,7 +53,7 @@ struct PagedLayout {
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-template <int D, int RT, bool BF16>
+template <int D, int RT, bool BF16, bool TREE>
 __global__ void __launch_bounds__(kPagedThreads, 2)
     paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const PagedParams p) {
@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
             if (lane == 0) mbar_arrive(u_empty + pending);
             // the last key that each of this thread's two rows sees
             int lim0 = u.len - 1, lim1 = u.len - 1;
-            if (p.causal) {
-                const int r0 = u.row0 + rows.rw * 16 + rows.qrow;
+            const int r0 = u.row0 + rows.rw * 16 + rows.qrow;
+            if (!TREE && p.causal) {
                 lim0 = min(lim0, u.len - u.nq + r0 / p.G);
                 lim1 = min(lim1, u.len - u.nq + (r0 + 8) / p.G);
             }
@@ -190,7 +190,13 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
                 const int st = tiles % L::kStages;
                 if (!lanes_wait(full + st, (tiles / L::kStages) & 1, abort_flag)) { ok = false; break; }
                 ++tiles;
-                rows.tile(ring + st * L::kStage, lim0 - j * kTile, lim1 - j * kTile, u.len - j * kTile, p.scale_log2);
+                if constexpr (TREE) {
+                    const SeqView s{u.t0, u.nq, u.len};
+                    rows.tile_seen(ring + st * L::kStage, tree_seen64(p, s, r0, j * kTile), tree_seen64(p, s, r0 + 8, j * kTile),
+                                   u.len - j * kTile, p.scale_log2);
+                } else {
+                    rows.tile(ring + st * L::kStage, lim0 - j * kTile, lim1 - j * kTile, u.len - j * kTile, p.scale_log2);
+                }
                 const bool pending = rows.loads_pending(zero);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + st + pending);
@@ -219,14 +225,14 @@ __global__ void __launch_bounds__(kPagedThreads, 2)
     }
 }
 
-template <int D, int RT, bool BF16>
+template <int D, int RT, bool BF16, bool TREE>
 int launch_rows(const PagedPass &a, cudaStream_t stream) {
     using L = PagedLayout<D, RT>;
     CUtensorMap mk, mv;
     int rc;
     if ((rc = make_page_map(&mk, a.c.k_pages, a.c, kTile)) != FA_OK) return rc;
     if ((rc = make_page_map(&mv, a.c.v_pages, a.c, kTile)) != FA_OK) return rc;
-    const auto kernel = paged_rows_kernel<D, RT, BF16>;
+    const auto kernel = paged_rows_kernel<D, RT, BF16, TREE>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, a.device, ready)) != FA_OK) return rc;
     PagedConfig cfg(a.grid, kPagedThreads, L::kSmemBytes, a.early, stream);
@@ -235,12 +241,17 @@ int launch_rows(const PagedPass &a, cudaStream_t stream) {
     return a.join ? launch_join<D, L::kRows>(a, stream) : FA_OK;
 }
 
+template <int D, int RT, bool BF16>
+int launch_rows_m(const PagedPass &a, cudaStream_t stream) {
+    return a.p.tree ? launch_rows<D, RT, BF16, true>(a, stream) : launch_rows<D, RT, BF16, false>(a, stream);
+}
+
 template <int D, bool BF16>
 int launch_rows_d(const PagedPass &a, cudaStream_t stream) {
     switch (a.plan.block_rows) {
-        case 16: return launch_rows<D, 1, BF16>(a, stream);
-        case 32: return launch_rows<D, 2, BF16>(a, stream);
-        default: return launch_rows<D, 4, BF16>(a, stream);
+        case 16: return launch_rows_m<D, 1, BF16>(a, stream);
+        case 32: return launch_rows_m<D, 2, BF16>(a, stream);
+        default: return launch_rows_m<D, 4, BF16>(a, stream);
     }
 }
 
@@ -292,6 +303,8 @@ PagedPass make_pass(const PagedLaunch &a, const DeviceInfo &dev, void *scratch) 
     p.page_shift = 0;
     while ((1 << p.page_shift) < a.c.page_size) ++p.page_shift;
     p.causal = a.causal;
+    p.tree = a.tree;
+    p.tree_words = a.tree_words;
     p.scale_log2 = a.scale * kLog2e;
     p.out_dtype = a.out_dtype;
     const PagedPlan pl = x.plan = plan_paged(a.max_q, p.G, a.c.head_dim);

@@ -88,7 +88,7 @@ __device__ __forceinline__ int tile_end(const PagedParams &p, const PagedPiece &
 // The last step of a piece reads V rows behind the sequence's last key.
 __device__ __forceinline__ bool has_tail(const PagedPiece &u) { return u.j1 * kKeys > u.len; }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const PagedParams p, const int scale_neg) {
@@ -376,7 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             int lim = u.len - 1;  // last key that the row sees
-            if (p.causal) lim = min(lim, u.len - u.nq + rr / p.G);
+            const SeqView view{u.t0, u.nq, u.len};
+            const uint32_t *see = nullptr;
+            if constexpr (TREE) see = tree_row(p, view, rr);
+            else if (p.causal) lim = min(lim, u.len - u.nq + rr / p.G);
             float m_ref = -INFINITY, l = 0.f;
             // kShift - m_ref once a key has been seen; before, masked scores still give weight 0
             float neg_m = 0.f;
@@ -395,11 +398,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_free + t);
                 }
-                const int cmax = lim - j * kKeys;  // columns behind it are masked
-                if (cmax < kKeys - 1) {
-                    const uint32_t fill = __float_as_uint(scale_neg ? INFINITY : -INFINITY);
+                const uint32_t fill = __float_as_uint(scale_neg ? INFINITY : -INFINITY);
+                if constexpr (TREE) {
+                    if ((j + 1) * kKeys > u.len - u.nq) {  // not context alone
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) sr[c >> 5][c & 31] = c > cmax ? fill : sr[c >> 5][c & 31];
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t seen = tree_seen32(p, view, see, j * kKeys + q * 32);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) sr[q][c] = seen >> c & 1 ? sr[q][c] : fill;
+                        }
+                    }
+                } else {
+                    const int cmax = lim - j * kKeys;  // columns behind it are masked
+                    if (cmax < kKeys - 1) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) sr[c >> 5][c & 31] = c > cmax ? fill : sr[c >> 5][c & 31];
+                    }
                 }
                 const float mx = scale_neg ? row_max128<true>(sr) : row_max128<false>(sr);
                 const float m_tile = mx == -INFINITY ? -INFINITY : mx * cabs;
@@ -565,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool BF16>
-int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
+template <int D, bool BF16, bool TREE>
+int launch_tiles_m(const PagedPass &a, cudaStream_t stream) {
     PagedParams p = a.p;
     using L = TilesLayout<D>;
     static_assert(L::kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -590,13 +604,18 @@ int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
     // (below 2^-126 the packed products would take it for 0)
     if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-100f;
     else if (std::fabs(p.scale_log2) < 0x1p-126f) p.scale_log2 = std::copysign(0x1p-126f, p.scale_log2);
-    const auto kernel = paged_tiles_kernel<D, BF16>;
+    const auto kernel = paged_tiles_kernel<D, BF16, TREE>;
     static std::atomic<bool> ready[kMaxDevices];
     if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, a.device, ready)) != FA_OK) return rc;
     PagedConfig cfg(a.grid, kThreads, L::kSmemBytes, a.early, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, mv, p, p.scale_log2 < 0.f ? 1 : 0);
     if (e != cudaSuccess) return cuda_fail(e);
     return a.join ? launch_join<D, 2 * kM>(a, stream) : FA_OK;
+}
+
+template <int D, bool BF16>
+int launch_tiles_d(const PagedPass &a, cudaStream_t stream) {
+    return a.p.tree ? launch_tiles_m<D, BF16, true>(a, stream) : launch_tiles_m<D, BF16, false>(a, stream);
 }
 
 }  // namespace

@@ -1,7 +1,7 @@
 /*
  * fa.h -- C ABI of libfa_gb300.so: fused scaled-dot-product attention (prefill,
- * its backward, split-K decode, and a paged key/value cache) for one NVIDIA GB300
- * (sm_103a).
+ * its backward, split-K decode, and a paged key/value cache with drafted trees and
+ * eviction) for one NVIDIA GB300 (sm_103a).
  *
  * What is computed (flash-attention-cuda README, "What is Attention?", "What is
  * Flash Attention?" and the "Kernel design" table):
@@ -60,8 +60,11 @@ typedef enum {
                               clamped (reported by fa_device_status only)         */
     FA_ERR_ALIAS = 12,     /* out overlaps an input                               */
     FA_ERR_SPLITS = 13,    /* num_splits outside [0, ceil(max_len / 64)]          */
-    FA_ERR_PAGE = 14       /* a page table entry in use was outside the cache
+    FA_ERR_PAGE = 14,      /* a page table entry in use was outside the cache
                               (reported by fa_device_status only)                 */
+    FA_ERR_INDEX = 15      /* a device-resident index (a node's parent, a token to
+                              keep) was out of range and was passed over (reported
+                              by fa_device_status only)                           */
 } fa_status;
 
 /* Flags for fa_prefill_gqa and the other prefill forms that take `flags`. */
@@ -554,6 +557,124 @@ int fa_decode_shared(const fa_paged_cache *cache, const void *q, void *out,
 size_t fa_paged_workspace_bytes(int Hq, int Hkv, int max_seqlen_q, int d, int device);
 size_t fa_shared_workspace_bytes(int B, int Hq, int Hkv, int d, int device);
 
+/* ------------------------------------------------------------- drafted trees
+ * Several continuations of a sequence checked in one pass: its drafted tokens (nodes)
+ * form a tree over the tokens in the cache (the context).  They are appended like any
+ * new tokens, at rotary positions by their depth, attend with fa_prefill_tree, and the
+ * accepted ones are moved up behind the context with fa_cache_keep. */
+
+/*
+ * The mask and the positions of drafted trees.
+ *   parents : device int32 [total_q]: the index among its own sequence's nodes of the node
+ *     that each one follows, below its own index, or -1 for one that follows the context.
+ *     Any other value counts as -1 and is recorded as FA_ERR_INDEX (fa_device_status).
+ *   mask : [total_q][mask_words], 32 * mask_words >= max_seqlen_q: bit j % 32 of word j / 32
+ *     of a node's row says that it sees node j of its sequence, itself or an ancestor.
+ *   positions : NULL, or int32 [total_q]: seq_lens[b] - n + depth of the sequence's n nodes,
+ *     the depth of one that follows the context being 0 (what fa_cache_append takes).
+ *   seq_lens : device int32 [B], the lengths with the nodes in; NULL without positions
+ *   cu_seqlens_q : device int32 [B + 1], the sequences' node offsets; clamped as in
+ *     fa_prefill_paged.  Rows outside every sequence are left alone.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE (also B * ceil(max_seqlen_q / 128) above INT_MAX),
+ * FA_ERR_ALIGN (4 bytes), FA_ERR_ALIAS, FA_ERR_ARCH, FA_ERR_CUDA.
+ */
+int fa_tree_mask(const int32_t *parents, uint32_t *mask, int mask_words,
+                 int32_t *positions, const int32_t *seq_lens,
+                 const int32_t *cu_seqlens_q, int B, int total_q,
+                 int max_seqlen_q, void *stream);
+
+/*
+ * fa_prefill_paged for drafted trees: query token i of a sequence's n sees the keys
+ * j < seq_lens[b] - n, and of the last n keys, its own tokens', those whose bits are set
+ * in its row of the mask (any bits, not only trees'; those of tokens behind the n-th count
+ * for nothing).  With more query tokens than seq_lens[b] the first tokens have no key.
+ * A row that sees no key gives zeros (lse -inf).
+ *   mask : device [total_q][mask_words], 4-byte aligned, 32 * mask_words >= max_seqlen_q
+ * The rest as fa_prefill_paged, the workspace too.
+ */
+int fa_prefill_tree(const fa_paged_cache *cache, const void *q, void *out,
+                    float *lse, const int32_t *page_table, int max_pages,
+                    const int32_t *seq_lens, const int32_t *cu_seqlens_q,
+                    const uint32_t *mask, int mask_words, int B, int Hq,
+                    int total_q, int max_seqlen_q, float scale,
+                    fa_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/* ------------------------------------------------------------------ eviction
+ * Keeping a cache at a budget by what its tokens got of the attention: fa_cache_weigh
+ * after the attention of some queries, fa_cache_select and fa_cache_keep when a sequence
+ * has grown past the budget.  The keys stay rotated as they were appended, so tokens
+ * appended later take their positions from the caller (fa_cache_append's `positions`). */
+
+/*
+ * Accumulated attention weights: for every sequence b, kv head h and key j,
+ *   out[b][h][j] = decay * weights[b][h][j] + sum of exp(scale q.k_j - lse)
+ * over the query rows of the sequence's tokens and the head's group that see the key.
+ *   q : [total_q][Hq][d] in the cache's type, lse : fp32 [total_q][Hq], both as in the
+ *     attention call over the same cache (fa_prefill_paged with the same causal and scale;
+ *     a row with lse = -inf adds nothing)
+ *   cu_seqlens_q : device int32 [B + 1], or NULL: max_seqlen_q tokens for each sequence,
+ *     total_q == B * max_seqlen_q
+ *   weights : fp32 [B][num_heads][weights_len], or NULL (nothing so far)
+ *   out : the same sizes; may be weights itself
+ * A sequence without query tokens keeps its weights as they are (out gets them).  Places at
+ * and behind seq_lens[b] are neither read nor written: zero them before their tokens come.
+ * Lengths are clamped to [0, min(max_pages * page_size, weights_len)] and recorded as
+ * FA_ERR_SEQ_LEN when they were outside.  Products, exponentials and sums are fp32, in a
+ * fixed order without atomics.  The cache's values are not read.
+ * Errors: as fa_prefill_paged; FA_ERR_SHAPE for weights_len < 1 or more than 2^40 weights,
+ * FA_ERR_SCALE for a decay that is not finite.
+ */
+int fa_cache_weigh(const fa_paged_cache *cache, const void *q, const float *lse,
+                   const int32_t *page_table, int max_pages,
+                   const int32_t *seq_lens, const int32_t *cu_seqlens_q, int B,
+                   int Hq, int total_q, int max_seqlen_q, int causal, float scale,
+                   const float *weights, float decay, float *out, int weights_len,
+                   void *stream);
+
+/*
+ * Selection: which `budget` tokens of every sequence and head stay.  Of a sequence of n
+ * tokens the first `sink` and the last `recent` stay, and of the others those with the
+ * largest weights; of equal ones (0 and -0 are equal) the first.  NaN counts as the
+ * largest weight.  With n <= budget all stay.
+ *   weights : fp32 [B][heads][weights_len], seq_lens : device int32 [B] (clamped to
+ *     [0, weights_len], recorded as FA_ERR_SEQ_LEN)
+ *   keep : int32 [B][heads][budget], the tokens that stay in rising order, then -1
+ *   counts : int32 [B]: min(n, budget), the sequence's length after fa_cache_keep
+ *   kept : NULL, or fp32 [B][heads][weights_len]: the weights of those tokens in the same
+ *     order, then zeros
+ * sink and recent >= 0, sink + recent <= budget, budget >= 1.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_ALIGN (4 bytes), FA_ERR_ALIAS, FA_ERR_ARCH,
+ * FA_ERR_CUDA.
+ */
+int fa_cache_select(const float *weights, const int32_t *seq_lens, int B,
+                    int heads, int weights_len, int budget, int sink, int recent,
+                    int32_t *keep, int32_t *counts, float *kept, void *stream);
+
+/*
+ * Moving the tokens that stay: the key and value of token keep[b][h][i] of sequence b, kv
+ * head h go to place first[b] + i, for i < counts[b].
+ *   keep : device int32 [B][heads][keep_len]; heads is the cache's, or 1: the same tokens for
+ *     all heads
+ *   counts : device int32 [B], clamped to [0, keep_len]; first : device int32 [B], or NULL: 0
+ *   out_table : NULL or page_table: in place.  Else int32 [B][out_max_pages], the pages that
+ *     the tokens go to, none of them a page that is read here.
+ * In place a token must lie at or behind the place that it goes to (rising lists do), and no
+ * two sequences may share a page that is written.  A token of keep outside [0, seq_lens[b]),
+ * or in front of its place, is passed over (FA_ERR_INDEX recorded); one whose place is outside
+ * the table, or whose new page is outside the cache, is not written; one of a page outside the
+ * cache moves as zeros (FA_ERR_SEQ_LEN, FA_ERR_PAGE).  Other slots are left as they were, and
+ * seq_lens is the caller's to set.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEAD_DIM, FA_ERR_DTYPE, FA_ERR_ALIGN, FA_ERR_ALIAS
+ * (the pages overlap an argument; k_pages and v_pages share a slot's place), FA_ERR_ARCH,
+ * FA_ERR_CUDA.
+ */
+int fa_cache_keep(const fa_paged_cache *cache, const int32_t *page_table,
+                  int max_pages, const int32_t *seq_lens, const int32_t *keep,
+                  int heads, int keep_len, const int32_t *counts,
+                  const int32_t *first, const int32_t *out_table,
+                  int out_max_pages, int B, void *stream);
+
 /* Static text for a status code ("unknown status" for other values). */
 const char *fa_status_string(int status);
 
@@ -562,8 +683,9 @@ int fa_last_cuda_error(void);
 
 /* Device-side status word of the current device: 0, FA_ERR_WATCHDOG after a
  * kernel's bounded wait ran out (this wins when several were recorded),
- * FA_ERR_SEQ_LEN after a kernel clamped a device-resident length, or FA_ERR_PAGE
- * after a page table entry in use was outside the cache.
+ * FA_ERR_SEQ_LEN after a kernel clamped a device-resident length, FA_ERR_PAGE
+ * after a page table entry in use was outside the cache, or FA_ERR_INDEX after an
+ * index on the device (a node's parent, a token to keep) was out of range.
  * Synchronises the device.  If reset is nonzero the word is cleared.  Returns
  * a negative value if it cannot be read. */
 int fa_device_status(int reset);
