@@ -35,10 +35,10 @@ struct SelectParams {
     const int *seq_lens;
     int *keep, *counts;
     float *kept;
-    int B, heads, len, budget, sink, recent;
-    int resident;  // floats of a CTA's slice that its shared memory holds
+    int heads, len, budget, sink, recent;
 };
 
+constexpr uint32_t kZeroKey = 0x80000000u;
 // Larger for larger weights; -0 is 0, and NaN comes above all.
 __device__ __forceinline__ uint32_t weight_key(float w) {
     if (w != w) return 0xfffffffeu;
@@ -50,10 +50,20 @@ __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t cluster_load(const uint32_t *at, int rank) {
-    uint32_t a, v;
+__device__ __forceinline__ uint32_t cluster_addr(const void *at, int rank) {
+    uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return a;
+}
+__device__ __forceinline__ uint4 cluster_load4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 cluster_load2(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
 }
 
@@ -66,25 +76,57 @@ __device__ __forceinline__ uint32_t scan_up(uint32_t v, int lane) {  // over the
     return v;
 }
 
-// A cluster of `size` CTAs per row, a slice of the row's tokens each.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p, const int size) {
-    extern __shared__ __align__(16) float slice[];  // [p.resident]
-    __shared__ uint32_t hist[2][kBins];
-    __shared__ uint32_t warp_sum[kSelWarps], found[2], cta_above, cta_equal;
-    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+// A cluster of `size` CTAs per row, a slice of the row's tokens each, and a run of the slice
+// each warp.  HOLDS: the slice's keys stay in shared memory; else, for rows of any length, the
+// weights are read again for every digit.
+constexpr int kHeld = 19456;  // two CTAs per SM
+template <bool HOLDS>
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, const int size) {
+    extern __shared__ __align__(16) uint32_t held[];
+    __shared__ __align__(16) uint32_t hist[2][kBins];  // counts by digit, the highest first
+    __shared__ __align__(16) uint32_t packed[2][HOLDS ? kBins / 2 : 4];
+    static_assert(kHeld < 65536);
+    __shared__ uint32_t warp_sum[kSelWarps], found[2];
+    __shared__ uint2 warp_has[kSelWarps], cta_has;  // keys above, and equal to, the last that stays
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < 2 * kBins; i += kSelThreads) hist[0][i] = 0;
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const int rank = blockIdx.x % size, row = blockIdx.x / size;
     const int b = row / p.heads;
     const int raw = __ldg(p.seq_lens + b), n = min(max(raw, 0), p.len);
     const int count = min(n, p.budget);
-    if (tid == 0 && rank == 0 && row % p.heads == 0) {
-        p.counts[b] = count;
-        if (raw != n) record_status(&g_evict_status, FA_ERR_SEQ_LEN);
-    }
     const float *w = p.weights + static_cast<long long>(row) * p.len;
     int *keep = p.keep + static_cast<long long>(row) * p.budget;
     float *kept = p.kept ? p.kept + static_cast<long long>(row) * p.len : nullptr;
     const int t = rank * kSelThreads + tid, threads = size * kSelThreads;
+    // this CTA's tokens, and this warp's
+    const int per = ((n + size - 1) / size + kSelThreads - 1) / kSelThreads * kSelThreads, run = per / kSelWarps;
+    const int w0 = min(rank * per + warp * run, n), w1 = min(w0 + run, n);
+    auto key_of = [&](int i) {
+        const uint32_t key = weight_key(__ldg(w + min(i, n - 1)));  // (loaded whatever it is: no branch between loads)
+        return i < p.sink || i >= n - p.recent ? 0xffffffffu : key;
+    };
+    uint32_t *mine = held + warp * run + lane;
+    constexpr int U = 8;  // tokens of a lane at a time
+    if constexpr (HOLDS) {
+        if (n > p.budget) {
+            for (int i0 = w0; i0 < w1; i0 += 2 * U * 32) {
+                uint32_t key[2 * U];
+#pragma unroll
+                for (int j = 0; j < 2 * U; ++j) {
+                    const int i = i0 + j * 32 + lane;
+                    key[j] = key_of(i);
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * U; ++j)
+                    if (i0 + j * 32 < w1) mine[i0 - w0 + j * 32] = key[j];
+            }
+        }
+    }
+    if (tid == 0 && rank == 0 && row % p.heads == 0) {
+        p.counts[b] = count;
+        if (raw != n) record_status(&g_evict_status, FA_ERR_SEQ_LEN);
+    }
     for (int i = count + t; i < p.budget; i += threads) keep[i] = -1;
     if (kept)
         for (int i = count + t; i < p.len; i += threads) kept[i] = 0.f;
@@ -95,20 +137,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         }
         return;
     }
-    // this CTA's tokens, and each warp's among them, in runs of whole warps
-    const int per = ((n + size - 1) / size + kSelThreads - 1) / kSelThreads * kSelThreads;
-    const int lo = min(rank * per, n), hi = min(lo + per, n);
-    const float *from = w + lo;
-    if (per <= p.resident) {
-        for (int i = tid; i < hi - lo; i += kSelThreads) slice[i] = __ldg(w + lo + i);
-        from = slice;
-    }
-    for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
-    __syncthreads();
-    auto key_of = [&](int i) {  // of token lo + i
-        const int at = lo + i;
-        return at < p.sink || at >= n - p.recent ? 0xffffffffu : weight_key(from[i]);
+    // each(f): f(token, key, whether there is one) for this warp's tokens, a lane each, in order
+    auto each = [&](auto f) {
+        for (int i0 = w0; i0 < w1; i0 += U * 32) {
+            uint32_t key[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if constexpr (HOLDS) key[j] = mine[min(i0 + j * 32, w1 - 1 & ~31) - w0];
+                else key[j] = key_of(i0 + j * 32 + lane);
+            }
+            __syncwarp();  // (f may write where these keys were)
+#pragma unroll
+            for (int j = 0; j < U; ++j) f(i0 + j * 32 + lane, key[j], i0 + j * 32 + lane < w1);
+        }
     };
+    __syncthreads();
     uint32_t top = 0, left = count;  // the digits found, and how many keys of that prefix stay
     int shift = 32;
 #pragma unroll 1
@@ -116,96 +159,127 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         const int bits = pass == 2 ? 10 : 11, above = shift;
         shift -= bits;
         uint32_t *h = hist[pass & 1];
-        for (int i0 = warp * 32; i0 < hi - lo; i0 += kSelThreads) {
-            const int i = i0 + lane;
-            const uint32_t key = i < hi - lo ? key_of(i) : 0u;
-            const bool in = i < hi - lo && (pass == 0 || key >> above == top);
-            const uint32_t bin = key >> shift & ((1u << bits) - 1u);
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
-            if (!who) continue;
-            const int one = __ffs(who) - 1;
-            const uint32_t its = __shfl_sync(0xffffffffu, bin, one);
-            // (many equal weights, zeros above all: one addition for the warp)
-            if (__all_sync(0xffffffffu, !in || bin == its)) {
-                if (lane == one) atomicAdd(h + bin, __popc(who));
-            } else if (in) {
-                atomicAdd(h + bin, 1u);
+        // (zeros, which many tokens may have, are counted apart: additions to one bin go one by one)
+        uint32_t zeros = 0;
+        each([&](int, uint32_t key, bool is) {
+            const bool in = is && (pass == 0 || key >> above == top), zero = key == kZeroKey;
+            zeros += in && zero;
+            if (in && !zero) atomicAdd(h + (~(key >> shift) & ((1u << bits) - 1u)), 1u);
+        });
+        zeros = __reduce_add_sync(0xffffffffu, zeros);
+        if (lane == 0 && zeros) atomicAdd(h + (~(kZeroKey >> shift) & ((1u << bits) - 1u)), zeros);
+        // four bins a thread, of all CTAs; on their way two of 16 bits in a word where a slice has no more
+        uint32_t c[4] = {0, 0, 0, 0};
+        if (HOLDS && size > 1) {
+            __syncthreads();
+            const uint4 own = reinterpret_cast<uint4 *>(h)[tid];
+            reinterpret_cast<uint2 *>(packed[pass & 1])[tid] = make_uint2(own.x | own.y << 16, own.z | own.w << 16);
+            cluster_sync();
+            uint2 v[kMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                v[r] = r < size ? cluster_load2(cluster_addr(packed[pass & 1] + 2 * tid, r)) : make_uint2(0, 0);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                c[0] += v[r].x & 0xffffu;
+                c[1] += v[r].x >> 16;
+                c[2] += v[r].y & 0xffffu;
+                c[3] += v[r].y >> 16;
+            }
+        } else {
+            cluster_sync();
+            for (int r = 0; r < size; ++r) {
+                const uint4 v = cluster_load4(cluster_addr(h + 4 * tid, r));
+                c[0] += v.x;
+                c[1] += v.y;
+                c[2] += v.z;
+                c[3] += v.w;
             }
         }
-        cluster_sync();
-        // bins from above, four a thread, of all CTAs
-        uint32_t c[4] = {0, 0, 0, 0};
-        for (int r = 0; r < size; ++r)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] += cluster_load(h + kBins - 1 - (tid * 4 + k), r);
-        const uint32_t mine = c[0] + c[1] + c[2] + c[3], incl = scan_up(mine, lane);
+        const uint32_t all = c[0] + c[1] + c[2] + c[3], incl = scan_up(all, lane);
         if (lane == 31) warp_sum[warp] = incl;
         // (the other CTAs have read the other table before they came here)
-        for (int i = tid; i < kBins; i += kSelThreads) hist[~pass & 1][i] = 0;
+        if (pass == 1)
+            for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
         __syncthreads();
-        uint32_t sum = incl - mine;
-        for (int k = 0; k < warp; ++k) sum += warp_sum[k];
+        uint32_t sum = incl - all;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (sum < left && left <= sum + c[k]) {
-                found[0] = kBins - 1 - (tid * 4 + k);
-                found[1] = left - sum;
+        for (int k = 0; k < kSelWarps - 1; ++k) sum += k < warp ? warp_sum[k] : 0u;
+        if (sum < left && left <= sum + all) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (sum < left && left <= sum + c[k]) {
+                    found[0] = ~static_cast<uint32_t>(4 * tid + k) & ((1u << bits) - 1u);
+                    found[1] = left - sum;
+                }
+                sum += c[k];
             }
-            sum += c[k];
         }
         __syncthreads();
         top = pass == 0 ? found[0] : top << bits | found[0];
         left = found[1];
     }
     // top: the smallest key that stays; left: how many of those equal to it
-    const int run = per / kSelWarps;  // a multiple of 32
-    const int w0 = min(warp * run, hi - lo), w1 = min(w0 + run, hi - lo);
     uint32_t above = 0, equal = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const uint32_t key = i0 + lane < w1 ? key_of(i0 + lane) : 0u;
-        above += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && key > top));
-        equal += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && key == top));
-    }
-    __shared__ uint32_t warp_above[kSelWarps], warp_equal[kSelWarps];
-    if (lane == 0) {
-        warp_above[warp] = above;
-        warp_equal[warp] = equal;
-    }
+    each([&](int, uint32_t key, bool is) {
+        above += is && key > top;
+        equal += is && key == top;
+    });
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) warp_has[warp] = make_uint2(above, equal);
     __syncthreads();
-    if (tid == 0) {
-        uint32_t x = 0, y = 0;
-        for (int k = 0; k < kSelWarps; ++k) {
-            x += warp_above[k];
-            y += warp_equal[k];
-        }
-        cta_above = x;
-        cta_equal = y;
-    }
+    uint2 has = lane < kSelWarps ? warp_has[lane] : make_uint2(0, 0);
+    has.x = scan_up(has.x, lane);
+    has.y = scan_up(has.y, lane);
+    if (tid == kSelWarps - 1) cta_has = has;
+    above = __shfl_sync(0xffffffffu, has.x, max(warp - 1, 0));
+    equal = __shfl_sync(0xffffffffu, has.y, max(warp - 1, 0));
+    if (warp == 0) above = equal = 0;
     cluster_sync();
-    above = equal = 0;
     for (int r = 0; r < rank; ++r) {
-        above += cluster_load(&cta_above, r);
-        equal += cluster_load(&cta_equal, r);
+        const uint2 v = cluster_load2(cluster_addr(&cta_has, r));
+        above += v.x;
+        equal += v.y;
     }
-    for (int k = 0; k < warp; ++k) {
-        above += warp_above[k];
-        equal += warp_equal[k];
-    }
-    const uint32_t before = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t key = i < w1 ? key_of(i) : 0u;
-        const uint32_t is_above = __ballot_sync(0xffffffffu, i < w1 && key > top);
-        const uint32_t is_equal = __ballot_sync(0xffffffffu, i < w1 && key == top);
-        const uint32_t a = above + __popc(is_above & before), e = equal + __popc(is_equal & before);
-        const bool stays = i < w1 && (key > top || (key == top && e < left));
+    // The tokens that stay, in order: first to this warp's part of the shared memory, whose keys they
+    // overtake nowhere, so that the weights are then read side by side; or out one by one.
+    const uint32_t before = (1u << lane) - 1u, to0 = above + min(equal, left);
+    uint32_t stay = 0;
+    each([&](int i, uint32_t key, bool is) {
+        const uint32_t is_above = __ballot_sync(0xffffffffu, is && key > top);
+        const uint32_t is_equal = __ballot_sync(0xffffffffu, is && key == top);
+        if (!(is_above | is_equal)) return;
+        const bool stays = is && (key > top || (key == top && equal + __popc(is_equal & before) < left));
+        const uint32_t who = __ballot_sync(0xffffffffu, stays), at = stay + __popc(who & before);
         if (stays) {
-            const uint32_t to = a + min(e, left);
-            keep[to] = lo + i;
-            if (kept) kept[to] = from[i];
+            if constexpr (HOLDS) {
+                held[warp * run + at] = i;
+            } else {
+                keep[to0 + at] = i;
+                if (kept) kept[to0 + at] = __ldg(w + i);
+            }
         }
-        above += __popc(is_above);
+        stay += __popc(who);
         equal += __popc(is_equal);
+    });
+    if constexpr (HOLDS) {
+        __syncwarp();
+        for (uint32_t k0 = lane; k0 < stay; k0 += U * 32) {
+            uint32_t i[U];
+            float x[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                i[j] = held[warp * run + min(k0 + j * 32, stay - 1)];
+                x[j] = kept ? __ldg(w + i[j]) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k0 + j * 32 < stay) {
+                    keep[to0 + k0 + j * 32] = i[j];
+                    if (kept) kept[to0 + k0 + j * 32] = x[j];
+                }
+        }
     }
     cluster_sync();  // nobody leaves while its counts are read
 }
@@ -221,8 +295,60 @@ struct KeepParams {
     int in_place;
 };
 
-// A thread moves a column of 16 bytes of a row (sequence, kv head, keys or values), kDeep tokens at a time.
+// One sequence and kv head: its list, checked token by token.
+struct KeepRow {
+    const int *list, *table, *out_table;
+    int len, first, count, mask, status;
+
+    __device__ __forceinline__ KeepRow(const KeepParams &p, int b, int h) {
+        const int raw_len = __ldg(p.seq_lens + b), raw_count = __ldg(p.counts + b), raw_first = p.first ? __ldg(p.first + b) : 0;
+        const int max_len = p.max_pages << p.page_shift, out_len = p.out_max_pages << p.page_shift;
+        len = min(max(raw_len, 0), max_len);
+        first = min(max(raw_first, 0), out_len);
+        count = min(min(max(raw_count, 0), p.keep_len), out_len - first);
+        status = len != raw_len || count != raw_count || first != raw_first ? FA_ERR_SEQ_LEN : 0;
+        list = p.keep + (static_cast<long long>(b) * p.heads + (p.heads > 1 ? h : 0)) * p.keep_len;
+        table = p.page_table + static_cast<long long>(b) * p.max_pages;
+        out_table = p.out_table + static_cast<long long>(b) * p.out_max_pages;
+        mask = (1 << p.page_shift) - 1;
+    }
+    __device__ __forceinline__ void fault(int s) {
+        if (!status) status = s;
+    }
+    // The i-th token to keep, or -1: there is none, or it is not to be moved.
+    __device__ __forceinline__ int number(const KeepParams &p, int i) {
+        if (i >= count) return -1;
+        const int src = __ldg(list + i);
+        if (src >= (p.in_place ? first + i : 0) && src < len) return src;
+        fault(FA_ERR_INDEX);
+        return -1;
+    }
+    __device__ __forceinline__ void pages(const KeepParams &p, int src, int i, int &page, int &out_page) const {
+        page = __ldg(table + (src >> p.page_shift));
+        out_page = __ldg(out_table + ((first + i) >> p.page_shift));
+    }
+    // Where it is and goes to, in elements from a head's first: to -1: nothing to do; from -1: zeros.
+    __device__ __forceinline__ void places(const KeepParams &p, int src, int i, int page, int out_page, long long &from,
+                                           long long &to) {
+        from = to = -1;
+        if (out_page < 0 || out_page >= p.num_pages) {
+            fault(FA_ERR_PAGE);
+            return;
+        }
+        to = out_page * p.page_stride + ((first + i) & mask) * p.slot_stride;
+        if (page < 0 || page >= p.num_pages) {
+            fault(FA_ERR_PAGE);
+            return;
+        }
+        from = page * p.page_stride + (src & mask) * p.slot_stride;
+        if (from == to) to = -1;
+    }
+};
+
+// Short lists: a thread moves a column of 16 bytes of a row (sequence, kv head, keys or values), kDeep
+// tokens at a time.
 constexpr int kDeep = 8;
+constexpr int kShort = 64;
 __global__ void __launch_bounds__(kKeepThreads) keep_columns_kernel(const KeepParams p) {
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const long long column = static_cast<long long>(blockIdx.x) * kKeepThreads + threadIdx.x;
@@ -231,50 +357,102 @@ __global__ void __launch_bounds__(kKeepThreads) keep_columns_kernel(const KeepPa
     if (pair >= 2LL * p.B * p.Hkv) return;
     const int h = pair / 2 % p.Hkv, b = pair / 2 / p.Hkv;
     uint16_t *base = (pair & 1 ? p.v_pages : p.k_pages) + h * p.head_stride + chunk * 8;
-    const int raw_len = __ldg(p.seq_lens + b), raw_count = __ldg(p.counts + b), raw_first = p.first ? __ldg(p.first + b) : 0;
-    const int max_len = p.max_pages << p.page_shift, out_len = p.out_max_pages << p.page_shift;
-    const int len = min(max(raw_len, 0), max_len);
-    const int first = min(max(raw_first, 0), out_len);
-    const int count = min(min(max(raw_count, 0), p.keep_len), out_len - first);
-    int status = len != raw_len || count != raw_count || first != raw_first ? FA_ERR_SEQ_LEN : 0;
-    const int *list = p.keep + (static_cast<long long>(b) * p.heads + (p.heads > 1 ? h : 0)) * p.keep_len;
-    const int *table = p.page_table + static_cast<long long>(b) * p.max_pages;
-    const int *out_table = p.out_table + static_cast<long long>(b) * p.out_max_pages;
-    const int mask = (1 << p.page_shift) - 1;
-    for (int i0 = 0; i0 < count; i0 += kDeep) {
+    KeepRow r(p, b, h);
+    for (int i0 = 0; i0 < r.count; i0 += kDeep) {
         uint4 data[kDeep];
-        uint16_t *to[kDeep];
+        long long to[kDeep];
+        int src[kDeep], page[kDeep], out_page[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) src[k] = r.number(p, i0 + k);
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+            if (src[k] >= 0) r.pages(p, src[k], i0 + k, page[k], out_page[k]);
 #pragma unroll
         for (int k = 0; k < kDeep; ++k) {
-            to[k] = nullptr;
-            const int i = i0 + k;
-            if (i >= count) continue;
-            const int src = __ldg(list + i), dst = first + i;
-            if (src < (p.in_place ? dst : 0) || src >= len) {
-                if (!status) status = FA_ERR_INDEX;
-                continue;
-            }
-            const int page = __ldg(table + (src >> p.page_shift)), out_page = __ldg(out_table + (dst >> p.page_shift));
-            if (out_page < 0 || out_page >= p.num_pages) {
-                if (!status) status = FA_ERR_PAGE;
-                continue;
-            }
-            uint16_t *at = base + out_page * p.page_stride + (dst & mask) * p.slot_stride;
-            if (page < 0 || page >= p.num_pages) {  // its tokens are zeros
-                if (!status) status = FA_ERR_PAGE;
-                data[k] = make_uint4(0, 0, 0, 0);
-            } else {
-                const uint16_t *s = base + page * p.page_stride + (src & mask) * p.slot_stride;
-                if (s == at) continue;
-                data[k] = *reinterpret_cast<const uint4 *>(s);
-            }
-            to[k] = at;
+            long long from = to[k] = -1;
+            if (src[k] >= 0) r.places(p, src[k], i0 + k, page[k], out_page[k], from, to[k]);
+            data[k] = make_uint4(0, 0, 0, 0);
+            if (to[k] >= 0 && from >= 0) data[k] = *reinterpret_cast<const uint4 *>(base + from);
         }
 #pragma unroll
         for (int k = 0; k < kDeep; ++k)
-            if (to[k]) *reinterpret_cast<uint4 *>(to[k]) = data[k];
+            if (to[k] >= 0) *reinterpret_cast<uint4 *>(base + to[k]) = data[k];
     }
-    if (status && chunk == 0) record_status(&g_evict_status, status);
+    if (r.status && chunk == 0) record_status(&g_evict_status, r.status);
+}
+
+// Long lists: a CTA moves some columns (16 << lane_shift bytes) of a row (sequence, kv head, keys
+// or values) in the order of the list, a batch of 256 >> lane_shift tokens after another, a thread 16
+// bytes of one token.  kAhead batches are on their way in shared memory ahead of the one that is
+// written, and the places of 256 tokens at a time, a token a thread, ahead of those: a token's
+// number, its pages and itself are loads that wait for one another.
+constexpr int kAhead = 7;
+constexpr int kPlaces = 4;  // lots of 256 places
+constexpr int kKeepSmem = (kAhead + 1 + kPlaces) * kKeepThreads * 16;
+
+__global__ void __launch_bounds__(kKeepThreads, 4) keep_rows_kernel(const KeepParams p, const int lane_shift) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint4 *data = reinterpret_cast<uint4 *>(smem) + threadIdx.x;  // [stage][thread]
+    longlong2 *places = reinterpret_cast<longlong2 *>(smem + (kAhead + 1) * kKeepThreads * 16);  // [lot][token]: from, to
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+    const int slices = p.chunks >> lane_shift, slice = blockIdx.x % slices, pair = blockIdx.x / slices;
+    const int h = pair / 2 % p.Hkv, b = pair / 2 / p.Hkv;
+    const int chunk = (slice << lane_shift) + (threadIdx.x & ((1 << lane_shift) - 1));
+    const int token = threadIdx.x >> lane_shift, each = kKeepThreads >> lane_shift;  // of a batch
+    uint16_t *base = (pair & 1 ? p.v_pages : p.k_pages) + h * p.head_stride + chunk * 8;
+    KeepRow r(p, b, h);
+    const int batches = (r.count + each - 1) / each;
+    int src1 = -1, src0 = -1, page0 = 0, out_page0 = 0;
+    auto number = [&](int lot) { src1 = r.number(p, lot * kKeepThreads + static_cast<int>(threadIdx.x)); };
+    auto pages = [&](int lot) {
+        src0 = src1;
+        if (src0 >= 0) r.pages(p, src0, lot * kKeepThreads + threadIdx.x, page0, out_page0);
+    };
+    auto publish = [&](int lot) {
+        longlong2 at = make_longlong2(-1, -1);
+        if (src0 >= 0) r.places(p, src0, lot * kKeepThreads + threadIdx.x, page0, out_page0, at.x, at.y);
+        places[lot % kPlaces * kKeepThreads + threadIdx.x] = at;
+    };
+    // batch n lies in lot n >> lane_shift
+    auto place = [&](int n) { return places[(n >> lane_shift) % kPlaces * kKeepThreads + (n & ((1 << lane_shift) - 1)) * each + token]; };
+    auto fetch = [&](int n) {  // (always one group of copies, empty or not)
+        if (n < batches) {
+            const longlong2 at = place(n);
+            uint4 *to = data + n % (kAhead + 1) * kKeepThreads;
+            if (at.x >= 0 && at.y >= 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(base + at.x) : "memory");
+            else
+                *to = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    number(0);
+    pages(0);
+    number(1);
+    for (int lot = 0; lot < 2; ++lot) {
+        publish(lot);
+        pages(lot + 1);
+        number(lot + 2);
+    }
+    __syncthreads();
+    for (int n = 0; n < kAhead; ++n) fetch(n);  // (of lots 0 and 1)
+    for (int n = 0; n < batches; ++n) {
+        // The first batch of lot l: lot l + 2 is published in the place of lot l - 2, and read behind the next
+        // barrier (batch n + kAhead is of lot l + 1 at most).
+        if ((n & ((1 << lane_shift) - 1)) == 0) {
+            const int lot = (n >> lane_shift) + 2;
+            publish(lot);
+            pages(lot + 1);
+            number(lot + 2);
+        }
+        fetch(n + kAhead);
+        // Batch n is here, the other threads' too: what is written now holds none of the tokens still on their way
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+        __syncthreads();
+        const long long to = place(n).y;
+        if (to >= 0) *reinterpret_cast<uint4 *>(base + to) = data[n % (kAhead + 1) * kKeepThreads];
+    }
+    if (r.status && slice == 0) record_status(&g_evict_status, r.status);
 }
 
 // ---------------------------------------------------------------- host side
@@ -302,25 +480,25 @@ struct Launch {
 
 int launch_select(const SelectLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
     const long long rows = static_cast<long long>(a.B) * a.heads;
+    // CTAs per row: as few as hold it, more where rows leave SMs idle
+    auto tokens = [&](int size) { return ((a.weights_len + size - 1LL) / size + kSelThreads - 1) / kSelThreads * kSelThreads; };
     int size = 1;
-    while (size < kMaxCluster && a.weights_len > 4096LL * size && rows * size < 2LL * dev.num_sms) size *= 2;
-    constexpr int kMostResident = 180 * 1024 / 4;
+    while (size < kMaxCluster && (tokens(size) > kHeld || (tokens(size) > 2048 && rows * size < dev.num_sms))) size *= 2;
+    const bool holds = tokens(size) <= kHeld;
+    const auto kernel = holds ? select_kernel<true> : select_kernel<false>;
     static std::atomic<bool> ready[kMaxDevices];
     if (!ready[dev.device].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostResident * 4);
+        const cudaError_t e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
         if (e != cudaSuccess) return cuda_fail(e);
         ready[dev.device].store(true, std::memory_order_release);
     }
-    const long long per = (a.weights_len + size - 1) / size;
-    const int want = static_cast<int>(std::min<long long>(kMostResident, (per + kSelThreads - 1) / kSelThreads * kSelThreads));
-    const SelectParams p = {a.weights, a.seq_lens, a.keep, a.counts, a.kept, a.B, a.heads, a.weights_len,
-                            a.budget, a.sink, a.recent, want};
-    Launch cfg(static_cast<unsigned>(rows * size), kSelThreads, want * 4, size, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, select_kernel, p, size);
+    const SelectParams p = {a.weights, a.seq_lens, a.keep, a.counts, a.kept, a.heads, a.weights_len, a.budget, a.sink, a.recent};
+    Launch cfg(static_cast<unsigned>(rows * size), kSelThreads, holds ? tokens(size) * 4 : 0, size, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, p, size);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-int launch_keep(const KeepLaunch &a, const DeviceInfo &, cudaStream_t stream) {
+int launch_keep(const KeepLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
     KeepParams p;
     p.k_pages = static_cast<uint16_t *>(a.c.k_pages);
     p.v_pages = static_cast<uint16_t *>(a.c.v_pages);
@@ -344,7 +522,16 @@ int launch_keep(const KeepLaunch &a, const DeviceInfo &, cudaStream_t stream) {
     while ((1 << p.page_shift) < a.c.page_size) ++p.page_shift;
     p.chunks = a.c.head_dim / 8;
     p.in_place = a.in_place ? 1 : 0;
-    const long long columns = 2LL * a.B * p.Hkv * p.chunks;
+    const long long rows = 2LL * a.B * p.Hkv;
+    if (a.keep_len > kShort) {
+        // 16-byte pieces of a token side by side, in as few slices of the row as fill the SMs
+        int lane_shift = p.chunks == 16 ? 4 : 3;
+        while (lane_shift > 2 && rows * (p.chunks >> lane_shift) < 4LL * dev.num_sms) --lane_shift;
+        Launch cfg(static_cast<unsigned>(rows * (p.chunks >> lane_shift)), kKeepThreads, kKeepSmem, 0, stream);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg.c, keep_rows_kernel, p, lane_shift);
+        return e == cudaSuccess ? FA_OK : cuda_fail(e);
+    }
+    const long long columns = rows * p.chunks;
     Launch cfg(static_cast<unsigned>((columns + kKeepThreads - 1) / kKeepThreads), kKeepThreads, 0, 0, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, keep_columns_kernel, p);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
