@@ -78,7 +78,8 @@ _SIGNATURES = {
     "fa_prefill_tree": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i,
                              _vp, _sz, _vp]),
     "fa_cache_weigh": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _f, _vp, _i,
-                            _vp]),
+                            _vp, _sz, _vp]),
+    "fa_weigh_workspace_bytes": (_sz, [_i]),
     "fa_cache_select": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
     "fa_cache_keep": (_i, [_vp, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _i, _i, _vp]),
     "fa_status_string": (ctypes.c_char_p, [_i]),
@@ -319,10 +320,15 @@ def fa_prefill_tree(cache, q, out, lse, page_table, max_pages, seq_lens, cu_seql
 
 
 def fa_cache_weigh(cache, q, lse, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq, total_q, max_seqlen_q,
-                   causal, scale, weights, decay, out, weights_len, stream=0) -> int:
+                   causal, scale, weights, decay, out, weights_len, workspace=None, workspace_bytes=0,
+                   stream=0) -> int:
     return load().fa_cache_weigh(ctypes.byref(cache), q, lse, page_table, max_pages, seq_lens, cu_seqlens_q, B,
                                  Hq, total_q, max_seqlen_q, int(causal), scale, weights, decay, out,
-                                 weights_len, stream)
+                                 weights_len, workspace, workspace_bytes, stream)
+
+
+def fa_weigh_workspace_bytes(device=-1) -> int:
+    return load().fa_weigh_workspace_bytes(device)
 
 
 def fa_cache_select(weights, seq_lens, B, heads, weights_len, budget, sink, recent, keep, counts, kept=None,
@@ -974,7 +980,8 @@ def _check_weights(name, t, device, shape):
 
 
 def cache_weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q=None, max_seqlen_q: int = 1,
-                causal: bool = True, scale: float | None = None, weights=None, decay: float = 1.0, out=None):
+                causal: bool = True, scale: float | None = None, weights=None, decay: float = 1.0, workspace=None,
+                out=None):
     """What every token of a paged cache got of the attention of q, added to what it had:
     out = decay * weights + the sum over the query rows that see the token of exp(scale q.k - lse).
 
@@ -1011,9 +1018,10 @@ def cache_weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q=Non
         _check_weights("out", out, device, (B, Hkv, width))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    ws, ws_bytes = _workspace(workspace, device)
     _run("fa_cache_weigh", device, cache, q.data_ptr(), lse.data_ptr(), page_table.data_ptr(), max_pages,
          seq_lens.data_ptr(), cu_ptr, B, Hq, total, int(max_seqlen_q), 1 if causal else 0, scale,
-         None if weights is None else weights.data_ptr(), decay, out.data_ptr(), out.shape[2])
+         None if weights is None else weights.data_ptr(), decay, out.data_ptr(), out.shape[2], ws, ws_bytes)
     return out
 
 

@@ -167,8 +167,11 @@ struct WeighLaunch {
     const float *weights;       // [B][heads][weights_len], or null: nothing
     float *out;                 // the same sizes
     int weights_len;
+    void *scratch;              // weigh_scratch_bytes(...), 16-byte aligned, where weigh_in_tiles
 };
 
+bool weigh_in_tiles(const WeighLaunch &a);
+size_t weigh_scratch_bytes(int num_sms);
 int launch_weigh(const WeighLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
 
 struct SelectLaunch {
@@ -201,6 +204,7 @@ int read_cluster_status(int reset);
 int read_append_status(int reset);
 int read_tree_status(int reset);
 int read_weigh_status(int reset);
+int read_weigh_tiles_status(int reset);
 int read_evict_status(int reset);
 
 }  // namespace fa

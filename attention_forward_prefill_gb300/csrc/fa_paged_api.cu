@@ -374,6 +374,11 @@ size_t fa_shared_workspace_bytes(int B, int Hq, int Hkv, int d, int device) {
     return sms < 0 ? 0 : paged_pair_scratch_bytes(B, Hq, Hkv, d, sms);
 }
 
+size_t fa_weigh_workspace_bytes(int device) {
+    const int sms = sms_of(device);
+    return sms < 0 ? 0 : weigh_scratch_bytes(sms);
+}
+
 int fa_prefill_paged(const fa_paged_cache *cache, const void *q, void *out, float *lse, const int32_t *page_table,
                      int max_pages, const int32_t *seq_lens, const int32_t *cu_seqlens_q, int B, int Hq, int total_q,
                      int max_seqlen_q, int causal, float scale, fa_dtype out_dtype, void *workspace,
@@ -435,11 +440,12 @@ int fa_prefill_tree(const fa_paged_cache *cache, const void *q, void *out, float
 
 int fa_cache_weigh(const fa_paged_cache *cache, const void *q, const float *lse, const int32_t *page_table, int max_pages,
                    const int32_t *seq_lens, const int32_t *cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q,
-                   int causal, float scale, const float *weights, float decay, float *out, int weights_len, void *stream) {
+                   int causal, float scale, const float *weights, float decay, float *out, int weights_len, void *workspace,
+                   size_t workspace_bytes, void *stream) {
     if (!lse || !out) return FA_ERR_NULL;
     // (no attention output here: q stands in for one of no rows)
     const Attention a = {cache, q, const_cast<void *>(q), nullptr, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq, 0,
-                         max_seqlen_q, scale, FA_F32, nullptr};
+                         max_seqlen_q, scale, FA_F32, workspace};
     int rc = check_weigh(a, lse, total_q, weights, decay, out, weights_len);
     if (rc != FA_OK) return rc;
     DeviceInfo dev;
@@ -462,7 +468,11 @@ int fa_cache_weigh(const fa_paged_cache *cache, const void *q, const float *lse,
     l.weights = weights;
     l.out = out;
     l.weights_len = weights_len;
-    return launch_weigh(l, dev, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    Scratch s(st);
+    if ((rc = s.take(workspace, workspace_bytes, weigh_scratch_bytes(dev.num_sms), weigh_in_tiles(l))) != FA_OK) return rc;
+    l.scratch = s.ptr;
+    return s.done(launch_weigh(l, dev, st));
 }
 
 int fa_cache_select(const float *weights, const int32_t *seq_lens, int B, int heads, int weights_len, int budget, int sink,

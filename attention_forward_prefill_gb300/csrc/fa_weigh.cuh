@@ -1,0 +1,74 @@
+// fa_weigh.cuh -- what the kernels that weigh cached tokens share.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#include "fa_paged_rows.cuh"
+#include "fa_weigh_cut.cuh"
+
+namespace fa {
+
+// The whole CTA (NT threads) adds up the sequences' steps, steps_of(sequence) for each kv head, and
+// finds its range; no more CTAs get one than there are lots of `least` steps.
+template <int NT, typename StepsOf>
+__device__ __forceinline__ void weigh_plan(const WeighParams &p, WeighStart &st, long long *warp_sum, int least, int *status,
+                                           StepsOf steps_of) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + NT - 1) / NT;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long mine = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+        mine += steps_of(weigh_seq(p, b)) * p.Hkv;
+        bad |= weigh_seq_bad(p, b);
+    }
+    if (bad && blockIdx.x == 0) record_status(status, FA_ERR_SEQ_LEN);
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, W = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const long long v = warp_sum[w];
+        if (w < warp) before += v;
+        W += v;
+    }
+    const int c = blockIdx.x, G = static_cast<int>(min(static_cast<long long>(gridDim.x), max(W / least, 1LL)));
+    const long long first = c < G ? c * W / G : W, end = c < G ? (c + 1) * W / G : W;
+    if (tid == 0) {
+        st.W = W;
+        st.G = G;
+        st.first = first;
+        st.end = end;
+    }
+    if (first < end && before <= first && first < before + mine) {
+        long long rem = first - before;
+        int b = b0;
+        for (; b < b1 - 1; ++b) {
+            const long long n = steps_of(weigh_seq(p, b)) * p.Hkv;
+            if (rem < n) break;
+            rem -= n;
+        }
+        st.b = b;
+        st.rem = rem;
+    }
+    __syncthreads();
+}
+
+// Key j's weight from the sum over its rows.
+__device__ __forceinline__ void weigh_store(const WeighParams &p, int b, int h, int nq, int key, float sum) {
+    const long long at = (static_cast<long long>(b) * p.Hkv + h) * p.len + key;
+    p.out[at] = p.in ? fmaf(nq > 0 ? p.decay : 1.f, p.in[at], sum) : sum;
+}
+// -lse in log2 units; a row that saw no key adds nothing.
+__device__ __forceinline__ float weigh_off(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+
+int launch_weigh_tiles(const WeighLaunch &a, WeighParams p, const DeviceInfo &dev, cudaStream_t stream);
+
+}  // namespace fa

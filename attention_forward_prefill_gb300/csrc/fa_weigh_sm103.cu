@@ -14,8 +14,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "fa_internal.h"
-#include "fa_paged_rows.cuh"
+#include "fa_weigh.cuh"
 
 namespace fa {
 
@@ -23,115 +22,25 @@ namespace {
 
 __device__ int g_weigh_status = 0;
 
-struct WeighParams {
-    const uint16_t *q, *k_pages;
-    const float *lse, *in;
-    float *out;
-    long long page_stride, head_stride, slot_stride;
-    const int *page_table, *seq_lens, *cu_q;
-    int B, Hq, Hkv, G, total_q, max_q, nq_each;
-    int max_pages, max_len, num_pages, page_shift, len;  // len: of a row of weights
-    int causal;
-    float scale_log2, decay;
-};
-
-struct WeighSeq {
-    int t0, nq, len;
-};
-
-__device__ __forceinline__ WeighSeq weigh_seq(const WeighParams &p, int b) {
-    WeighSeq s;
-    s.len = min(max(__ldg(p.seq_lens + b), 0), p.max_len);
-    if (p.cu_q) {
-        s.t0 = min(max(__ldg(p.cu_q + b), 0), p.total_q);
-        s.nq = min(min(max(__ldg(p.cu_q + b + 1), s.t0), p.total_q) - s.t0, p.max_q);
-    } else {
-        s.t0 = b * p.nq_each;
-        s.nq = p.nq_each;
-    }
-    return s;
-}
-__device__ __forceinline__ bool weigh_seq_bad(const WeighParams &p, int b) {
-    const int raw = __ldg(p.seq_lens + b);
-    bool bad = raw < 0 || raw > p.max_len;
-    if (p.cu_q) {
-        const int lo = __ldg(p.cu_q + b), hi = __ldg(p.cu_q + b + 1);
-        bad |= lo < 0 || hi < lo || hi > p.total_q || hi - lo > p.max_q;
-    }
-    return bad;
-}
-
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16;
 constexpr int kStepKeys = kWarps * kWarpKeys;  // keys of a CTA's step
 
-// A CTA's range of the call's steps, an equal share: the sequence that it starts in and the
-// steps of that sequence before it.
-struct WeighStart {
-    long long first, end, rem;
-    int b;
-};
-__device__ __forceinline__ int weigh_steps(const WeighParams &p, const WeighSeq &s) {
-    return (s.len + kStepKeys - 1) / kStepKeys;
-}
-__device__ void weigh_plan(const WeighParams &p, WeighStart &st, long long *warp_sum) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mine = 0;
-    bool bad = false;
-    for (int b = b0; b < b1; ++b) {
-        mine += static_cast<long long>(weigh_steps(p, weigh_seq(p, b))) * p.Hkv;
-        bad |= weigh_seq_bad(p, b);
-    }
-    if (bad && blockIdx.x == 0) record_status(&g_weigh_status, FA_ERR_SEQ_LEN);
-    long long incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    long long before = incl - mine, W = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const long long v = warp_sum[w];
-        if (w < warp) before += v;
-        W += v;
-    }
-    const long long first = blockIdx.x * W / gridDim.x, end = (blockIdx.x + 1LL) * W / gridDim.x;
-    if (tid == 0) {
-        st.first = first;
-        st.end = end;
-    }
-    if (first < end && before <= first && first < before + mine) {
-        long long rem = first - before;
-        int b = b0;
-        for (; b < b1 - 1; ++b) {
-            const long long c = static_cast<long long>(weigh_steps(p, weigh_seq(p, b))) * p.Hkv;
-            if (rem < c) break;
-            rem -= c;
-        }
-        st.b = b;
-        st.rem = rem;
-    }
-    __syncthreads();
-}
+__device__ __forceinline__ int weigh_steps(const WeighSeq &s) { return (s.len + kStepKeys - 1) / kStepKeys; }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighParams p) {
     __shared__ WeighStart st;
     __shared__ long long warp_sum[kWarps];
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
-    weigh_plan(p, st, warp_sum);
+    weigh_plan<kThreads>(p, st, warp_sum, 1, &g_weigh_status, [&](const WeighSeq &s) { return static_cast<long long>(weigh_steps(s)); });
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
     long long left = st.end - st.first;
     if (left <= 0) return;
     int b = st.b;
     WeighSeq s = weigh_seq(p, b);
-    int steps = weigh_steps(p, s);  // (of this sequence: at least one)
+    int steps = weigh_steps(s);  // (of this sequence: at least one)
     int h = static_cast<int>(st.rem / steps), j = static_cast<int>(st.rem % steps);
     for (; left > 0; --left) {
         const int k0 = j * kStepKeys + warp * kWarpKeys, key[2] = {k0 + g, k0 + g + 8};
@@ -178,8 +87,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
                     const int r = r0 + quad * 2 + e;
                     if (r >= rows) continue;
                     const float lse = __ldg(p.lse + (static_cast<long long>(s.t0) + r / p.G) * p.Hq + h * p.G + r % p.G);
-                    // (a row that saw no key adds nothing)
-                    const float off = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+                    const float off = weigh_off(lse);
                     if (r >= see[0]) sum[0] += ex2_approx(fmaf(c[e], p.scale_log2, off));
                     if (r >= see[1]) sum[1] += ex2_approx(fmaf(c[2 + e], p.scale_log2, off));
                 }
@@ -188,11 +96,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
             for (int r = 0; r < 2; ++r) {
                 sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
                 sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-                if (quad == 0 && key[r] < s.len) {
-                    const long long at = (static_cast<long long>(b) * p.Hkv + h) * p.len + key[r];
-                    const float decay = s.nq > 0 ? p.decay : 1.f;
-                    p.out[at] = p.in ? fmaf(decay, p.in[at], sum[r]) : sum[r];
-                }
+                if (quad == 0 && key[r] < s.len) weigh_store(p, b, h, s.nq, key[r], sum[r]);
             }
         }
         if (left > 1 && ++j == steps) {
@@ -201,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
                 h = 0;
                 do {
                     s = weigh_seq(p, ++b);  // steps are left, so a later sequence has some
-                    steps = weigh_steps(p, s);
+                    steps = weigh_steps(s);
                 } while (steps == 0 && b + 1 < p.B);
                 if (steps == 0) return;
             }
@@ -220,7 +124,7 @@ int launch_rows(const WeighParams &p, const DeviceInfo &dev, cudaStream_t stream
 }  // namespace
 
 int launch_weigh(const WeighLaunch &a, const DeviceInfo &dev, cudaStream_t stream) {
-    WeighParams p;
+    WeighParams p = {};
     p.q = static_cast<const uint16_t *>(a.q);
     p.k_pages = static_cast<const uint16_t *>(a.c.k_pages);
     p.lse = a.lse;
@@ -248,6 +152,7 @@ int launch_weigh(const WeighLaunch &a, const DeviceInfo &dev, cudaStream_t strea
     p.causal = a.causal;
     p.scale_log2 = a.scale * kLog2e;
     p.decay = a.decay;
+    if (weigh_in_tiles(a)) return launch_weigh_tiles(a, p, dev, stream);
     const bool bf16 = a.c.dtype == FA_BF16;
     if (a.c.head_dim == 64) return bf16 ? launch_rows<64, true>(p, dev, stream) : launch_rows<64, false>(p, dev, stream);
     return bf16 ? launch_rows<128, true>(p, dev, stream) : launch_rows<128, false>(p, dev, stream);

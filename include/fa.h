@@ -622,6 +622,8 @@ int fa_prefill_tree(const fa_paged_cache *cache, const void *q, void *out,
  * Lengths are clamped to [0, min(max_pages * page_size, weights_len)] and recorded as
  * FA_ERR_SEQ_LEN when they were outside.  Products, exponentials and sums are fp32, in a
  * fixed order without atomics.  The cache's values are not read.
+ *   workspace : NULL (the library's stream-ordered pool) or at least
+ *     fa_weigh_workspace_bytes(-1) bytes, 16-byte aligned, which one call at a time may use
  * Errors: as fa_prefill_paged; FA_ERR_SHAPE for weights_len < 1 or more than 2^40 weights,
  * FA_ERR_SCALE for a decay that is not finite.
  */
@@ -630,7 +632,11 @@ int fa_cache_weigh(const fa_paged_cache *cache, const void *q, const float *lse,
                    const int32_t *seq_lens, const int32_t *cu_seqlens_q, int B,
                    int Hq, int total_q, int max_seqlen_q, int causal, float scale,
                    const float *weights, float decay, float *out, int weights_len,
-                   void *stream);
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of fa_cache_weigh on `device` (< 0 = the current device); 0 when the
+ * device cannot be queried. */
+size_t fa_weigh_workspace_bytes(int device);
 
 /*
  * Selection: which `budget` tokens of every sequence and head stay.  Of a sequence of n
