@@ -2,7 +2,7 @@
 // Plain arithmetic: tests/test_weigh_cut_host.py compiles this file for the host.
 //
 // weigh_tiles_kernel.  A sequence's n query tokens give each kv head n * G query rows, in
-// chunks of tile_tokens whole tokens (128 rows at most).  A unit = (sequence, kv head, 256
+// chunks of tile_tokens whole tokens (kWeighRows rows at most).  A unit = (sequence, kv head, 256
 // keys); it costs kWeighUnit steps for its start and end and one for every chunk with rows that
 // see any of its keys: the chunks from the first such to the last.  The W steps of the call, in
 // the order (sequence, kv head, keys), are cut into one equal range per CTA, by every CTA for
@@ -57,6 +57,7 @@ __device__ __forceinline__ bool weigh_seq_bad(const WeighParams &p, int b) {
 }
 
 constexpr int kWeighKeys = 256;  // of a unit
+constexpr int kWeighRows = 128;  // of a chunk, at most
 constexpr int kWeighUnit = 2;
 
 // The first query token that sees key k: all of them where k lies in front of the query tokens.

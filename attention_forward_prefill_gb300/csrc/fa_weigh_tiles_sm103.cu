@@ -1,21 +1,19 @@
 // fa_weigh_tiles_sm103.cu -- what cached tokens got of the attention of many query rows.
 //
-// The sums of fa_weigh_sm103.cu, S^T = K Q^T on 128 x 128 tiles in tensor memory: a thread holds
-// a key (a lane of the accumulator) and goes through the rows (its columns), so that the sum over
-// the rows stays in the thread.  One product and one exponential per pair of key and row: at
-// d = 128 a tile takes the tensor core 256 clocks and the 16384 exponentials 512 at 32 a clock
-// and SM, which sets the time.
+// The sums of fa_weigh_sm103.cu, S^T = K Q^T on tiles of 128 keys x 128 rows in tensor memory: a
+// thread holds a key (a lane of the accumulator) and goes through the rows (its columns), so that
+// the sum over the rows stays in the thread.  One product and one exponential per pair of key and
+// row: at d = 128 the tensor core and the exponential unit (32 a clock and SM) take as long.
 //
-// CTA (one per SM, 12 warps):
-//   warps 0-3   exponentials and sums of the unit's keys 0 .. 127 (thread = key = TMEM lane)
-//   warps 4-7   of keys 128 .. 255
-//   warp  8     producer: both key tiles of a unit, then its chunks of query rows, by TMA
-//   warp  9     issues the products (one thread), owns the tensor memory
-//   warps 10-11 the chunks' log-sum-exps, in turn
-// A unit's 256 keys stay in shared memory while the chunks of 128 rows go by, so that a chunk is
+// CTA (one per SM, 20 warps):
+//   warps 0-15  exponentials and sums, four warps for each key tile of the unit and parity of the
+//               chunk (thread = key = TMEM lane)
+//   warp  16    producer: both key tiles of a unit, then its chunks of query rows, by TMA
+//   warp  17    issues the products (one thread), owns the tensor memory
+//   warps 18-19 the chunks' log-sum-exps, in turn
+// A unit's 256 keys stay in shared memory while the chunks of rows go by, so that a chunk is
 // loaded once for two products.  Every warp walks through the CTA's pieces (fa_weigh_cut.cuh) by
-// itself.  TMEM: two accumulators for each key tile, so that a product runs under the other's
-// exponentials.
+// itself.  TMEM: S of (tile, parity).
 #include <algorithm>
 #include <atomic>
 
@@ -25,35 +23,66 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsSums = 176;
-constexpr int kRegsOther = 152;
-constexpr int kMinLaunchRegs = (2 * 128 * kRegsSums + 128 * kRegsOther + kThreads - 1) / kThreads;
-constexpr int kTmaWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kM = 128;  // keys of a tile, rows of a chunk
+constexpr int kThreads = 640;
+constexpr int kTmaWarp = 16;
+constexpr int kMmaWarp = 17;
+constexpr int kOffWarp = 18;  // and the next
+constexpr int kKeyStages = 2;
+constexpr int kM = 128;          // keys of a tile
+constexpr int kRows = kWeighRows;  // rows of a chunk
 constexpr uint32_t kTmemCols = 512;
-constexpr int kKeyStages = 2, kOffStages = 4;
+constexpr int kOffStages = 2;  // (even: a stage belongs to one of the two warps that fill them)
 
 __device__ int g_weigh_tiles_status = 0;
 
 template <int D>
 struct WeighLayout {
-    static constexpr int kSlab = kM * 128;
-    static constexpr int kSlabs = D / 64;
+    static constexpr int kSlabs = D / 64, kSlab = 128 * 128;
     static constexpr int kTileBytes = kSlabs * kSlab;
-    static constexpr int kRowStages = D == 128 ? 3 : 4;
+    static constexpr int kRowStages = D == 128 ? 3 : 6;
     static constexpr int kRowsOff = 2 * kKeyStages * kTileBytes;
-    static constexpr int kOffOff = kRowsOff + kRowStages * kTileBytes;  // [kOffStages][kM] floats
-    static constexpr int kBarOff = kOffOff + kOffStages * kM * 4;
-    // k_full, k_empty, q_full, q_empty, off_full, off_empty, s_full[tile][buffer], s_free[tile][buffer], drain
-    static constexpr int kNumBars = 2 * kKeyStages + 2 * kRowStages + 2 * kOffStages + 8 + 1;
+    static constexpr int kOffOff = kRowsOff + kRowStages * kTileBytes;  // [kOffStages][kRows] floats
+    static constexpr int kOddOff = kOffOff + kOffStages * kRows * 4;    // [2][kM]: sums over the odd chunks
+    static constexpr int kBarOff = kOddOff + 2 * kM * 4;
+    // k_full, k_empty, q_full, q_empty, off_full, off_empty, s_full[tile][parity], s_free[tile][parity],
+    // sum_full[tile], sum_free[tile], drain
+    static constexpr int kNumBars = 2 * kKeyStages + 2 * kRowStages + 2 * kOffStages + 8 + 4 + 1;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kStartOff = kMiscOff + 8;
     static constexpr int kSumOff = kStartOff + (int)sizeof(WeighStart);
     static constexpr int kSmemBytes = kSumOff + 8 * (kThreads / 32);
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
+
+// The weights of 8 rows' columns s, added to two pairs of sums; MASKED: of columns [lo, hi) alone.
+// (Written stage by stage, so that eight exponentials are in flight: column by column, each waited for its
+// own chain of a load, a product and an exponential.)
+template <bool MASKED>
+__device__ __forceinline__ void add_weights(const uint32_t *s, const ulonglong2 *off, uint64_t scale2, int lo, int hi,
+                                            uint64_t (&acc)[2]) {
+    uint64_t x[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const ulonglong2 o = off[i];
+        x[2 * i] = o.x;
+        x[2 * i + 1] = o.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = ffma2(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, x[i]);
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        e[2 * i] = ex2_approx(f2_lo(x[i]));
+        e[2 * i + 1] = ex2_approx(f2_hi(x[i]));
+    }
+    if constexpr (MASKED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = i >= lo && i < hi ? e[i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i & 1] = fadd2(acc[i & 1], f2_pack(e[2 * i], e[2 * i + 1]));
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -62,7 +91,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBarOff), *k_empty = k_full + kKeyStages,
              *q_full = k_empty + kKeyStages, *q_empty = q_full + L::kRowStages, *off_full = q_empty + L::kRowStages,
-             *off_empty = off_full + kOffStages, *s_full = off_empty + kOffStages, *s_free = s_full + 4, *drain = s_free + 4;
+             *off_empty = off_full + kOffStages, *s_full = off_empty + kOffStages, *s_free = s_full + 4, *sum_full = s_free + 4,
+             *sum_free = sum_full + 2, *drain = sum_free + 2;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMiscOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMiscOff + 4);
     WeighStart *start = reinterpret_cast<WeighStart *>(smem + L::kStartOff);
@@ -82,11 +112,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kOffStages; ++i) {
             mbar_init(off_full + i, 1);
-            mbar_init(off_empty + i, 8);  // one arrival per summing warp
+            mbar_init(off_empty + i, 8);  // one arrival per summing warp of the chunk
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(s_free + i, 4);
+            mbar_init(sum_full + i, 4);  // (sum_full, then sum_free)
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -112,12 +143,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ch = 0;  // chunks so far
     bool ok = true;
     WeighCursor cur;
-    cur.begin(p, *start);
     WeighPiece u;
+    cur.begin(p, *start);
 
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ producer
-        regs_shrink<kRegsOther>();
         const uint64_t pol_k = l2_policy_evict_first(), pol_q = l2_policy_evict_last();
         const int page = 1 << p.page_shift;
         const int box = min(page, kM), boxes = kM / box;
@@ -158,36 +188,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ products
-        regs_shrink<kRegsOther>();
-        const uint32_t idesc = idesc_f16(BF16, kM, kM, false, false);
+        const uint32_t idesc = idesc_f16(BF16, kM, kRows, false, false);
         const uint32_t base = smem_u32(smem);
         while (ok && cur.next(p, u)) {
             if (u.s.nq == 0) continue;
             if (lane == 0) {
                 const uint32_t st = kc % kKeyStages;
                 const int tiles = u.u * kWeighKeys + kM < u.s.len ? 2 : 1;
-                do {
-                    if (!mbar_wait(k_full + st, (kc / kKeyStages) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
-                    for (int c = u.c0; c < u.c1; ++c) {
-                        const uint32_t qs = ch % L::kRowStages, buf = ch & 1;
-                        if (!mbar_wait(q_full + qs, (ch / L::kRowStages) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
-                        const uint64_t q_desc = sdesc_sw128(base + L::kRowsOff + qs * L::kTileBytes, 16, 1024);
-                        for (int t = 0; t < 2; ++t) {  // (a tile without keys goes through the same steps)
-                            if (ch >= 2 && !mbar_wait(s_free + t * 2 + buf, (ch / 2 - 1) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
-                            tc_fence_after();
-                            if (t < tiles)
-                                issue_qk<D>(tmem + (t * 2 + buf) * kM, sdesc_sw128(base + (2 * st + t) * L::kTileBytes, 16, 1024), q_desc, idesc);
-                            umma_commit(s_full + t * 2 + buf);
-                        }
-                        if (!ok) break;
-                        umma_commit(q_empty + qs);
-                        ++ch;
+                const uint64_t k_desc[2] = {sdesc_sw128(base + 2 * st * L::kTileBytes, 16, 1024),
+                                            sdesc_sw128(base + (2 * st + 1) * L::kTileBytes, 16, 1024)};
+                ok = mbar_wait(k_full + st, (kc / kKeyStages) & 1, abort_flag, kWatchdogNs);
+                for (int c = u.c0; ok && c < u.c1; ++c) {
+                    const uint32_t qs = ch % L::kRowStages;
+                    if (!mbar_wait(q_full + qs, (ch / L::kRowStages) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
+                    const uint64_t q_desc = sdesc_sw128(base + L::kRowsOff + qs * L::kTileBytes, 16, 1024);
+                    for (int t = 0; t < 2; ++t) {  // (a tile without keys goes through the same steps)
+                        const int at = t * 2 + (ch & 1);
+                        // polled: the product should start the moment the accumulator is free
+                        if (ch >= 2 && !mbar_spin(s_free + at, (ch / 2 - 1) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
+                        tc_fence_after();
+                        if (t < tiles) issue_qk<D>(tmem + at * kRows, k_desc[t], q_desc, idesc);
+                        umma_commit(s_full + at);
                     }
                     if (!ok) break;
-                    umma_commit(k_empty + st);
-                } while (false);
-                ++kc;
+                    umma_commit(q_empty + qs);
+                    ++ch;
+                }
+                if (ok) umma_commit(k_empty + st);
             }
+            ++kc;
             ok = __all_sync(0xffffffffu, ok);
         }
         if (lane == 0) {  // nothing may still run on the tensor core at teardown
@@ -196,13 +225,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(drain, 0, &dummy, kWatchdogNs);
         }
         __syncwarp();
-    } else if (warp >= 10) {
-        // ------------------------------------------------------------ log-sum-exps (warps 10, 11)
-        regs_shrink<kRegsOther>();
+    } else if (warp >= kOffWarp) {
+        // ------------------------------------------------------------ log-sum-exps
         int at[4];  // this lane's four rows of a chunk
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = lane * 4 + i;
+            const int c = i * 32 + lane;
             at[i] = c < tile_rows ? c / p.G * p.Hq + c % p.G : -1;
         }
         while (ok && cur.next(p, u)) {
@@ -211,24 +239,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((ch & 1) != (warp & 1)) continue;
                 const float *lse = p.lse + (static_cast<long long>(u.s.t0) + c * p.tile_tokens) * p.Hq + u.h * p.G;
                 const int rows = u.s.nq * p.G - c * tile_rows;
-                float4 v;
-                v.x = at[0] >= 0 && lane * 4 < rows ? weigh_off(__ldg(lse + at[0])) : -INFINITY;
-                v.y = at[1] >= 0 && lane * 4 + 1 < rows ? weigh_off(__ldg(lse + at[1])) : -INFINITY;
-                v.z = at[2] >= 0 && lane * 4 + 2 < rows ? weigh_off(__ldg(lse + at[2])) : -INFINITY;
-                v.w = at[3] >= 0 && lane * 4 + 3 < rows ? weigh_off(__ldg(lse + at[3])) : -INFINITY;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = at[i] >= 0 && i * 32 + lane < rows ? weigh_off(__ldg(lse + at[i])) : -INFINITY;
                 const uint32_t os = ch % kOffStages;
                 if (ch >= kOffStages && !lanes_wait(off_empty + os, (ch / kOffStages - 1) & 1, abort_flag)) { ok = false; break; }
-                *reinterpret_cast<float4 *>(offs + os * kM + lane * 4) = v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) offs[os * kRows + i * 32 + lane] = v[i];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(off_full + os);
             }
         }
     } else {
         // ------------------------------------------------------------ exponentials and sums
-        regs_grow<kRegsSums>();
-        const int t = warp >> 2;
+        const int t = warp >> 3;
+        const uint32_t odd = warp >> 2 & 1;
+        float *odd_sum = reinterpret_cast<float *>(smem + L::kOddOff) + t * kM + (warp & 3) * 32 + lane;
+        uint32_t pieces = 0;  // with rows
         const int in_unit = t * kM + (warp & 3) * 32 + lane;
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 2 * kM;
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (t * 2 + odd) * kRows;
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
         if (threadIdx.x == 0) p.open[blockIdx.x] = make_int4(-1, 0, 0, 0);
         while (ok && cur.next(p, u)) {
@@ -237,52 +266,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             float sum = 0.f;
             if (u.s.nq > 0) {
                 const int see = weigh_first_token(p, u.s, key) * p.G;  // the first row that sees the key
-                // two sums of two each
-                uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                for (int c = u.c0; c < u.c1; ++c, ++ch) {
-                    const uint32_t buf = ch & 1, os = ch % kOffStages;
-                    if (!warp_wait(off_full + os, (ch / kOffStages) & 1, abort_flag)) { ok = false; break; }
-                    if (!warp_wait(s_full + t * 2 + buf, (ch / 2) & 1, abort_flag)) { ok = false; break; }
-                    if (tile_live) {
-                        tc_fence_after();
-                        // columns of the chunk that the key is seen from: what lies outside may be anything
-                        const int first = see - c * tile_rows, end = min(u.s.nq * p.G - c * tile_rows, tile_rows);
-                        const bool all = __all_sync(0xffffffffu, first <= 0);
-                        const float4 *off4 = reinterpret_cast<const float4 *>(offs + os * kM);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t s[32];
-                            tmem_ld32(s_addr + buf * kM + q * 32, s);
-                            tmem_ld_wait();
-                            reg_fence32(s);
-                            if (q == 3) {  // S is in registers: the next one may start
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(s_free + t * 2 + buf);
-                            }
-                            const bool plain = all && end >= q * 32 + 32;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 o = off4[q * 8 + i];
-                                const uint64_t x = ffma2(f2_pack(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), scale2,
-                                                         f2_pack(o.x, o.y));
-                                const uint64_t y = ffma2(f2_pack(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), scale2,
-                                                         f2_pack(o.z, o.w));
-                                float e[4] = {ex2_approx(f2_lo(x)), ex2_approx(f2_hi(x)), ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y))};
-                                if (!plain) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const int column = q * 32 + i * 4 + k;
-                                        if (column < first || column >= end) e[k] = 0.f;
-                                    }
-                                }
-                                acc[0] = fadd2(acc[0], f2_pack(e[0], e[1]));
-                                acc[1] = fadd2(acc[1], f2_pack(e[2], e[3]));
-                            }
+                uint64_t acc[2] = {};  // two pairs of sums
+                const int c1 = u.c1, rows = u.s.nq * p.G;
+                for (int c = u.c0; c < c1; ++c, ++ch) {
+                    if ((ch & 1) != odd) continue;
+                    const uint32_t os = ch % kOffStages;
+                    if (!lanes_wait(off_full + os, (ch / kOffStages) & 1, abort_flag)) { ok = false; break; }
+                    if (!warp_wait(s_full + t * 2 + odd, (ch / 2) & 1, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                    // columns of the chunk that the key is seen from: what lies outside may be anything
+                    const int first = see - c * tile_rows, end = tile_live ? min(rows - c * tile_rows, tile_rows) : 0;
+                    const bool all = __all_sync(0xffffffffu, first <= 0);
+                    const ulonglong2 *off = reinterpret_cast<const ulonglong2 *>(offs + os * kRows);
+#pragma unroll 1
+                    for (int q = 0; q < kRows / 32; ++q) {
+                        uint32_t s[32];
+                        tmem_ld32(s_addr + q * 32, s);
+                        tmem_ld_wait();
+                        reg_fence32(s);
+                        if (q == kRows / 32 - 1) {  // S is in registers: the next one may start
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(s_free + t * 2 + odd);
                         }
-                    } else {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(s_free + t * 2 + buf);
+                        if (all && end >= q * 32 + 32) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) add_weights<false>(&s[i * 8], off + q * 8 + i * 2, scale2, 0, 8, acc);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, first - q * 32 - i * 8, end - q * 32 - i * 8, acc);
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(off_empty + os);
@@ -290,7 +304,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const uint64_t both = fadd2(acc[0], acc[1]);
                 sum = f2_lo(both) + f2_hi(both);
+                // the odd chunks' sums go to the even ones' warps
+                if (odd) {
+                    if (pieces > 0 && !lanes_wait(sum_free + t, (pieces - 1) & 1, abort_flag)) { ok = false; break; }
+                    *odd_sum = sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sum_full + t);
+                } else {
+                    if (!lanes_wait(sum_full + t, pieces & 1, abort_flag)) { ok = false; break; }
+                    sum += *odd_sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sum_free + t);
+                }
+                ++pieces;
             }
+            if (odd) continue;
             if (u.opens && u.closes) {
                 if (key < u.s.len) weigh_store(p, u.b, u.h, u.s.nq, key, sum);
             } else {
@@ -354,7 +382,7 @@ int launch_d(const WeighLaunch &a, const WeighParams &p, const DeviceInfo &dev, 
     if (rc != FA_OK) return rc;
     const auto kernel = weigh_tiles_kernel<D, BF16>;
     static std::atomic<bool> ready[kMaxDevices];
-    if ((rc = ready_kernel(kernel, L::kSmemBytes, kMinLaunchRegs, dev.device, ready)) != FA_OK) return rc;
+    if ((rc = ready_kernel(kernel, L::kSmemBytes, 0, dev.device, ready)) != FA_OK) return rc;
     PagedConfig cfg(dev.num_sms, kThreads, L::kSmemBytes, true, stream);
     cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, mq, mk, p);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -369,13 +397,13 @@ size_t part_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * kWeig
 
 bool weigh_in_tiles(const WeighLaunch &a) {
     const int group = a.Hq / a.c.num_heads;
-    return static_cast<long long>(a.max_q) * group > 64 && group <= kM && a.total_q > 0;
+    return static_cast<long long>(a.max_q) * group > 64 && group <= kRows && a.total_q > 0;
 }
 
 size_t weigh_scratch_bytes(int num_sms) { return part_bytes(num_sms) + static_cast<size_t>(num_sms) * sizeof(int4); }
 
 int launch_weigh_tiles(const WeighLaunch &a, WeighParams p, const DeviceInfo &dev, cudaStream_t stream) {
-    p.tile_tokens = kM / p.G;
+    p.tile_tokens = kRows / p.G;
     p.part = static_cast<float *>(a.scratch);
     p.open = reinterpret_cast<int4 *>(static_cast<char *>(a.scratch) + part_bytes(dev.num_sms));
     const bool bf16 = a.c.dtype == FA_BF16;

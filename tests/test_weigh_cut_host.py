@@ -38,7 +38,7 @@ int main() {
         p.max_len = max_len;
         p.total_q = cu[B];
         p.max_q = 1 << 30;
-        p.tile_tokens = 128 / G;
+        p.tile_tokens = kWeighRows / G;
         std::vector<long long> steps(B);
         long long W = 0;
         for (int b = 0; b < B; ++b) W += steps[b] = weigh_head_steps(p, weigh_seq(p, b)) * Hkv;
@@ -83,7 +83,7 @@ def cut(tmp_path_factory):
 def calls():
     rng = random.Random(4)
     some = [([1], [0, 1], 1, 1, True, 1, 152), ([0], [0, 5], 2, 4, True, 64, 152), ([0, 0], [0, 0, 0], 1, 1, False, 64, 3),
-            ([256], [0, 256], 1, 128, True, 256, 152), ([4096], [0, 4096], 8, 4, True, 4096, 152), ([100], [0, 300], 2, 7, True, 128, 9),
+            ([256], [0, 256], 1, 96, True, 256, 152), ([4096], [0, 4096], 8, 4, True, 4096, 152), ([100], [0, 300], 2, 7, True, 128, 9),
             ([131072], [0, 131072], 1, 8, True, 131072, 152)]
     for _ in range(150):
         B = rng.randint(1, 9)
@@ -91,7 +91,7 @@ def calls():
         cu = [rng.randint(0, 3)]
         for n in lens:
             cu.append(cu[-1] + rng.choice([0, 1, n, n + 5, rng.randint(0, 900)]))
-        some.append((lens, cu, rng.randint(1, 8), rng.choice([1, 2, 4, 5, 7, 8, 16, 100, 128]), rng.random() < 0.7, 4096,
+        some.append((lens, cu, rng.randint(1, 8), rng.choice([1, 2, 4, 5, 7, 8, 16, 50, 96]), rng.random() < 0.7, 4096,
                      rng.choice([1, 2, 7, 152])))
     return some
 
@@ -100,7 +100,7 @@ def test_every_chunk_once(cut):
     asked = calls()
     for (lens, cu, Hkv, G, causal, _, ctas), lines in zip(asked, cut(asked), strict=True):
         W, used = (int(x) for x in lines[0].split()[1:])
-        tokens = 128 // G
+        tokens = 96 // G
         want, total = [], 0
         for b, n in enumerate(lens):
             nq = cu[b + 1] - cu[b]
