@@ -9,10 +9,12 @@
 //   warps 0-15  exponentials and sums, four warps for each key tile of the unit and parity of the
 //               chunk (thread = key = TMEM lane)
 //   warp  16    producer: both key tiles of a unit, then its chunks of query rows, by TMA
-//   warp  17    issues the products (one thread), owns the tensor memory
-//   warps 18-19 the chunks' log-sum-exps, in turn
+//   warps 17-18 issue the products of a key tile each (one thread); the first owns the tensor memory
+//   warp  19    the chunks' log-sum-exps, four chunks at a time
 // A unit's 256 keys stay in shared memory while the chunks of rows go by, so that a chunk is
-// loaded once for two products.  Every warp walks through the CTA's pieces (fa_weigh_cut.cuh) by
+// loaded once for two products.  What a wait costs under sixteen warps that keep the issue slots
+// busy (200 to 350 clocks, whether there is anything to wait for or not) is what the split of the
+// products between two threads and the lots of log-sum-exps are for.  Every warp walks through the CTA's pieces (fa_weigh_cut.cuh) by
 // itself.  TMEM: S of (tile, parity).
 #include <algorithm>
 #include <atomic>
@@ -25,13 +27,12 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kTmaWarp = 16;
-constexpr int kMmaWarp = 17;
-constexpr int kOffWarp = 18;  // and the next
-constexpr int kKeyStages = 2;
+constexpr int kMmaWarp = 17;  // and the next
+constexpr int kOffWarp = 19;
 constexpr int kM = 128;          // keys of a tile
 constexpr int kRows = kWeighRows;  // rows of a chunk
 constexpr uint32_t kTmemCols = 512;
-constexpr int kOffStages = 2;  // (even: a stage belongs to one of the two warps that fill them)
+constexpr int kOffStages = 2, kOffChunks = 4;  // lots of log-sum-exps, and chunks of a lot
 
 __device__ int g_weigh_tiles_status = 0;
 
@@ -39,14 +40,14 @@ template <int D>
 struct WeighLayout {
     static constexpr int kSlabs = D / 64, kSlab = 128 * 128;
     static constexpr int kTileBytes = kSlabs * kSlab;
-    static constexpr int kRowStages = D == 128 ? 3 : 6;
-    static constexpr int kRowsOff = 2 * kKeyStages * kTileBytes;
-    static constexpr int kOffOff = kRowsOff + kRowStages * kTileBytes;  // [kOffStages][kRows] floats
-    static constexpr int kOddOff = kOffOff + kOffStages * kRows * 4;    // [2][kM]: sums over the odd chunks
+    static constexpr int kRowStages = D == 128 ? 4 : 8;
+    static constexpr int kRowsOff = 2 * kTileBytes;
+    static constexpr int kOffOff = kRowsOff + kRowStages * kTileBytes;  // [kOffStages][kOffChunks][kRows] floats
+    static constexpr int kOddOff = kOffOff + kOffStages * kOffChunks * kRows * 4;    // [2][kM]: sums over the odd chunks
     static constexpr int kBarOff = kOddOff + 2 * kM * 4;
-    // k_full, k_empty, q_full, q_empty, off_full, off_empty, s_full[tile][parity], s_free[tile][parity],
-    // sum_full[tile], sum_free[tile], drain
-    static constexpr int kNumBars = 2 * kKeyStages + 2 * kRowStages + 2 * kOffStages + 8 + 4 + 1;
+    // k_full[tile], k_empty[tile], q_full, q_empty, off_full, off_empty, s_full[tile][parity], s_free[tile][parity],
+    // sum_full[tile], sum_free[tile], drain[tile]
+    static constexpr int kNumBars = 4 + 2 * kRowStages + 2 * kOffStages + 8 + 4 + 2;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kStartOff = kMiscOff + 8;
     static constexpr int kSumOff = kStartOff + (int)sizeof(WeighStart);
@@ -89,10 +90,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     weigh_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const WeighParams p) {
     using L = WeighLayout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBarOff), *k_empty = k_full + kKeyStages,
-             *q_full = k_empty + kKeyStages, *q_empty = q_full + L::kRowStages, *off_full = q_empty + L::kRowStages,
-             *off_empty = off_full + kOffStages, *s_full = off_empty + kOffStages, *s_free = s_full + 4, *sum_full = s_free + 4,
-             *sum_free = sum_full + 2, *drain = sum_free + 2;
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBarOff), *k_empty = k_full + 2, *q_full = k_empty + 2,
+             *q_empty = q_full + L::kRowStages, *off_full = q_empty + L::kRowStages, *off_empty = off_full + kOffStages,
+             *s_full = off_empty + kOffStages, *s_free = s_full + 4, *sum_full = s_free + 4, *sum_free = sum_full + 2,
+             *drain = sum_free + 2;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMiscOff);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMiscOff + 4);
     WeighStart *start = reinterpret_cast<WeighStart *>(smem + L::kStartOff);
@@ -102,24 +103,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile_rows = p.tile_tokens * p.G;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kKeyStages; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(k_full + i, 1);
             mbar_init(k_empty + i, 1);
+            mbar_init(drain + i, 1);
         }
         for (int i = 0; i < L::kRowStages; ++i) {
             mbar_init(q_full + i, 1);
-            mbar_init(q_empty + i, 1);
+            mbar_init(q_empty + i, 2);  // both tiles' products
         }
         for (int i = 0; i < kOffStages; ++i) {
             mbar_init(off_full + i, 1);
-            mbar_init(off_empty + i, 8);  // one arrival per summing warp of the chunk
+            mbar_init(off_empty + i, 16);  // one arrival per summing warp
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(s_free + i, 4);
             mbar_init(sum_full + i, 4);  // (sum_full, then sum_free)
         }
-        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -158,19 +159,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int key = u.u * kWeighKeys + my_tile * kM + my_box * box;
             const bool live = my_tile < 2 && key < u.s.len;
             int id = live ? __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + (key >> p.page_shift)) : 0;
-            const uint32_t st = kc % kKeyStages;
-            if (kc >= kKeyStages && !lanes_wait(k_empty + st, (kc / kKeyStages - 1) & 1, abort_flag)) { ok = false; break; }
-            const int copies = __popc(__ballot_sync(0xffffffffu, live));
-            if (lane == 0) mbar_arrive_expect_tx(k_full + st, copies * box * 128);
-            __syncwarp();
-            if (live) {
-                if (id < 0 || id >= p.num_pages) {
-                    record_status(&g_weigh_tiles_status, FA_ERR_PAGE);
-                    id = p.num_pages;  // outside the tensor: the copy writes zeros
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (kc > 0 && !lanes_wait(k_empty + t, (kc - 1) & 1, abort_flag)) { ok = false; break; }
+                const bool mine = live && my_tile == t;
+                const int copies = __popc(__ballot_sync(0xffffffffu, mine));
+                if (lane == 0) mbar_arrive_expect_tx(k_full + t, copies * box * 128);  // (a tile without keys: none)
+                __syncwarp();
+                if (mine) {
+                    if (id < 0 || id >= p.num_pages) {
+                        record_status(&g_weigh_tiles_status, FA_ERR_PAGE);
+                        id = p.num_pages;  // outside the tensor: the copy writes zeros
+                    }
+                    tma_load_4d(smem + t * L::kTileBytes + my_slab * L::kSlab + my_box * box * 128, &map_k, k_full + t, my_slab * 64,
+                                key & (page - 1), u.h, id, pol_k);
                 }
-                tma_load_4d(smem + (2 * st + my_tile) * L::kTileBytes + my_slab * L::kSlab + my_box * box * 128, &map_k, k_full + st,
-                            my_slab * 64, key & (page - 1), u.h, id, pol_k);
             }
+            if (!ok) break;
             ++kc;
             for (int c = u.c0; c < u.c1; ++c) {
                 const uint32_t qs = ch % L::kRowStages;
@@ -186,43 +190,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ------------------------------------------------------------ products
         const uint32_t idesc = idesc_f16(BF16, kM, kRows, false, false);
-        const uint32_t base = smem_u32(smem);
+        const int t = warp - kMmaWarp;  // the key tile
+        const uint32_t rows = smem_u32(smem) + L::kRowsOff, acc = tmem + t * 2 * kRows;
+        const uint64_t k_desc = sdesc_sw128(smem_u32(smem) + t * L::kTileBytes, 16, 1024);
         while (ok && cur.next(p, u)) {
             if (u.s.nq == 0) continue;
             if (lane == 0) {
-                const uint32_t st = kc % kKeyStages;
-                const int tiles = u.u * kWeighKeys + kM < u.s.len ? 2 : 1;
-                const uint64_t k_desc[2] = {sdesc_sw128(base + 2 * st * L::kTileBytes, 16, 1024),
-                                            sdesc_sw128(base + (2 * st + 1) * L::kTileBytes, 16, 1024)};
-                ok = mbar_wait(k_full + st, (kc / kKeyStages) & 1, abort_flag, kWatchdogNs);
-                for (int c = u.c0; ok && c < u.c1; ++c) {
-                    const uint32_t qs = ch % L::kRowStages;
+                const bool has_keys = u.u * kWeighKeys + t * kM < u.s.len;
+                ok = mbar_wait(k_full + t, kc & 1, abort_flag, kWatchdogNs);
+                for (int c = u.c0; ok && c < u.c1; ++c) {  // (a tile without keys goes through the same steps)
+                    const uint32_t qs = ch % L::kRowStages, buf = ch & 1;
+                    // polled: the product should start the moment the accumulator is free
+                    if (ch >= 2 && !mbar_spin(s_free + t * 2 + buf, (ch / 2 - 1) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
                     if (!mbar_wait(q_full + qs, (ch / L::kRowStages) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
-                    const uint64_t q_desc = sdesc_sw128(base + L::kRowsOff + qs * L::kTileBytes, 16, 1024);
-                    for (int t = 0; t < 2; ++t) {  // (a tile without keys goes through the same steps)
-                        const int at = t * 2 + (ch & 1);
-                        // polled: the product should start the moment the accumulator is free
-                        if (ch >= 2 && !mbar_spin(s_free + at, (ch / 2 - 1) & 1, abort_flag, kWatchdogNs)) { ok = false; break; }
-                        tc_fence_after();
-                        if (t < tiles) issue_qk<D>(tmem + at * kRows, k_desc[t], q_desc, idesc);
-                        umma_commit(s_full + at);
-                    }
-                    if (!ok) break;
+                    tc_fence_after();
+                    if (has_keys) issue_qk<D>(acc + buf * kRows, k_desc, sdesc_sw128(rows + qs * L::kTileBytes, 16, 1024), idesc);
+                    umma_commit(s_full + t * 2 + buf);
                     umma_commit(q_empty + qs);
                     ++ch;
                 }
-                if (ok) umma_commit(k_empty + st);
+                if (ok) umma_commit(k_empty + t);
             }
             ++kc;
             ok = __all_sync(0xffffffffu, ok);
         }
         if (lane == 0) {  // nothing may still run on the tensor core at teardown
-            umma_commit(drain);
+            umma_commit(drain + t);
             int dummy = 0;
-            mbar_wait(drain, 0, &dummy, kWatchdogNs);
+            mbar_wait(drain + t, 0, &dummy, kWatchdogNs);
         }
         __syncwarp();
     } else if (warp >= kOffWarp) {
@@ -235,17 +233,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         while (ok && cur.next(p, u)) {
             if (u.s.nq == 0) continue;
-            for (int c = u.c0; c < u.c1; ++c, ++ch) {
-                if ((ch & 1) != (warp & 1)) continue;
-                const float *lse = p.lse + (static_cast<long long>(u.s.t0) + c * p.tile_tokens) * p.Hq + u.h * p.G;
-                const int rows = u.s.nq * p.G - c * tile_rows;
-                float v[4];
+            // (a lot is of one piece: the last of a piece may have fewer chunks)
+            const int rows = u.s.nq * p.G;
+            for (int c0 = u.c0; c0 < u.c1; c0 += kOffChunks, ++ch) {
+                float v[kOffChunks][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = at[i] >= 0 && i * 32 + lane < rows ? weigh_off(__ldg(lse + at[i])) : -INFINITY;
+                for (int k = 0; k < kOffChunks; ++k) {
+                    const int c = c0 + k;
+                    const float *lse = p.lse + (static_cast<long long>(u.s.t0) + c * p.tile_tokens) * p.Hq + u.h * p.G;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[k][i] = c < u.c1 && at[i] >= 0 && c * tile_rows + i * 32 + lane < rows ? weigh_off(__ldg(lse + at[i])) : -INFINITY;
+                }
                 const uint32_t os = ch % kOffStages;
                 if (ch >= kOffStages && !lanes_wait(off_empty + os, (ch / kOffStages - 1) & 1, abort_flag)) { ok = false; break; }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) offs[os * kRows + i * 32 + lane] = v[i];
+                for (int k = 0; k < kOffChunks; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) offs[(os * kOffChunks + k) * kRows + i * 32 + lane] = v[k][i];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(off_full + os);
             }
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp >> 3;
         const uint32_t odd = warp >> 2 & 1;
         float *odd_sum = reinterpret_cast<float *>(smem + L::kOddOff) + t * kM + (warp & 3) * 32 + lane;
-        uint32_t pieces = 0;  // with rows
+        uint32_t pieces = 0, lots = 0;  // pieces with rows, lots of log-sum-exps
         const int in_unit = t * kM + (warp & 3) * 32 + lane;
         const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (t * 2 + odd) * kRows;
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
@@ -268,16 +273,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int see = weigh_first_token(p, u.s, key) * p.G;  // the first row that sees the key
                 uint64_t acc[2] = {};  // two pairs of sums
                 const int c1 = u.c1, rows = u.s.nq * p.G;
-                for (int c = u.c0; c < c1; ++c, ++ch) {
+                for (int c0 = u.c0; ok && c0 < c1; c0 += kOffChunks, ++lots) {
+                  const uint32_t os = lots % kOffStages;
+                  if (!lanes_wait(off_full + os, (lots / kOffStages) & 1, abort_flag)) { ok = false; break; }
+                  for (int c = c0; c < min(c1, c0 + kOffChunks); ++c, ++ch) {
                     if ((ch & 1) != odd) continue;
-                    const uint32_t os = ch % kOffStages;
-                    if (!lanes_wait(off_full + os, (ch / kOffStages) & 1, abort_flag)) { ok = false; break; }
                     if (!warp_wait(s_full + t * 2 + odd, (ch / 2) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     // columns of the chunk that the key is seen from: what lies outside may be anything
                     const int first = see - c * tile_rows, end = tile_live ? min(rows - c * tile_rows, tile_rows) : 0;
                     const bool all = __all_sync(0xffffffffu, first <= 0);
-                    const ulonglong2 *off = reinterpret_cast<const ulonglong2 *>(offs + os * kRows);
+                    const ulonglong2 *off = reinterpret_cast<const ulonglong2 *>(offs + (os * kOffChunks + c - c0) * kRows);
 #pragma unroll 1
                     for (int q = 0; q < kRows / 32; ++q) {
                         uint32_t s[32];
@@ -298,8 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, first - q * 32 - i * 8, end - q * 32 - i * 8, acc);
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(off_empty + os);
+                  }
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(off_empty + os);
                 }
                 if (!ok) break;
                 const uint64_t both = fadd2(acc[0], acc[1]);
@@ -337,8 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // let every copy already issued land before the CTA goes away
         constexpr uint64_t kDrainNs = 200ull * 1000ull * 1000ull;
         int dummy = 0;
-        for (uint32_t i = kc > kKeyStages ? kc - kKeyStages : 0; i < kc; ++i)
-            mbar_wait(k_full + i % kKeyStages, (i / kKeyStages) & 1, &dummy, kDrainNs);
+        for (int t = 0; t < 2 && kc > 0; ++t) mbar_wait(k_full + t, (kc - 1) & 1, &dummy, kDrainNs);
         for (uint32_t i = ch > L::kRowStages ? ch - L::kRowStages : 0; i < ch; ++i)
             mbar_wait(q_full + i % L::kRowStages, (i / L::kRowStages) & 1, &dummy, kDrainNs);
         record_status(&g_weigh_tiles_status, FA_ERR_WATCHDOG);
