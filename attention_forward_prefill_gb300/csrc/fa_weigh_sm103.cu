@@ -12,7 +12,7 @@
 // products' channels; the order of the channels does not matter to q.k), and goes through
 // the query rows eight at a time.
 #include <algorithm>
-#include <cmath>
+#include <climits>
 
 #include "fa_weigh.cuh"
 
@@ -29,87 +29,163 @@ constexpr int kStepKeys = kWarps * kWarpKeys;  // keys of a CTA's step
 
 __device__ __forceinline__ int weigh_steps(const WeighSeq &s) { return (s.len + kStepKeys - 1) / kStepKeys; }
 
-template <int D, bool BF16>
+// A warp's 16 keys of a step: where they are, and what they bring.
+template <int D>
+struct WeighKeys {
+    uint4 k[2][D / 32];  // keys k0 + lane / 4 and the one 8 behind it: eight channels a lane and 32 channels
+    float old[2];        // their weights so far, in the lanes that write them
+    int b, h, k0;
+    WeighSeq s;
+};
+
+// Walks through a CTA's steps.
+struct WeighWalk {
+    WeighSeq s;
+    int b, h, j, steps;
+    long long left;
+
+    __device__ __forceinline__ void begin(const WeighParams &p, const WeighStart &st) {
+        left = st.end - st.first;
+        if (left <= 0) return;
+        b = st.b;
+        s = weigh_seq(p, b);
+        steps = weigh_steps(s);  // (at least one)
+        h = static_cast<int>(st.rem / steps);
+        j = static_cast<int>(st.rem % steps);
+    }
+    __device__ __forceinline__ void next(const WeighParams &p) {
+        if (--left <= 0 || ++j < steps) return;
+        j = 0;
+        if (++h < p.Hkv) return;
+        h = 0;
+        do {
+            s = weigh_seq(p, ++b);  // steps are left, so a later sequence has some
+            steps = weigh_steps(s);
+        } while (steps == 0 && b + 1 < p.B);
+        if (steps == 0) left = 0;
+    }
+};
+
+// FEW: at most 8 rows a kv head (one token of up to 8 heads), which stay in registers while the warp's
+// keys are of one sequence and head.  HBM-bound: the next step's keys are on their way while a step is
+// computed, and its page's number while they are.
+template <int D, bool BF16, bool FEW>
 __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighParams p) {
     __shared__ WeighStart st;
     __shared__ long long warp_sum[kWarps];
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     weigh_plan<kThreads>(p, st, warp_sum, 1, &g_weigh_status, [&](const WeighSeq &s) { return static_cast<long long>(weigh_steps(s)); });
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
-    long long left = st.end - st.first;
-    if (left <= 0) return;
-    int b = st.b;
-    WeighSeq s = weigh_seq(p, b);
-    int steps = weigh_steps(s);  // (of this sequence: at least one)
-    int h = static_cast<int>(st.rem / steps), j = static_cast<int>(st.rem % steps);
-    for (; left > 0; --left) {
-        const int k0 = j * kStepKeys + warp * kWarpKeys, key[2] = {k0 + g, k0 + g + 8};
-        if (k0 < s.len) {
-            // the keys, eight channels a lane and 32 channels: places 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9
-            // of two products
-            uint4 kf[2][D / 32];
+    WeighWalk walk;
+    walk.begin(p, st);
+    if (walk.left <= 0) return;
+    // the page of a step's keys (16 of one page), or -1 without keys
+    auto page_of = [&](const WeighWalk &w) {
+        const int k0 = w.j * kStepKeys + warp * kWarpKeys;
+        return w.left > 0 && k0 < w.s.len ? __ldg(p.page_table + static_cast<long long>(w.b) * p.max_pages + (k0 >> p.page_shift)) : -1;
+    };
+    auto load = [&](const WeighWalk &w, int page, WeighKeys<D> &x) {
+        x.b = w.b;
+        x.h = w.h;
+        x.s = w.s;
+        x.k0 = w.left > 0 ? w.j * kStepKeys + warp * kWarpKeys : INT_MAX / 2;
+        const bool there = page >= 0 && page < p.num_pages;
+        if (x.k0 < x.s.len && !there) record_status(&g_weigh_status, FA_ERR_PAGE);  // zeros
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint16_t *row = nullptr;
-                if (key[r] < s.len) {
-                    const int page = __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + (key[r] >> p.page_shift));
-                    if (page < 0 || page >= p.num_pages) record_status(&g_weigh_status, FA_ERR_PAGE);  // zeros
-                    else row = p.k_pages + page * p.page_stride + h * p.head_stride +
-                               (key[r] & ((1 << p.page_shift) - 1)) * p.slot_stride + quad * 8;
-                }
+        for (int r = 0; r < 2; ++r) {
+            const int key = x.k0 + g + 8 * r;
+            // the eight channels take places 2 quad, 2 quad + 1, 2 quad + 8 and 2 quad + 9 of two products
+            const uint16_t *row = p.k_pages + page * p.page_stride + w.h * p.head_stride +
+                                  (key & ((1 << p.page_shift) - 1)) * p.slot_stride + quad * 8;
+            const bool live = there && key < x.s.len;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c)
-                    kf[r][c] = row ? __ldg(reinterpret_cast<const uint4 *>(row + c * 32)) : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 32; ++c)
+                x.k[r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(row + c * 32)) : make_uint4(0, 0, 0, 0);
+            x.old[r] = p.in && quad == 0 && key < x.s.len
+                           ? __ldcg(p.in + (static_cast<long long>(w.b) * p.Hkv + w.h) * p.len + key) : 0.f;
+        }
+    };
+    uint4 z[FEW ? D / 32 : 1];
+    float lse[2] = {-INFINITY, -INFINITY};
+    int z_of = -1;  // the sequence and head of z
+    auto rows_of = [&](const WeighKeys<D> &x, int r0, uint4 (&q)[D / 32]) {  // 8 rows from r0 on, eight channels a lane
+        const int rq = min(r0 + g, x.s.nq * p.G - 1);
+        const uint16_t *qr = p.q + ((static_cast<long long>(x.s.t0) + rq / p.G) * p.Hq + x.h * p.G + rq % p.G) * D + quad * 8;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) q[i] = __ldg(reinterpret_cast<const uint4 *>(qr + i * 32));
+    };
+    auto off_of = [&](const WeighKeys<D> &x, int r) {
+        return r < x.s.nq * p.G ? weigh_off(__ldg(p.lse + (static_cast<long long>(x.s.t0) + r / p.G) * p.Hq + x.h * p.G + r % p.G)) : -INFINITY;
+    };
+    auto products = [&](const WeighKeys<D> &x, const uint4 (&q)[D / 32], float (&c)[4]) {
+        c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint32_t lo[4] = {x.k[0][i].x, x.k[1][i].x, x.k[0][i].y, x.k[1][i].y};
+            const uint32_t hi[4] = {x.k[0][i].z, x.k[1][i].z, x.k[0][i].w, x.k[1][i].w};
+            mma_16816<BF16>(c, lo, q[i].x, q[i].y);
+            mma_16816<BF16>(c, hi, q[i].z, q[i].w);
+        }
+    };
+    auto compute = [&](const WeighKeys<D> &x) {
+        if (x.k0 >= x.s.len) return;
+        const int rows = x.s.nq * p.G, key[2] = {x.k0 + g, x.k0 + g + 8};
+        // rows from `see` on see the key
+        const int see[2] = {weigh_first_token(p, x.s, key[0]) * p.G, weigh_first_token(p, x.s, key[1]) * p.G};
+        float sum[2] = {0.f, 0.f}, c[4];
+        auto add = [&](int r0, float off0, float off1) {
+            const float off[2] = {off0, off1};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + quad * 2 + e;
+                if (r < rows && r >= see[0]) sum[0] += ex2_approx(fmaf(c[e], p.scale_log2, off[e]));
+                if (r < rows && r >= see[1]) sum[1] += ex2_approx(fmaf(c[2 + e], p.scale_log2, off[e]));
             }
-            // rows from `see` on see the key
-            const int rows = s.nq * p.G, past = s.len - s.nq;
-            int see[2] = {0, 0};
-            if (p.causal) {
-                see[0] = min(max(key[0] - past, 0), s.nq) * p.G;
-                see[1] = min(max(key[1] - past, 0), s.nq) * p.G;
-            }
-            const int r_first = p.causal ? min(max(k0 - past, 0), s.nq) * p.G & ~7 : 0;
-            float sum[2] = {0.f, 0.f};
-            for (int r0 = r_first; r0 < rows; r0 += 8) {
-                const int rq = min(r0 + g, rows - 1);
-                const uint16_t *qr = p.q + ((static_cast<long long>(s.t0) + rq / p.G) * p.Hq + h * p.G + rq % p.G) * D + quad * 8;
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint4 z = __ldg(reinterpret_cast<const uint4 *>(qr + i * 32));
-                    const uint32_t lo[4] = {kf[0][i].x, kf[1][i].x, kf[0][i].y, kf[1][i].y};
-                    const uint32_t hi[4] = {kf[0][i].z, kf[1][i].z, kf[0][i].w, kf[1][i].w};
-                    mma_16816<BF16>(c, lo, z.x, z.y);
-                    mma_16816<BF16>(c, hi, z.z, z.w);
+        };
+        if constexpr (FEW) {
+            if (rows > 0) {
+                if (z_of != x.b * p.Hkv + x.h) {
+                    z_of = x.b * p.Hkv + x.h;
+                    rows_of(x, 0, z);
+                    lse[0] = off_of(x, quad * 2);
+                    lse[1] = off_of(x, quad * 2 + 1);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = r0 + quad * 2 + e;
-                    if (r >= rows) continue;
-                    const float lse = __ldg(p.lse + (static_cast<long long>(s.t0) + r / p.G) * p.Hq + h * p.G + r % p.G);
-                    const float off = weigh_off(lse);
-                    if (r >= see[0]) sum[0] += ex2_approx(fmaf(c[e], p.scale_log2, off));
-                    if (r >= see[1]) sum[1] += ex2_approx(fmaf(c[2 + e], p.scale_log2, off));
-                }
+                products(x, z, c);
+                add(0, lse[0], lse[1]);
             }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-                sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-                if (quad == 0 && key[r] < s.len) weigh_store(p, b, h, s.nq, key[r], sum[r]);
+        } else {
+            for (int r0 = weigh_first_token(p, x.s, x.k0) * p.G & ~7; r0 < rows; r0 += 8) {
+                uint4 q[D / 32];
+                rows_of(x, r0, q);
+                const float off0 = off_of(x, r0 + quad * 2), off1 = off_of(x, r0 + quad * 2 + 1);
+                products(x, q, c);
+                add(r0, off0, off1);
             }
         }
-        if (left > 1 && ++j == steps) {
-            j = 0;
-            if (++h == p.Hkv) {
-                h = 0;
-                do {
-                    s = weigh_seq(p, ++b);  // steps are left, so a later sequence has some
-                    steps = weigh_steps(s);
-                } while (steps == 0 && b + 1 < p.B);
-                if (steps == 0) return;
-            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+            if (quad == 0 && key[r] < x.s.len)
+                p.out[(static_cast<long long>(x.b) * p.Hkv + x.h) * p.len + key[r]] =
+                    p.in ? fmaf(x.s.nq > 0 ? p.decay : 1.f, x.old[r], sum[r]) : sum[r];
         }
+    };
+    WeighKeys<D> one, two;
+    load(walk, page_of(walk), one);
+    walk.next(p);
+    int page = page_of(walk);
+    for (;;) {
+        load(walk, page, two);
+        if (walk.left > 0) walk.next(p);
+        page = page_of(walk);
+        compute(one);
+        if (two.k0 == INT_MAX / 2) break;
+        load(walk, page, one);
+        if (walk.left > 0) walk.next(p);
+        page = page_of(walk);
+        compute(two);
+        if (one.k0 == INT_MAX / 2) break;
     }
 }
 
@@ -117,7 +193,8 @@ template <int D, bool BF16>
 int launch_rows(const WeighParams &p, const DeviceInfo &dev, cudaStream_t stream) {
     const long long most = static_cast<long long>(p.B) * p.Hkv * ((p.max_len + kStepKeys - 1) / kStepKeys);
     PagedConfig cfg(static_cast<unsigned>(std::min<long long>(most, 2LL * dev.num_sms)), kThreads, 0, true, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, weigh_rows_kernel<D, BF16>, p);
+    const bool few = static_cast<long long>(p.max_q) * p.G <= 8 && static_cast<long long>(p.B) * p.Hkv <= INT_MAX;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, few ? weigh_rows_kernel<D, BF16, true> : weigh_rows_kernel<D, BF16, false>, p);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
