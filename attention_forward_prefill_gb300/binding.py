@@ -136,7 +136,7 @@ _calls = None
 
 class _InPython:
     """In the place of _paged_calls where it is not built: every call goes through the checks in Python."""
-    append = decode = prefill = shared = staticmethod(lambda *args: NotImplemented)
+    append = decode = prefill = shared = mask = tree = weigh = select = keep = staticmethod(lambda *args: NotImplemented)
 
 
 def _fast():
@@ -150,7 +150,8 @@ def _fast():
             _calls = _InPython
             return _calls
         _paged_calls.init(_torch(), FaError, *(ctypes.cast(getattr(lib, n), _vp).value for n in (
-            "fa_cache_append", "fa_decode_paged", "fa_prefill_paged", "fa_decode_shared")))
+            "fa_cache_append", "fa_decode_paged", "fa_prefill_paged", "fa_decode_shared", "fa_tree_mask",
+            "fa_prefill_tree", "fa_cache_weigh", "fa_cache_select", "fa_cache_keep")))
         _calls = _paged_calls
     return _calls
 
@@ -851,9 +852,9 @@ def prefill_paged(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_s
     lse: optional fp32 [T, Hq] that receives the row log-sum-exp.  Returns [T, Hq, d]; rows
     outside every sequence are not written.
     """
-    if out_dtype is None and workspace is None and lse is None:
+    if out_dtype is None and workspace is None:
         done = (_calls or _fast()).prefill(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal,
-                                           scale, out)
+                                           scale, out, lse)
         if done is not NotImplemented:
             return done
     cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
@@ -914,6 +915,9 @@ def tree_mask(parents, cu_seqlens_q, max_seqlen_q: int, seq_lens=None):
     nodes' positions, int32 [T], as cache_append takes them; None without.  Rows outside every
     sequence are not written.
     """
+    done = (_calls or _fast()).mask(parents, cu_seqlens_q, max_seqlen_q, seq_lens)
+    if done is not NotImplemented:
+        return done
     torch = _torch()
     device = parents.device
     if not parents.is_cuda:
@@ -943,6 +947,11 @@ def prefill_tree(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_se
 
     The rest as prefill_paged; the keys and values of the query tokens are in the cache already.
     """
+    if out_dtype is None and workspace is None:
+        done = (_calls or _fast()).tree(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, mask, scale,
+                                        out, lse)
+        if done is not NotImplemented:
+            return done
     cache, d, device, B, max_pages, scale, code, out = _paged_args(q, k_pages, v_pages, page_table, seq_lens, scale,
                                                                    out_dtype, out)
     if q.dim() != 3 or q.shape[2] != d:
@@ -991,6 +1000,11 @@ def cache_weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q=Non
     of weights or of the page table.  Places behind a sequence's last token are neither read nor
     written (zeros in a new array).  A sequence without query tokens keeps its weights.
     """
+    if workspace is None:
+        done = (_calls or _fast()).weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal,
+                                         scale, weights, decay, out)
+        if done is not NotImplemented:
+            return done
     torch = _torch()
     cache, Hkv, d = _pages(k_pages, v_pages)
     device = k_pages.device
@@ -1035,6 +1049,9 @@ def cache_select(weights, seq_lens, budget: int, sink: int = 0, recent: int = 0)
     order, then -1; counts, int32 [B], the new lengths; and the weights of those tokens in the same
     order, zeros behind, in the shape of weights.
     """
+    done = (_calls or _fast()).select(weights, seq_lens, budget, sink, recent)
+    if done is not NotImplemented:
+        return done
     torch = _torch()
     if not weights.is_cuda:
         raise ValueError("weights must be a CUDA tensor")
@@ -1042,7 +1059,9 @@ def cache_select(weights, seq_lens, budget: int, sink: int = 0, recent: int = 0)
     _check_weights("weights", weights, device, (None, None, None))
     B, heads, width = weights.shape
     _check_ints(device, "seq_lens", seq_lens, (B,))
-    keep = torch.empty((B, heads, max(int(budget), 0)), dtype=torch.int32, device=device)
+    if budget < 1:
+        raise FaError(FA_ERR_SHAPE, "fa_cache_select")
+    keep = torch.empty((B, heads, int(budget)), dtype=torch.int32, device=device)
     counts = torch.empty_like(seq_lens)
     kept = torch.empty_like(weights)
     _run("fa_cache_select", device, weights.data_ptr(), seq_lens.data_ptr(), B, heads, width, int(budget), int(sink),
@@ -1059,6 +1078,9 @@ def cache_keep(k_pages, v_pages, page_table, seq_lens, keep, counts, first=None,
     rising lists do.  out_table int32 [B, pages]: into these pages instead, none of which holds
     a token that is read.  The new lengths (first + counts) are the caller's to set.
     """
+    done = (_calls or _fast()).keep(k_pages, v_pages, page_table, seq_lens, keep, counts, first, out_table)
+    if done is not NotImplemented:
+        return done
     cache, Hkv, _ = _pages(k_pages, v_pages)
     device = k_pages.device
     B, max_pages = _tables(device, page_table, seq_lens)

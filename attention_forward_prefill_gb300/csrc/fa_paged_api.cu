@@ -442,9 +442,10 @@ int fa_cache_weigh(const fa_paged_cache *cache, const void *q, const float *lse,
                    const int32_t *seq_lens, const int32_t *cu_seqlens_q, int B, int Hq, int total_q, int max_seqlen_q,
                    int causal, float scale, const float *weights, float decay, float *out, int weights_len, void *workspace,
                    size_t workspace_bytes, void *stream) {
-    if (!lse || !out) return FA_ERR_NULL;
-    // (no attention output here: q stands in for one of no rows)
-    const Attention a = {cache, q, const_cast<void *>(q), nullptr, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq, 0,
+    if (!out || (total_q != 0 && (!q || !lse)) || !cache) return FA_ERR_NULL;
+    // (no attention output here, and without query tokens no queries: something stands in for no rows of them)
+    void *none = q ? const_cast<void *>(q) : cache->k_pages;
+    const Attention a = {cache, none, none, nullptr, page_table, max_pages, seq_lens, cu_seqlens_q, B, Hq, 0,
                          max_seqlen_q, scale, FA_F32, workspace};
     int rc = check_weigh(a, lse, total_q, weights, decay, out, weights_len);
     if (rc != FA_OK) return rc;

@@ -39,6 +39,16 @@ static int (*c_prefill)(const fa_paged_cache *, const void *, void *, float *, c
                         const int32_t *, int, int, int, int, int, float, fa_dtype, void *, size_t, void *);
 static int (*c_shared)(const fa_paged_cache *, const void *, void *, const int32_t *, int, const int32_t *,
                        const int32_t *, int, const int32_t *, int, int, float, fa_dtype, void *, size_t, void *);
+static int (*c_mask)(const int32_t *, uint32_t *, int, int32_t *, const int32_t *, const int32_t *, int, int, int, void *);
+static int (*c_tree)(const fa_paged_cache *, const void *, void *, float *, const int32_t *, int, const int32_t *,
+                     const int32_t *, const uint32_t *, int, int, int, int, int, float, fa_dtype, void *, size_t, void *);
+static int (*c_weigh)(const fa_paged_cache *, const void *, const float *, const int32_t *, int, const int32_t *,
+                      const int32_t *, int, int, int, int, int, float, const float *, float, float *, int, void *, size_t,
+                      void *);
+static int (*c_select)(const float *, const int32_t *, int, int, int, int, int, int, int32_t *, int32_t *, float *, void *);
+static int (*c_keep)(const fa_paged_cache *, const int32_t *, int, const int32_t *, const int32_t *, int, int,
+                     const int32_t *, const int32_t *, const int32_t *, int, int, void *);
+static PyObject *s_new_empty;
 static PyObject *s_shape, *s_stride, *s_dtype, *s_get_device, *s_data_ptr, *s_memory_format, *s_names;
 
 static int longs(PyObject *tuple, long long *out, int *n) {
@@ -266,15 +276,64 @@ static PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return result(rc, "fa_decode_paged", out);
 }
 
-/* prefill(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal, scale, out) */
+/* fp32, contiguous, nd dimensions, on the device */
+static int floats(PyObject *o, Tensor *t, int nd, long device) {
+    if (!read_tensor(o, t) || t->dtype != t_f32 || t->nd != nd || t->device != device || !contiguous(t)) return 0;
+    for (int i = 0; i < nd; ++i)
+        if (!fits(t->size[i])) return 0;
+    return 1;
+}
+
+/* an int that fits */
+static int whole(PyObject *o, int *v) {
+    if (!PyLong_CheckExact(o)) return 0;
+    const long long x = PyLong_AsLongLong(o);
+    if ((x == -1 && PyErr_Occurred()) || x < INT32_MIN || x > INT32_MAX) {
+        PyErr_Clear();
+        return 0;
+    }
+    *v = (int)x;
+    return 1;
+}
+
+/* torch.empty_like(like), contiguous as like is.  A new reference, or NULL with no exception. */
+static PyObject *like(PyObject *o, void **ptr) {
+    PyObject *out = PyObject_CallOneArg(t_empty_like, o), *p = NULL;
+    if (out && (p = PyObject_CallMethodNoArgs(out, s_data_ptr))) {
+        *ptr = PyLong_AsVoidPtr(p);
+        Py_DECREF(p);
+        return out;
+    }
+    Py_XDECREF(out);
+    PyErr_Clear();
+    return NULL;
+}
+
+/* o.new_empty(sizes): steals sizes */
+static PyObject *of_sizes(PyObject *o, PyObject *sizes, void **ptr) {
+    PyObject *out = sizes ? PyObject_CallMethodOneArg(o, s_new_empty, sizes) : NULL, *p = NULL;
+    Py_XDECREF(sizes);
+    if (out && (p = PyObject_CallMethodNoArgs(out, s_data_ptr))) {
+        *ptr = PyLong_AsVoidPtr(p);
+        Py_DECREF(p);
+        return out;
+    }
+    Py_XDECREF(out);
+    PyErr_Clear();
+    return NULL;
+}
+
+/* prefill(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal, scale, out, lse) */
 static PyObject *py_prefill(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     fa_paged_cache c;
-    Tensor q, table, lens, cu, to;
+    Tensor q, table, lens, cu, to, lse;
     float scale;
     void *stream;
-    if (n != 10 || !attention(a, a[3], a[4], a[8], &c, &q, &table, &lens, &scale, &stream) || q.nd != 3 || q.size[0] < 1 ||
-        !ints(a[5], &cu, 1, q.device) || cu.size[0] != lens.size[0] + 1 || !PyLong_CheckExact(a[6]))
+    lse.ptr = NULL;
+    if (n != 11 || !attention(a, a[3], a[4], a[8], &c, &q, &table, &lens, &scale, &stream) || q.nd != 3 || q.size[0] < 1 ||
+        !ints(a[5], &cu, 1, q.device) || cu.size[0] != lens.size[0] + 1 || !PyLong_CheckExact(a[6]) ||
+        (a[10] != Py_None && (!floats(a[10], &lse, 2, q.device) || lse.size[0] != q.size[0] || lse.size[1] != q.size[1])))
         GIVE_UP;
     const long long most = PyLong_AsLongLong(a[6]);
     const int causal = PyObject_IsTrue(a[7]);
@@ -290,7 +349,7 @@ static PyObject *py_prefill(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     }
     int rc;
     Py_BEGIN_ALLOW_THREADS
-    rc = c_prefill(&c, q.ptr, to.ptr, NULL, table.ptr, (int)table.size[1], lens.ptr, cu.ptr, (int)lens.size[0], (int)q.size[1],
+    rc = c_prefill(&c, q.ptr, to.ptr, lse.ptr, table.ptr, (int)table.size[1], lens.ptr, cu.ptr, (int)lens.size[0], (int)q.size[1],
                    (int)q.size[0], (int)most, causal, scale, c.dtype, NULL, 0, stream);
     Py_END_ALLOW_THREADS
     return result(rc, "fa_prefill_paged", out);
@@ -320,17 +379,159 @@ static PyObject *py_shared(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return result(rc, "fa_decode_shared", out);
 }
 
-/* init(torch, FaError, addresses of fa_cache_append, fa_decode_paged, fa_prefill_paged, fa_decode_shared) */
+/* tree(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, mask, scale, out, lse) */
+static PyObject *py_tree(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    fa_paged_cache c;
+    Tensor q, table, lens, cu, mask, to, lse;
+    float scale;
+    void *stream;
+    int most;
+    lse.ptr = NULL;
+    if (n != 11 || !attention(a, a[3], a[4], a[8], &c, &q, &table, &lens, &scale, &stream) || q.nd != 3 || q.size[0] < 1 ||
+        !ints(a[5], &cu, 1, q.device) || cu.size[0] != lens.size[0] + 1 || !whole(a[6], &most) ||
+        !ints(a[7], &mask, 2, q.device) || mask.size[0] != q.size[0] ||
+        (a[10] != Py_None && (!floats(a[10], &lse, 2, q.device) || lse.size[0] != q.size[0] || lse.size[1] != q.size[1])))
+        GIVE_UP;
+    PyObject *out = output(a[9], a[0], &q, &to);
+    if (!out) GIVE_UP;
+    if (!contiguous(&to)) {
+        Py_DECREF(out);
+        GIVE_UP;
+    }
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = c_tree(&c, q.ptr, to.ptr, lse.ptr, table.ptr, (int)table.size[1], lens.ptr, cu.ptr, mask.ptr, (int)mask.size[1],
+                (int)lens.size[0], (int)q.size[1], (int)q.size[0], most, scale, c.dtype, NULL, 0, stream);
+    Py_END_ALLOW_THREADS
+    return result(rc, "fa_prefill_tree", out);
+}
+
+/* mask(parents, cu_seqlens_q, max_seqlen_q, seq_lens) -> (mask, positions) */
+static PyObject *py_mask(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor parents, cu, lens;
+    int most;
+    void *stream, *words_at, *positions_at = NULL;
+    if (n != 4 || !read_tensor(a[0], &parents) || !ints(a[0], &parents, 1, parents.device) || parents.size[0] < 1 ||
+        !ints(a[1], &cu, 1, parents.device) || cu.size[0] < 2 || !whole(a[2], &most) || most < 1)
+        GIVE_UP;
+    lens.ptr = NULL;
+    if (a[3] != Py_None && (!ints(a[3], &lens, 1, parents.device) || lens.size[0] != cu.size[0] - 1)) GIVE_UP;
+    if (!stream_of(parents.device, &stream)) GIVE_UP;
+    const int words = (most - 1) / 32 + 1;
+    PyObject *mask = of_sizes(a[0], Py_BuildValue("(Li)", parents.size[0], words), &words_at);
+    if (!mask) GIVE_UP;
+    PyObject *positions = a[3] == Py_None ? Py_NewRef(Py_None) : like(a[0], &positions_at);
+    if (!positions) {
+        Py_DECREF(mask);
+        GIVE_UP;
+    }
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = c_mask(parents.ptr, words_at, words, positions_at, lens.ptr, cu.ptr, (int)cu.size[0] - 1, (int)parents.size[0], most, stream);
+    Py_END_ALLOW_THREADS
+    return result(rc, "fa_tree_mask", Py_BuildValue("(NN)", mask, positions));
+}
+
+/* weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal, scale, weights, decay, out) */
+static PyObject *py_weigh(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    fa_paged_cache c;
+    Tensor kp, q, lse, table, lens, cu, weights, out;
+    float scale;
+    int most;
+    void *stream;
+    cu.ptr = weights.ptr = NULL;
+    if (n != 13 || !cache_of(a[2], a[3], &c, &kp) || !read_tensor(a[0], &q) || q.dtype != kp.dtype || q.device != kp.device ||
+        q.nd != 3 || q.size[2] != c.head_dim || !contiguous(&q) || !fits(q.size[0]) || !fits(q.size[1]) ||
+        !floats(a[1], &lse, 2, kp.device) || lse.size[0] != q.size[0] || lse.size[1] != q.size[1] ||
+        !ints(a[4], &table, 2, kp.device) || !ints(a[5], &lens, 1, kp.device) || table.size[0] != lens.size[0] ||
+        (a[6] != Py_None && (!ints(a[6], &cu, 1, kp.device) || cu.size[0] != lens.size[0] + 1)) || !whole(a[7], &most) ||
+        (a[6] == Py_None && q.size[0] != lens.size[0] * (long long)most) || !scale_of(a[9], c.head_dim, &scale) ||
+        !PyFloat_CheckExact(a[11]) || !floats(a[12], &out, 3, kp.device) || out.size[0] != lens.size[0] || out.size[1] != c.num_heads)
+        GIVE_UP;
+    if (a[10] != Py_None) {
+        if (!floats(a[10], &weights, 3, kp.device)) GIVE_UP;
+        for (int i = 0; i < 3; ++i)
+            if (weights.size[i] != out.size[i]) GIVE_UP;
+    }
+    const int causal = PyObject_IsTrue(a[8]);
+    if (causal < 0) {
+        PyErr_Clear();
+        GIVE_UP;
+    }
+    if (!stream_of(kp.device, &stream)) GIVE_UP;
+    const float decay = (float)PyFloat_AS_DOUBLE(a[11]);
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = c_weigh(&c, q.ptr, lse.ptr, table.ptr, (int)table.size[1], lens.ptr, cu.ptr, (int)lens.size[0], (int)q.size[1],
+                 (int)q.size[0], most, causal, scale, weights.ptr, decay, out.ptr, (int)out.size[2], NULL, 0, stream);
+    Py_END_ALLOW_THREADS
+    return result(rc, "fa_cache_weigh", Py_NewRef(a[12]));
+}
+
+/* select(weights, seq_lens, budget, sink, recent) -> (keep, counts, kept) */
+static PyObject *py_select(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Tensor w, lens;
+    int budget, sink, recent;
+    void *stream, *keep_at, *counts_at, *kept_at;
+    if (n != 5 || !read_tensor(a[0], &w) || !floats(a[0], &w, 3, w.device) || !ints(a[1], &lens, 1, w.device) ||
+        lens.size[0] != w.size[0] || !whole(a[2], &budget) || budget < 1 || !whole(a[3], &sink) || !whole(a[4], &recent) ||
+        !stream_of(w.device, &stream))
+        GIVE_UP;
+    PyObject *keep = of_sizes(a[1], Py_BuildValue("(LLi)", w.size[0], w.size[1], budget), &keep_at);
+    PyObject *counts = like(a[1], &counts_at), *kept = like(a[0], &kept_at);
+    if (!keep || !counts || !kept) {
+        Py_XDECREF(keep);
+        Py_XDECREF(counts);
+        Py_XDECREF(kept);
+        GIVE_UP;
+    }
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = c_select(w.ptr, lens.ptr, (int)w.size[0], (int)w.size[1], (int)w.size[2], budget, sink, recent, keep_at, counts_at,
+                  kept_at, stream);
+    Py_END_ALLOW_THREADS
+    return result(rc, "fa_cache_select", Py_BuildValue("(NNN)", keep, counts, kept));
+}
+
+/* keep(k_pages, v_pages, page_table, seq_lens, keep, counts, first, out_table) -> (k_pages, v_pages) */
+static PyObject *py_keep(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    fa_paged_cache c;
+    Tensor kp, table, lens, keep, counts, first, to;
+    void *stream;
+    first.ptr = to.ptr = NULL;
+    to.size[1] = 0;
+    if (n != 8 || !cache_of(a[0], a[1], &c, &kp) || !ints(a[2], &table, 2, kp.device) || !ints(a[3], &lens, 1, kp.device) ||
+        table.size[0] != lens.size[0] || !ints(a[4], &keep, 3, kp.device) || keep.size[0] != lens.size[0] || keep.size[2] < 1 ||
+        (keep.size[1] != 1 && keep.size[1] != c.num_heads) || !ints(a[5], &counts, 1, kp.device) || counts.size[0] != lens.size[0] ||
+        (a[6] != Py_None && (!ints(a[6], &first, 1, kp.device) || first.size[0] != lens.size[0])) ||
+        (a[7] != Py_None && (!ints(a[7], &to, 2, kp.device) || to.size[0] != lens.size[0])) || !stream_of(kp.device, &stream))
+        GIVE_UP;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = c_keep(&c, table.ptr, (int)table.size[1], lens.ptr, keep.ptr, (int)keep.size[1], (int)keep.size[2], counts.ptr,
+                first.ptr, to.ptr, (int)to.size[1], (int)lens.size[0], stream);
+    Py_END_ALLOW_THREADS
+    return result(rc, "fa_cache_keep", PyTuple_Pack(2, a[0], a[1]));
+}
+
+/* init(torch, FaError, addresses of fa_cache_append, fa_decode_paged, fa_prefill_paged, fa_decode_shared, fa_tree_mask,
+ * fa_prefill_tree, fa_cache_weigh, fa_cache_select, fa_cache_keep) */
 static PyObject *py_init(PyObject *self, PyObject *args) {
     (void)self;
     PyObject *torch, *error, *inner;
-    unsigned long long f[4];
-    if (!PyArg_ParseTuple(args, "OOKKKK", &torch, &error, &f[0], &f[1], &f[2], &f[3])) return NULL;
+    unsigned long long f[9];
+    if (!PyArg_ParseTuple(args, "OOKKKKKKKKK", &torch, &error, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8]))
+        return NULL;
     struct {
         PyObject **to;
         const char *name;
     } const names[] = {{&s_shape, "shape"}, {&s_stride, "stride"}, {&s_dtype, "dtype"}, {&s_get_device, "get_device"},
-                       {&s_data_ptr, "data_ptr"}, {&s_memory_format, "memory_format"}};
+                       {&s_data_ptr, "data_ptr"}, {&s_memory_format, "memory_format"}, {&s_new_empty, "new_empty"}};
     for (size_t i = 0; i < sizeof names / sizeof *names; ++i)
         if (!*names[i].to && !(*names[i].to = PyUnicode_InternFromString(names[i].name))) return NULL;
     if (!s_names && !(s_names = PyTuple_Pack(1, s_memory_format))) return NULL;
@@ -352,6 +553,11 @@ static PyObject *py_init(PyObject *self, PyObject *args) {
     c_decode = (void *)(uintptr_t)f[1];
     c_prefill = (void *)(uintptr_t)f[2];
     c_shared = (void *)(uintptr_t)f[3];
+    c_mask = (void *)(uintptr_t)f[4];
+    c_tree = (void *)(uintptr_t)f[5];
+    c_weigh = (void *)(uintptr_t)f[6];
+    c_select = (void *)(uintptr_t)f[7];
+    c_keep = (void *)(uintptr_t)f[8];
     Py_RETURN_NONE;
 }
 
@@ -360,6 +566,11 @@ static PyMethodDef methods[] = {{"init", py_init, METH_VARARGS, NULL},
                                 {"decode", (PyCFunction)(void *)py_decode, METH_FASTCALL, NULL},
                                 {"prefill", (PyCFunction)(void *)py_prefill, METH_FASTCALL, NULL},
                                 {"shared", (PyCFunction)(void *)py_shared, METH_FASTCALL, NULL},
+                                {"mask", (PyCFunction)(void *)py_mask, METH_FASTCALL, NULL},
+                                {"tree", (PyCFunction)(void *)py_tree, METH_FASTCALL, NULL},
+                                {"weigh", (PyCFunction)(void *)py_weigh, METH_FASTCALL, NULL},
+                                {"select", (PyCFunction)(void *)py_select, METH_FASTCALL, NULL},
+                                {"keep", (PyCFunction)(void *)py_keep, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
 PyMODINIT_FUNC PyInit__paged_calls(void) { return PyModule_Create(&module); }
