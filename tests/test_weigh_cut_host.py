@@ -23,8 +23,8 @@ inline int __ldg(const int *p) { return *p; }
 using namespace fa;
 
 int main() {
-    int B, Hkv, G, causal, max_len, ctas;
-    while (std::scanf("%d %d %d %d %d %d", &B, &Hkv, &G, &causal, &max_len, &ctas) == 6) {
+    int B, Hkv, tokens, causal, max_len, ctas;
+    while (std::scanf("%d %d %d %d %d %d", &B, &Hkv, &tokens, &causal, &max_len, &ctas) == 6) {
         std::vector<int> lens(B), cu(B + 1);
         for (int &n : lens) if (std::scanf("%d", &n) != 1) return 1;
         for (int &n : cu) if (std::scanf("%d", &n) != 1) return 1;
@@ -33,12 +33,11 @@ int main() {
         p.cu_q = cu.data();
         p.B = B;
         p.Hkv = Hkv;
-        p.G = G;
         p.causal = causal;
         p.max_len = max_len;
         p.total_q = cu[B];
         p.max_q = 1 << 30;
-        p.tile_tokens = kWeighRows / G;
+        p.tile_tokens = tokens;
         std::vector<long long> steps(B);
         long long W = 0;
         for (int b = 0; b < B; ++b) W += steps[b] = weigh_head_steps(p, weigh_seq(p, b)) * Hkv;
@@ -73,8 +72,8 @@ def cut(tmp_path_factory):
     subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-O1", "-Wall", "-I", build.CSRC, str(src), "-o", str(exe)], check=True)
 
     def run(calls):
-        text = "".join(f"{len(lens)} {Hkv} {G} {int(causal)} {max_len} {ctas} {' '.join(map(str, lens))} {' '.join(map(str, cu))}\n"
-                       for lens, cu, Hkv, G, causal, max_len, ctas in calls)
+        text = "".join(f"{len(lens)} {Hkv} {tokens} {int(causal)} {max_len} {ctas} {' '.join(map(str, lens))} {' '.join(map(str, cu))}\n"
+                       for lens, cu, Hkv, tokens, causal, max_len, ctas in calls)
         out = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout
         return [c.strip().splitlines() for c in out.split("E\n") if c.strip()]
     return run
@@ -91,16 +90,15 @@ def calls():
         cu = [rng.randint(0, 3)]
         for n in lens:
             cu.append(cu[-1] + rng.choice([0, 1, n, n + 5, rng.randint(0, 900)]))
-        some.append((lens, cu, rng.randint(1, 8), rng.choice([1, 2, 4, 5, 7, 8, 16, 50, 96]), rng.random() < 0.7, 4096,
+        some.append((lens, cu, rng.randint(1, 8), rng.choice([1, 2, 12, 24, 27, 48, 96, 192]), rng.random() < 0.7, 4096,
                      rng.choice([1, 2, 7, 152])))
     return some
 
 
 def test_every_chunk_once(cut):
     asked = calls()
-    for (lens, cu, Hkv, G, causal, _, ctas), lines in zip(asked, cut(asked), strict=True):
+    for (lens, cu, Hkv, tokens, causal, _, ctas), lines in zip(asked, cut(asked), strict=True):
         W, used = (int(x) for x in lines[0].split()[1:])
-        tokens = 96 // G
         want, total = [], 0
         for b, n in enumerate(lens):
             nq = cu[b + 1] - cu[b]
