@@ -89,6 +89,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     __shared__ uint32_t warp_sum[kSelWarps], found[2];
     __shared__ uint2 warp_has[kSelWarps], cta_has;  // keys above, and equal to, the last that stays
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto sync_row = [&] {
+        if (size > 1) cluster_sync();
+        else __syncthreads();
+    };
     for (int i = tid; i < 2 * kBins; i += kSelThreads) hist[0][i] = 0;
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const int rank = blockIdx.x % size, row = blockIdx.x / size;
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
             __syncthreads();
             const uint4 own = reinterpret_cast<uint4 *>(h)[tid];
             reinterpret_cast<uint2 *>(packed[pass & 1])[tid] = make_uint2(own.x | own.y << 16, own.z | own.w << 16);
-            cluster_sync();
+            sync_row();
             uint2 v[kMaxCluster];
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r)
@@ -187,9 +191,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
                 c[3] += v[r].y >> 16;
             }
         } else {
-            cluster_sync();
+            sync_row();
             for (int r = 0; r < size; ++r) {
-                const uint4 v = cluster_load4(cluster_addr(h + 4 * tid, r));
+                const uint4 v = size > 1 ? cluster_load4(cluster_addr(h + 4 * tid, r)) : reinterpret_cast<const uint4 *>(h)[tid];
                 c[0] += v.x;
                 c[1] += v.y;
                 c[2] += v.z;
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     above = __shfl_sync(0xffffffffu, has.x, max(warp - 1, 0));
     equal = __shfl_sync(0xffffffffu, has.y, max(warp - 1, 0));
     if (warp == 0) above = equal = 0;
-    cluster_sync();
+    sync_row();
     for (int r = 0; r < rank; ++r) {
         const uint2 v = cluster_load2(cluster_addr(&cta_has, r));
         above += v.x;
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
                 }
         }
     }
-    cluster_sync();  // nobody leaves while its counts are read
+    sync_row();  // nobody leaves while its counts are read
 }
 
 // ---------------------------------------------------------------- moving
@@ -493,7 +497,7 @@ int launch_select(const SelectLaunch &a, const DeviceInfo &dev, cudaStream_t str
         ready[dev.device].store(true, std::memory_order_release);
     }
     const SelectParams p = {a.weights, a.seq_lens, a.keep, a.counts, a.kept, a.heads, a.weights_len, a.budget, a.sink, a.recent};
-    Launch cfg(static_cast<unsigned>(rows * size), kSelThreads, holds ? tokens(size) * 4 : 0, size, stream);
+    Launch cfg(static_cast<unsigned>(rows * size), kSelThreads, holds ? tokens(size) * 4 : 0, size > 1 ? size : 0, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.c, kernel, p, size);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }

@@ -43,32 +43,31 @@ __global__ void __launch_bounds__(kThreads) tree_mask_kernel(const TreeParams p)
         const int last = min(nq, first + kThreads);  // (ancestors stand in front of a node)
         for (int i = threadIdx.x; i < last; i += kThreads) up[i] = __ldg(parent + i);
         __syncthreads();
-        parent = up;
     }
     const int i = first + threadIdx.x;
     if (i >= nq) return;
     uint32_t *row = p.mask + static_cast<long long>(t0 + i) * p.words;
-    int w = p.words - 1, depth = -1;
-    uint32_t bits = 0;
+    int depth = -1;
     bool bad = false;
-    for (int at = i; at >= 0;) {
-        for (; w > at >> 5; --w) {
+    auto walk = [&](auto parent_of) {
+        int at = i;
+        for (int w = p.words - 1; w >= 0; --w) {
+            uint32_t bits = 0;
+            while (at >> 5 == w) {  // (-1 is of no word)
+                bits |= 1u << (at & 31);
+                ++depth;
+                int next = parent_of(at);
+                if (next >= at || next < -1) {
+                    bad = true;
+                    next = -1;
+                }
+                at = next;
+            }
             row[w] = bits;
-            bits = 0;
         }
-        bits |= 1u << (at & 31);
-        ++depth;
-        int next = parent[at];
-        if (next >= at || next < -1) {
-            bad = true;
-            next = -1;
-        }
-        at = next;
-    }
-    for (; w >= 0; --w) {
-        row[w] = bits;
-        bits = 0;
-    }
+    };
+    if (nq <= kShared) walk([&](int at) { return up[at]; });
+    else walk([&](int at) { return __ldg(parent + at); });
     if (p.positions) p.positions[t0 + i] = __ldg(p.seq_lens + b) - nq + depth;
     if (bad) record_status(&g_tree_status, FA_ERR_INDEX);
 }
