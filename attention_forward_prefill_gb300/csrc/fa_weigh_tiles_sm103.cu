@@ -12,10 +12,10 @@
 //   warps 17-18 issue the products of a key tile each (one thread); the first owns the tensor memory
 //   warp  19    the chunks' log-sum-exps, four chunks at a time
 // A unit's 256 keys stay in shared memory while the chunks of rows go by, so that a chunk is
-// loaded once for two products.  What a wait costs under sixteen warps that keep the issue slots
-// busy (200 to 350 clocks, whether there is anything to wait for or not) is what the split of the
-// products between two threads and the lots of log-sum-exps are for.  Every warp walks through the CTA's pieces (fa_weigh_cut.cuh) by
-// itself.  TMEM: S of (tile, parity).
+// loaded once for two products.  A wait costs 200 to 350 clocks under sixteen busy warps, whether
+// there is anything to wait for or not: hence a thread for each tile's products, and log-sum-exps
+// in lots.  Every warp walks through the CTA's pieces (fa_weigh_cut.cuh) by itself.  TMEM: S of
+// (tile, parity).
 #include <algorithm>
 #include <atomic>
 
@@ -274,39 +274,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint64_t acc[2] = {};  // two pairs of sums
                 const int c1 = u.c1, rows = u.s.nq * p.G;
                 for (int c0 = u.c0; ok && c0 < c1; c0 += kOffChunks, ++lots) {
-                  const uint32_t os = lots % kOffStages;
-                  if (!lanes_wait(off_full + os, (lots / kOffStages) & 1, abort_flag)) { ok = false; break; }
-                  for (int c = c0; c < min(c1, c0 + kOffChunks); ++c, ++ch) {
-                    if ((ch & 1) != odd) continue;
-                    if (!warp_wait(s_full + t * 2 + odd, (ch / 2) & 1, abort_flag)) { ok = false; break; }
-                    tc_fence_after();
-                    // columns of the chunk that the key is seen from: what lies outside may be anything
-                    const int first = see - c * tile_rows, end = tile_live ? min(rows - c * tile_rows, tile_rows) : 0;
-                    const bool all = __all_sync(0xffffffffu, first <= 0);
-                    const ulonglong2 *off = reinterpret_cast<const ulonglong2 *>(offs + (os * kOffChunks + c - c0) * kRows);
-#pragma unroll 1
-                    for (int q = 0; q < kRows / 32; ++q) {
-                        uint32_t s[32];
-                        tmem_ld32(s_addr + q * 32, s);
-                        tmem_ld_wait();
-                        reg_fence32(s);
-                        if (q == kRows / 32 - 1) {  // S is in registers: the next one may start
+                    const uint32_t os = lots % kOffStages;
+                    if (!lanes_wait(off_full + os, (lots / kOffStages) & 1, abort_flag)) { ok = false; break; }
+                    for (int c = c0; c < min(c1, c0 + kOffChunks); ++c, ++ch) {
+                        if ((ch & 1) != odd) continue;
+                        if (!warp_wait(s_full + t * 2 + odd, (ch / 2) & 1, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        auto load = [&](int q, uint32_t (&s)[32]) {
+                            tmem_ld32(s_addr + q * 32, s);
+                            tmem_ld_wait();
+                            reg_fence32(s);
+                        };
+                        auto release = [&] {  // S is in registers: the next one may start
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(s_free + t * 2 + odd);
-                        }
-                        if (all && end >= q * 32 + 32) {
+                        };
+                        // Columns [first, end) of the chunk are rows that see the key; what lies outside may be anything.
+                        const int first = see - c * tile_rows, end = tile_live ? min(rows - c * tile_rows, tile_rows) : 0;
+                        const ulonglong2 *off = reinterpret_cast<const ulonglong2 *>(offs + (os * kOffChunks + c - c0) * kRows);
+                        if (__all_sync(0xffffffffu, first <= 0) && end >= kRows) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) add_weights<false>(&s[i * 8], off + q * 8 + i * 2, scale2, 0, 8, acc);
+                            for (int q = 0; q < kRows / 32; ++q) {
+                                uint32_t s[32];
+                                load(q, s);
+                                if (q == kRows / 32 - 1) release();
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) add_weights<false>(&s[i * 8], off + q * 8 + i * 2, scale2, 0, 8, acc);
+                            }
                         } else {
+                            // the quarters that any of the warp's keys are seen from
+                            const int q0 = max(0, __reduce_min_sync(0xffffffffu, first)) / 32, q1 = (end + 31) / 32;
+#pragma unroll 1
+                            for (int q = q0; q < q1; ++q) {
+                                uint32_t s[32];
+                                load(q, s);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, first - q * 32 - i * 8, end - q * 32 - i * 8, acc);
+                                for (int i = 0; i < 4; ++i)
+                                    add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, first - q * 32 - i * 8, end - q * 32 - i * 8, acc);
+                            }
+                            release();
                         }
                     }
-                  }
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(off_empty + os);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(off_empty + os);
                 }
                 if (!ok) break;
                 const uint64_t both = fadd2(acc[0], acc[1]);
