@@ -46,26 +46,46 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_addr(const void *at, int rank) {
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ uint4 cluster_load4(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
+// 16 or 8 bytes to shared memory of a CTA of the cluster, whose barrier counts them as they come in.
+__device__ __forceinline__ void cluster_send(void *at, int rank, uint64_t *bar, uint4 v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::
+                 "r"(cluster_addr(at, rank)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(cluster_addr(bar, rank)) : "memory");
 }
-__device__ __forceinline__ uint2 cluster_load2(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
+__device__ __forceinline__ void cluster_send(void *at, int rank, uint64_t *bar, uint2 v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1,%2}, [%3];" ::
+                 "r"(cluster_addr(at, rank)), "r"(v.x), "r"(v.y), "r"(cluster_addr(bar, rank)) : "memory");
 }
+__device__ __forceinline__ bool cluster_received(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done;
+}
+constexpr uint64_t kReceiveNs = 1500ull * 1000ull * 1000ull;
+// False: it has not come within the limit.
+__device__ __forceinline__ bool cluster_receive(uint64_t *bar, uint32_t parity) {
+    if (cluster_received(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    do {
+        if (cluster_received(bar, parity)) return true;
+    } while (globaltimer_ns() - t0 <= kReceiveNs);
+    return false;
+}
+__device__ __forceinline__ uint4 add4(uint4 a, uint4 b) { return make_uint4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
 __device__ __forceinline__ uint32_t scan_up(uint32_t v, int lane) {  // over the lanes, inclusive
 #pragma unroll
@@ -77,23 +97,35 @@ __device__ __forceinline__ uint32_t scan_up(uint32_t v, int lane) {  // over the
 }
 
 // A cluster of `size` CTAs per row, a slice of the row's tokens each, and a run of the slice
-// each warp.  HOLDS: the slice's keys stay in shared memory; else, for rows of any length, the
-// weights are read again for every digit.
+// each warp.  HOLDS: the slice's keys stay in shared memory, and after the first digit a lane holds
+// bits for up to 32 tokens side by side, or twice 32: whether a key is above those that share the
+// digits found, or one of them.  Only the latter are looked at again.  Else, for rows of any length,
+// the weights are read again for every digit.
 constexpr int kHeld = 19456;  // two CTAs per SM
+constexpr int kWords = 2;     // words of such bits a lane
+static_assert(kHeld / kSelWarps <= kWords * 32 * 32);
 template <bool HOLDS>
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, const int size) {
     extern __shared__ __align__(16) uint32_t held[];
-    __shared__ __align__(16) uint32_t hist[2][kBins];  // counts by digit, the highest first
-    __shared__ __align__(16) uint32_t packed[2][HOLDS ? kBins / 2 : 4];
-    static_assert(kHeld < 65536);
+    // counts by digit, the highest first, in two tables (and for the first digit in a third, the sums'), as additions
+    // to one bin go one by one; what the cluster's CTAs sent for the bins that this one adds up; and the sums of all
+    __shared__ __align__(16) uint32_t hist[2][kBins];
+    __shared__ __align__(16) uint4 sent[kBins / 4], sums[kBins / 4];
     __shared__ uint32_t warp_sum[kSelWarps], found[2];
-    __shared__ uint2 warp_has[kSelWarps], cta_has;  // keys above, and equal to, the last that stays
+    __shared__ uint2 warp_has[kSelWarps], cta_has[kMaxCluster];  // keys above, and equal to, the last that stays
+    __shared__ uint64_t sent_bar, sums_bar, has_bar;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    auto sync_row = [&] {
-        if (size > 1) cluster_sync();
-        else __syncthreads();
-    };
+    if (tid == 0 && size > 1) {
+        mbar_init(&sent_bar, 1);
+        mbar_init(&sums_bar, 1);
+        mbar_init(&has_bar, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&sent_bar, sizeof(sent));
+        mbar_arrive_expect_tx(&sums_bar, sizeof(sums));
+        mbar_arrive_expect_tx(&has_bar, blockIdx.x % size * sizeof(uint2));
+    }
     for (int i = tid; i < 2 * kBins; i += kSelThreads) hist[0][i] = 0;
+    sums[tid] = make_uint4(0, 0, 0, 0);
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
     const int rank = blockIdx.x % size, row = blockIdx.x / size;
     const int b = row / p.heads;
@@ -110,20 +142,46 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         const uint32_t key = weight_key(__ldg(w + min(i, n - 1)));  // (loaded whatever it is: no branch between loads)
         return i < p.sink || i >= n - p.recent ? 0xffffffffu : key;
     };
-    uint32_t *mine = held + warp * run + lane;
+    // The keys of the run, group by group: token i of group g lies where neither the lanes of a group
+    // nor the same token of 32 groups share a bank.  0: there is none (no key is 0).
+    const int groups = run / 32;
+    uint32_t *mine = held + warp * run;
+    auto place = [&](int g, int i) { return g * 32 + (i ^ (g & 31)); };
     constexpr int U = 8;  // tokens of a lane at a time
+    // (zeros, which many tokens may have, are counted apart: additions to one bin go one by one)
+    uint32_t zeros = 0;
+    __syncthreads();
+    if (size > 1 && n > p.budget) cluster_arrive();  // (nothing is sent to a CTA that has not started)
     if constexpr (HOLDS) {
         if (n > p.budget) {
-            for (int i0 = w0; i0 < w1; i0 += 2 * U * 32) {
-                uint32_t key[2 * U];
+            uint32_t *h = lane % 3 == 2 ? reinterpret_cast<uint32_t *>(sums) : hist[lane % 3];
+            auto take = [&](int g, uint32_t key) {
+                mine[place(g, lane)] = key;
+                const bool zero = key == kZeroKey;
+                zeros += zero;
+                if (!zero) atomicAdd(h + (~key >> 21), 1u);
+            };
+            constexpr int E = 4;  // where not all 16 groups are tokens to choose among
+            for (int g0 = 0; g0 < groups;) {
+                const int i0 = w0 + g0 * 32;
+                if (i0 >= p.sink && i0 + 2 * U * 32 <= min(w1, n - p.recent)) {
+                    uint32_t key[2 * U];
 #pragma unroll
-                for (int j = 0; j < 2 * U; ++j) {
-                    const int i = i0 + j * 32 + lane;
-                    key[j] = key_of(i);
+                    for (int j = 0; j < 2 * U; ++j) key[j] = __float_as_uint(__ldg(w + i0 + j * 32 + lane));
+#pragma unroll
+                    for (int j = 0; j < 2 * U; ++j) take(g0 + j, weight_key(__uint_as_float(key[j])));
+                    g0 += 2 * U;
+                    continue;
                 }
+                uint32_t key[E];
 #pragma unroll
-                for (int j = 0; j < 2 * U; ++j)
-                    if (i0 + j * 32 < w1) mine[i0 - w0 + j * 32] = key[j];
+                for (int j = 0; j < E; ++j) key[j] = key_of(i0 + j * 32 + lane);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    if (i0 + j * 32 + lane < w1) take(g0 + j, key[j]);
+                    else if (g0 + j < groups) mine[place(g0 + j, lane)] = 0;
+                }
+                g0 += E;
             }
         }
     }
@@ -146,66 +204,100 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         for (int i0 = w0; i0 < w1; i0 += U * 32) {
             uint32_t key[U];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if constexpr (HOLDS) key[j] = mine[min(i0 + j * 32, w1 - 1 & ~31) - w0];
-                else key[j] = key_of(i0 + j * 32 + lane);
-            }
-            __syncwarp();  // (f may write where these keys were)
+            for (int j = 0; j < U; ++j) key[j] = key_of(i0 + j * 32 + lane);
 #pragma unroll
             for (int j = 0; j < U; ++j) f(i0 + j * 32 + lane, key[j], i0 + j * 32 + lane < w1);
         }
     };
-    __syncthreads();
     uint32_t top = 0, left = count;  // the digits found, and how many keys of that prefix stay
+    // of tokens `own` + 1024 h and on: keys above that prefix, and with it
+    uint32_t more[kWords] = {}, same[kWords] = {};
+    const int log_own = groups >= 32 ? 5 : 32 - __clz(groups - 1), own = lane << log_own;  // (all lanes, even of few groups)
+    // sort(s, f): keys without the prefix leave `same`, and f gets the others.
+    auto sort = [&](int s, auto f) {
+#pragma unroll
+        for (int h = 0; h < kWords; ++h)
+            for (uint32_t m = same[h]; m; m &= m - 1) {
+                const uint32_t key = mine[place((own >> 5) + 32 * h, (own & 31) + __ffs(m) - 1)], bit = m & -m;
+                if (key >> s == top) {
+                    f(key);
+                } else {
+                    same[h] ^= bit;
+                    more[h] |= key >> s > top ? bit : 0;
+                }
+            }
+    };
+    // Nobody leaves while others may still send to it.
+    auto give_up = [&] {
+        if (lane == 0) record_status(&g_evict_status, FA_ERR_WATCHDOG);
+        cluster_arrive();
+        cluster_wait();
+    };
     int shift = 32;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int bits = pass == 2 ? 10 : 11, above = shift;
         shift -= bits;
-        uint32_t *h = hist[pass & 1];
-        // (zeros, which many tokens may have, are counted apart: additions to one bin go one by one)
-        uint32_t zeros = 0;
-        each([&](int, uint32_t key, bool is) {
-            const bool in = is && (pass == 0 || key >> above == top), zero = key == kZeroKey;
-            zeros += in && zero;
-            if (in && !zero) atomicAdd(h + (~(key >> shift) & ((1u << bits) - 1u)), 1u);
-        });
-        zeros = __reduce_add_sync(0xffffffffu, zeros);
-        if (lane == 0 && zeros) atomicAdd(h + (~(kZeroKey >> shift) & ((1u << bits) - 1u)), zeros);
-        // four bins a thread, of all CTAs; on their way two of 16 bits in a word where a slice has no more
-        uint32_t c[4] = {0, 0, 0, 0};
-        if (HOLDS && size > 1) {
-            __syncthreads();
-            const uint4 own = reinterpret_cast<uint4 *>(h)[tid];
-            reinterpret_cast<uint2 *>(packed[pass & 1])[tid] = make_uint2(own.x | own.y << 16, own.z | own.w << 16);
-            sync_row();
-            uint2 v[kMaxCluster];
+        uint32_t *h = hist[lane & 1];
+        if (!HOLDS || pass > 0) zeros = 0;
+        auto add = [&](uint32_t key) {
+            if (key == kZeroKey) ++zeros;
+            else atomicAdd(h + (~(key >> shift) & ((1u << bits) - 1u)), 1u);
+        };
+        if constexpr (!HOLDS) {
+            each([&](int, uint32_t key, bool is) {
+                if (is && (pass == 0 || key >> above == top)) add(key);
+            });
+        } else if (pass == 1) {
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                v[r] = r < size ? cluster_load2(cluster_addr(packed[pass & 1] + 2 * tid, r)) : make_uint2(0, 0);
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) {
-                c[0] += v[r].x & 0xffffu;
-                c[1] += v[r].x >> 16;
-                c[2] += v[r].y & 0xffffu;
-                c[3] += v[r].y >> 16;
-            }
-        } else {
-            sync_row();
-            for (int r = 0; r < size; ++r) {
-                const uint4 v = size > 1 ? cluster_load4(cluster_addr(h + 4 * tid, r)) : reinterpret_cast<const uint4 *>(h)[tid];
-                c[0] += v.x;
-                c[1] += v.y;
-                c[2] += v.z;
-                c[3] += v.w;
+            for (int w = 0; w < kWords; ++w) {
+                const int g1 = min(groups, w * 32 + 32);
+#pragma unroll 8
+                for (int g = w * 32; g < g1; ++g) {
+                    const uint32_t digit = mine[place(g, lane)] >> above;
+                    const uint32_t is_more = __ballot_sync(0xffffffffu, digit > top);
+                    const uint32_t is_same = __ballot_sync(0xffffffffu, digit == top);
+                    if ((own >> 5) == (g & 31)) more[w] = is_more, same[w] = is_same;
+                }
+                const uint32_t bits_own = (2u << ((1 << log_own) - 1)) - 1u;
+                more[w] = more[w] >> (own & 31) & bits_own;
+                same[w] = same[w] >> (own & 31) & bits_own;
             }
         }
+        if (HOLDS && pass > 0) sort(above, add);
+        zeros = __reduce_add_sync(0xffffffffu, zeros);
+        if (lane == 0 && zeros) atomicAdd(h + (~(kZeroKey >> shift) & ((1u << bits) - 1u)), zeros);
+        // four bins a thread; a CTA adds up an equal part of them for all, and sends the sums round
+        __syncthreads();
+        uint4 *own_bins = reinterpret_cast<uint4 *>(hist[0]) + tid;
+        uint4 sum4 = add4(own_bins[0], own_bins[kBins / 4]);
+        if (HOLDS && pass == 0) sum4 = add4(sum4, sums[tid]);  // (its part of the sums comes after this thread's counts have gone)
+        own_bins[0] = own_bins[kBins / 4] = make_uint4(0, 0, 0, 0);
+        bool ok = true;
+        if (size > 1) {
+            const int part = kBins / 4 / size, to = tid / part, at = tid % part;
+            if (pass == 0) cluster_wait();
+            cluster_send(sent + rank * part + at, to, &sent_bar, sum4);
+            ok = cluster_receive(&sent_bar, pass & 1);
+            if (tid == 0 && ok) mbar_arrive_expect_tx(&sent_bar, sizeof(sent));
+            sum4 = sent[at];
+#pragma unroll
+            for (int r = 1; r < kMaxCluster; ++r)
+                if (r < size) sum4 = add4(sum4, sent[r * part + at]);
+            if (ok) cluster_send(sums + rank * part + at, to, &sums_bar, sum4);  // (else nobody goes on)
+            ok = ok && cluster_receive(&sums_bar, pass & 1);
+            if (tid == 0 && ok) mbar_arrive_expect_tx(&sums_bar, sizeof(sums));
+            sum4 = sums[tid];
+        }
+        const uint32_t c[4] = {sum4.x, sum4.y, sum4.z, sum4.w};
         const uint32_t all = c[0] + c[1] + c[2] + c[3], incl = scan_up(all, lane);
         if (lane == 31) warp_sum[warp] = incl;
-        // (the other CTAs have read the other table before they came here)
-        if (pass == 1)
-            for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
-        __syncthreads();
+        if (size == 1) {
+            __syncthreads();
+        } else if (__syncthreads_or(!ok)) {
+            give_up();
+            return;
+        }
         uint32_t sum = incl - all;
 #pragma unroll
         for (int k = 0; k < kSelWarps - 1; ++k) sum += k < warp ? warp_sum[k] : 0u;
@@ -225,56 +317,70 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     }
     // top: the smallest key that stays; left: how many of those equal to it
     uint32_t above = 0, equal = 0;
-    each([&](int, uint32_t key, bool is) {
-        above += is && key > top;
-        equal += is && key == top;
-    });
-    above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
+    uint32_t ups[kWords] = {}, ups_all = 0;  // above | equal << 16 before this lane's groups, and in the run
+    if constexpr (HOLDS) {
+        sort(0, [](uint32_t) {});
+#pragma unroll
+        for (int h = 0; h < kWords; ++h) {
+            const uint32_t c = __popc(more[h]) | __popc(same[h]) << 16, incl = scan_up(c, lane);
+            ups[h] = ups_all + incl - c;
+            ups_all += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        above = ups_all & 0xffffu;
+        equal = ups_all >> 16;
+    } else {
+        each([&](int, uint32_t key, bool is) {
+            above += is && key > top;
+            equal += is && key == top;
+        });
+        above = __reduce_add_sync(0xffffffffu, above);
+        equal = __reduce_add_sync(0xffffffffu, equal);
+    }
     if (lane == 0) warp_has[warp] = make_uint2(above, equal);
     __syncthreads();
     uint2 has = lane < kSelWarps ? warp_has[lane] : make_uint2(0, 0);
     has.x = scan_up(has.x, lane);
     has.y = scan_up(has.y, lane);
-    if (tid == kSelWarps - 1) cta_has = has;
     above = __shfl_sync(0xffffffffu, has.x, max(warp - 1, 0));
     equal = __shfl_sync(0xffffffffu, has.y, max(warp - 1, 0));
     if (warp == 0) above = equal = 0;
-    sync_row();
-    for (int r = 0; r < rank; ++r) {
-        const uint2 v = cluster_load2(cluster_addr(&cta_has, r));
-        above += v.x;
-        equal += v.y;
-    }
-    // The tokens that stay, in order: first to this warp's part of the shared memory, whose keys they
-    // overtake nowhere, so that the weights are then read side by side; or out one by one.
-    const uint32_t before = (1u << lane) - 1u, to0 = above + min(equal, left);
-    uint32_t stay = 0;
-    each([&](int i, uint32_t key, bool is) {
-        const uint32_t is_above = __ballot_sync(0xffffffffu, is && key > top);
-        const uint32_t is_equal = __ballot_sync(0xffffffffu, is && key == top);
-        if (!(is_above | is_equal)) return;
-        const bool stays = is && (key > top || (key == top && equal + __popc(is_equal & before) < left));
-        const uint32_t who = __ballot_sync(0xffffffffu, stays), at = stay + __popc(who & before);
-        if (stays) {
-            if constexpr (HOLDS) {
-                held[warp * run + at] = i;
-            } else {
-                keep[to0 + at] = i;
-                if (kept) kept[to0 + at] = __ldg(w + i);
-            }
+    if (size > 1) {  // to the CTAs of the tokens behind
+        const uint2 cta = make_uint2(__shfl_sync(0xffffffffu, has.x, kSelWarps - 1), __shfl_sync(0xffffffffu, has.y, kSelWarps - 1));
+        if (warp == 0 && lane > rank && lane < size) cluster_send(cta_has + rank, lane, &has_bar, cta);
+        if (!__all_sync(0xffffffffu, cluster_receive(&has_bar, 0))) {
+            give_up();
+            return;
         }
-        stay += __popc(who);
-        equal += __popc(is_equal);
-    });
+        const uint2 v = lane < rank ? cta_has[lane] : make_uint2(0, 0);
+        above += __reduce_add_sync(0xffffffffu, v.x);
+        equal += __reduce_add_sync(0xffffffffu, v.y);
+    }
+    if (size > 1) cluster_arrive();  // nothing is sent any more
+    const uint32_t to0 = above + min(equal, left);
     if constexpr (HOLDS) {
+        // The tokens that stay, in order: first to where the warp's keys were, so that the lists are then
+        // written, and the weights read, side by side.
+        uint32_t stay = 0;
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < kWords; ++h) {
+            const uint32_t e = equal + (ups[h] >> 16);
+            uint32_t at = above + (ups[h] & 0xffffu) + min(e, left) - to0;
+            int more_of_same = static_cast<int>(left) - static_cast<int>(min(e, left));
+            for (uint32_t m = more[h] | same[h]; m; m &= m - 1) {
+                if (same[h] & m & -m && more_of_same-- <= 0) continue;
+                mine[at++] = w0 + own + 1024 * h + __ffs(m) - 1;
+            }
+            stay = max(stay, at);
+        }
+        stay = __reduce_max_sync(0xffffffffu, stay);
         __syncwarp();
         for (uint32_t k0 = lane; k0 < stay; k0 += U * 32) {
             uint32_t i[U];
             float x[U];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                i[j] = held[warp * run + min(k0 + j * 32, stay - 1)];
+                i[j] = mine[min(k0 + j * 32, stay - 1)];
                 x[j] = kept ? __ldg(w + i[j]) : 0.f;
             }
 #pragma unroll
@@ -284,8 +390,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
                     if (kept) kept[to0 + k0 + j * 32] = x[j];
                 }
         }
+    } else {
+        const uint32_t before = (1u << lane) - 1u;
+        uint32_t stay = to0;
+        each([&](int i, uint32_t key, bool is) {
+            const uint32_t is_above = __ballot_sync(0xffffffffu, is && key > top);
+            const uint32_t is_equal = __ballot_sync(0xffffffffu, is && key == top);
+            if (!(is_above | is_equal)) return;
+            const bool stays = is && (key > top || (key == top && equal + __popc(is_equal & before) < left));
+            const uint32_t who = __ballot_sync(0xffffffffu, stays), at = stay + __popc(who & before);
+            if (stays) {
+                keep[at] = i;
+                if (kept) kept[at] = __ldg(w + i);
+            }
+            stay += __popc(who);
+            equal += __popc(is_equal);
+        });
     }
-    sync_row();  // nobody leaves while its counts are read
+    if (size > 1) cluster_wait();
 }
 
 // ---------------------------------------------------------------- moving
