@@ -471,43 +471,7 @@ struct KeepRow {
     }
 };
 
-// Short lists: a thread moves a column of 16 bytes of a row (sequence, kv head, keys or values), kDeep
-// tokens at a time.
-constexpr int kDeep = 8;
-constexpr int kShort = 64;
-__global__ void __launch_bounds__(kKeepThreads) keep_columns_kernel(const KeepParams p) {
-    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
-    const long long column = static_cast<long long>(blockIdx.x) * kKeepThreads + threadIdx.x;
-    const int chunk = column % p.chunks;
-    const long long pair = column / p.chunks;  // ((b, h), keys or values)
-    if (pair >= 2LL * p.B * p.Hkv) return;
-    const int h = pair / 2 % p.Hkv, b = pair / 2 / p.Hkv;
-    uint16_t *base = (pair & 1 ? p.v_pages : p.k_pages) + h * p.head_stride + chunk * 8;
-    KeepRow r(p, b, h);
-    for (int i0 = 0; i0 < r.count; i0 += kDeep) {
-        uint4 data[kDeep];
-        long long to[kDeep];
-        int src[kDeep], page[kDeep], out_page[kDeep];
-#pragma unroll
-        for (int k = 0; k < kDeep; ++k) src[k] = r.number(p, i0 + k);
-#pragma unroll
-        for (int k = 0; k < kDeep; ++k)
-            if (src[k] >= 0) r.pages(p, src[k], i0 + k, page[k], out_page[k]);
-#pragma unroll
-        for (int k = 0; k < kDeep; ++k) {
-            long long from = to[k] = -1;
-            if (src[k] >= 0) r.places(p, src[k], i0 + k, page[k], out_page[k], from, to[k]);
-            data[k] = make_uint4(0, 0, 0, 0);
-            if (to[k] >= 0 && from >= 0) data[k] = *reinterpret_cast<const uint4 *>(base + from);
-        }
-#pragma unroll
-        for (int k = 0; k < kDeep; ++k)
-            if (to[k] >= 0) *reinterpret_cast<uint4 *>(base + to[k]) = data[k];
-    }
-    if (r.status && chunk == 0) record_status(&g_evict_status, r.status);
-}
-
-// Long lists: a CTA moves some columns (16 << lane_shift bytes) of a row (sequence, kv head, keys
+// A CTA moves some columns (16 << lane_shift bytes) of a row (sequence, kv head, keys
 // or values) in the order of the list, a batch of 256 >> lane_shift tokens after another, a thread 16
 // bytes of one token.  kAhead batches are on their way in shared memory ahead of the one that is
 // written, and the places of 256 tokens at a time, a token a thread, ahead of those: a token's
@@ -649,17 +613,13 @@ int launch_keep(const KeepLaunch &a, const DeviceInfo &dev, cudaStream_t stream)
     p.chunks = a.c.head_dim / 8;
     p.in_place = a.in_place ? 1 : 0;
     const long long rows = 2LL * a.B * p.Hkv;
-    if (a.keep_len > kShort) {
-        // 16-byte pieces of a token side by side, in as few slices of the row as fill the SMs
-        int lane_shift = p.chunks == 16 ? 4 : 3;
-        while (lane_shift > 2 && rows * (p.chunks >> lane_shift) < 4LL * dev.num_sms) --lane_shift;
-        Launch cfg(static_cast<unsigned>(rows * (p.chunks >> lane_shift)), kKeepThreads, kKeepSmem, 0, stream);
-        const cudaError_t e = cudaLaunchKernelEx(&cfg.c, keep_rows_kernel, p, lane_shift);
-        return e == cudaSuccess ? FA_OK : cuda_fail(e);
-    }
-    const long long columns = rows * p.chunks;
-    Launch cfg(static_cast<unsigned>((columns + kKeepThreads - 1) / kKeepThreads), kKeepThreads, 0, 0, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, keep_columns_kernel, p);
+    // 16-byte pieces of a token side by side, in as few slices of the row as give every SM a CTA, or four where
+    // lists are long and the copies in flight set the rate (8 sequences, 8 heads of 128: 64 tokens 2.8 us with 256
+    // CTAs, 3.6 with 512; 8192 of 32768 tokens 101 and 93)
+    int lane_shift = p.chunks == 16 ? 4 : 3;
+    while (lane_shift > 2 && rows * (p.chunks >> lane_shift) < (a.keep_len > 1024 ? 4LL : 1LL) * dev.num_sms) --lane_shift;
+    Launch cfg(static_cast<unsigned>(rows * (p.chunks >> lane_shift)), kKeepThreads, kKeepSmem, 0, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.c, keep_rows_kernel, p, lane_shift);
     return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

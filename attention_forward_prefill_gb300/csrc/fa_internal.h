@@ -170,7 +170,7 @@ struct WeighLaunch {
     void *scratch;              // weigh_scratch_bytes(...), 16-byte aligned, where weigh_in_tiles
 };
 
-bool weigh_in_tiles(const WeighLaunch &a);
+bool weigh_in_tiles(const WeighLaunch &a, int num_sms);
 size_t weigh_scratch_bytes(int num_sms);
 int launch_weigh(const WeighLaunch &a, const DeviceInfo &dev, cudaStream_t stream);
 

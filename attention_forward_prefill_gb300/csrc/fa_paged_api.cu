@@ -471,7 +471,7 @@ int fa_cache_weigh(const fa_paged_cache *cache, const void *q, const float *lse,
     l.weights_len = weights_len;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     Scratch s(st);
-    if ((rc = s.take(workspace, workspace_bytes, weigh_scratch_bytes(dev.num_sms), weigh_in_tiles(l))) != FA_OK) return rc;
+    if ((rc = s.take(workspace, workspace_bytes, weigh_scratch_bytes(dev.num_sms), weigh_in_tiles(l, dev.num_sms))) != FA_OK) return rc;
     l.scratch = s.ptr;
     return s.done(launch_weigh(l, dev, st));
 }

@@ -229,7 +229,7 @@ int launch_weigh(const WeighLaunch &a, const DeviceInfo &dev, cudaStream_t strea
     p.causal = a.causal;
     p.scale_log2 = a.scale * kLog2e;
     p.decay = a.decay;
-    if (weigh_in_tiles(a)) return launch_weigh_tiles(a, p, dev, stream);
+    if (weigh_in_tiles(a, dev.num_sms)) return launch_weigh_tiles(a, p, dev, stream);
     const bool bf16 = a.c.dtype == FA_BF16;
     if (a.c.head_dim == 64) return bf16 ? launch_rows<64, true>(p, dev, stream) : launch_rows<64, false>(p, dev, stream);
     return bf16 ? launch_rows<128, true>(p, dev, stream) : launch_rows<128, false>(p, dev, stream);

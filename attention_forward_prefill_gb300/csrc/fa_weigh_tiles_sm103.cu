@@ -412,9 +412,18 @@ size_t part_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * kWeig
 
 }  // namespace
 
-bool weigh_in_tiles(const WeighLaunch &a) {
+// Which kernel: the tiles' takes as long for one row of a kv head as for 128, the warp products' some more with each.
+// In us, theirs against the tiles':
+//   16 sequences of 4096, 32 heads over 8, d = 128:   8 rows 28 : 40, 16 rows 46 : 40, 32 rows 64 : 40, 128 rows 183 : 42
+//   4 of 16384, 12 heads, d = 64:                     8 rows 24 : 47, 16 rows 44 : 47, 24 rows 56 : 47, 128 rows 215 : 48
+//   32 of 1000, 64 over 8, d = 128:                   8 rows 13 : 25, 16 rows 22 : 25, 32 rows 32 : 26, 128 rows 92 : 27
+//   1 of 4096, 32 over 8, d = 128 (its start counts): 8 rows  6 : 11, 32 rows  9 : 11, 48 rows 10 : 12, 64 rows 12 : 12
+bool weigh_in_tiles(const WeighLaunch &a, int num_sms) {
     const int group = a.Hq / a.c.num_heads;
-    return static_cast<long long>(a.max_q) * group > 64 && group <= kRows && a.total_q > 0;
+    const long long rows = static_cast<long long>(a.max_q) * group;
+    const int max_len = std::min(a.max_pages * a.c.page_size, a.weights_len);
+    const long long units = static_cast<long long>(a.B) * a.c.num_heads * ((max_len + kWeighKeys - 1) / kWeighKeys);
+    return rows > (units >= 2LL * num_sms ? 16 : 48) && group <= kRows && a.total_q > 0;
 }
 
 size_t weigh_scratch_bytes(int num_sms) { return part_bytes(num_sms) + static_cast<size_t>(num_sms) * sizeof(int4); }

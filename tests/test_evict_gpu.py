@@ -49,6 +49,8 @@ FORMS = [
     ([100, 4], [300, 9], 6, 2, 128, 64, torch.float16, False),   # more query tokens than keys
     ([257], [255], 130, 1, 64, 256, torch.bfloat16, False),
     ([70, 33] * 40, [2, 1] * 40, 64, 8, 128, 32, torch.bfloat16, False),
+    ([1000, 40, 513] * 10, [5, 8, 1] * 10, 32, 8, 128, 64, torch.bfloat16, False),   # few rows, many keys
+    ([2000, 1, 600] * 12, [6, 1, 3] * 12, 14, 2, 64, 16, torch.float16, True),
 ]
 
 
