@@ -6,11 +6,17 @@
 // key T that stays is found digit by digit from the top (11, 11 and 10 bits): the
 // counts of a digit's values, summed from above, say which value holds the k-th key.
 // All keys above T stay, and of those equal to T the ones at the lowest positions.
+// Latency: a digit costs a pass over the row in shared memory and two exchanges between the CTAs
+// of its cluster.  4 x 8 rows of 90001 to 131071 weights, 16384 to keep: 26 us (110 with the weights
+// read again for every digit, 90 with them in shared memory, 35 with all CTAs' counts read by every CTA and the
+// whole row looked at again for every digit and twice for the lists; the weights and lists take 4.9 us at 6.8 TB/s).
+// 2 x 2 rows of 1000 weights: 5.9 us.
 //
 // Moving.  Token keep[i] goes to place first + i.  In place, keep[i] >= first + i, so
 // that the place a token comes from is written by the token of the same or a later i
 // alone: whoever reads a column of a row in the order of i, ahead of what it writes, can
-// move it without a copy.
+// move it without a copy.  HBM-bound: 8 sequences of up to 32768 tokens, 8192 to keep, 8 heads
+// of 128: 93 us for 539 MB (5.8 TB/s); with one token after another 2279.
 #include <algorithm>
 #include <atomic>
 

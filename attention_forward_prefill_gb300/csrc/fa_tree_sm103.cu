@@ -6,6 +6,10 @@
 //   row_i = bit i + (parent < 0 ? 0 : row_parent),   position_i = len - nq + depth_i.
 // A thread walks up from its node: the nodes on the way come in falling order, so that
 // the words of its row are finished, and written, one after another.
+//
+// The bytes are nothing (256 trees of 20 to 256 nodes: 1.3 MB, 0.2 us); the depth of the trees, a
+// load from shared memory for every ancestor, and the launch set the time.  That batch takes 4.3 us
+// (8.1 with the parents read from L1 and the words kept until the walk's end), a tree of 8 nodes 1.6.
 #include <algorithm>
 
 #include "fa_internal.h"

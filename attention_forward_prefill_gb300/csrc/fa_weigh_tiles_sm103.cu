@@ -16,6 +16,12 @@
 // there is anything to wait for or not: hence a thread for each tile's products, and log-sum-exps
 // in lots.  Every warp walks through the CTA's pieces (fa_weigh_cut.cuh) by itself.  TMEM: S of
 // (tile, parity).
+//
+// 4 chunks of 700 to 2048 tokens on up to 11048, 32 heads over 8, d = 128: 118 us (1209 TFLOP/s; tensor pipe
+// 56% active, exponential unit 55%, issue 57%), of which the start takes 8 and the join 5.  Before: eight
+// summing warps 230, a branch for every quarter of a chunk 159, sixteen warps and eight columns at a
+// time 145, a product thread for each tile 138 (products alone 98, sums alone 120), hidden quarters
+// passed over 124, a whole chunk without a loop 118.
 #include <algorithm>
 #include <atomic>
 
