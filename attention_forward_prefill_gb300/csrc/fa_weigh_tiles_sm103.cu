@@ -12,16 +12,19 @@
 //   warps 17-18 issue the products of a key tile each (one thread); the first owns the tensor memory
 //   warp  19    the chunks' log-sum-exps, four chunks at a time
 // A unit's 256 keys stay in shared memory while the chunks of rows go by, so that a chunk is
-// loaded once for two products.  A wait costs 200 to 350 clocks under sixteen busy warps, whether
-// there is anything to wait for or not: hence a thread for each tile's products, and log-sum-exps
-// in lots.  Every warp walks through the CTA's pieces (fa_weigh_cut.cuh) by itself.  TMEM: S of
-// (tile, parity).
+// loaded once for two products, and the next unit's are on their way.  A wait costs 200 to 350
+// clocks under sixteen busy warps, whether there is anything to wait for or not: hence a thread for
+// each tile's products, and log-sum-exps in lots.  Every warp walks through the CTA's pieces
+// (fa_weigh_cut.cuh) by itself.  TMEM: S of (tile, parity).
 //
-// 4 chunks of 700 to 2048 tokens on up to 11048, 32 heads over 8, d = 128: 118 us (1209 TFLOP/s; tensor pipe
+// 4 chunks of 700 to 2048 tokens on up to 11048, 32 heads over 8, d = 128: 116 us (1226 TFLOP/s; tensor pipe
 // 56% active, exponential unit 55%, issue 57%), of which the start takes 8 and the join 5.  Before: eight
 // summing warps 230, a branch for every quarter of a chunk 159, sixteen warps and eight columns at a
 // time 145, a product thread for each tile 138 (products alone 98, sums alone 120), hidden quarters
-// passed over 124, a whole chunk without a loop 118.
+// passed over 124, a whole chunk without a loop 118, two units' keys and two chunks of rows held instead
+// of one and four 116.
+// One chunk a unit (up to 128 rows), 16 sequences of 4096 tokens: 35 to 38 us for 134 MB (40 with one
+// unit's keys, 37 where the warps of both parities still met at every unit).
 #include <algorithm>
 #include <atomic>
 
@@ -40,20 +43,22 @@ constexpr int kRows = kWeighRows;  // rows of a chunk
 constexpr uint32_t kTmemCols = 512;
 constexpr int kOffStages = 2, kOffChunks = 4;  // lots of log-sum-exps, and chunks of a lot
 
+constexpr int kKeySets = 2;  // units whose keys are in shared memory
+
 __device__ int g_weigh_tiles_status = 0;
 
 template <int D>
 struct WeighLayout {
     static constexpr int kSlabs = D / 64, kSlab = 128 * 128;
     static constexpr int kTileBytes = kSlabs * kSlab;
-    static constexpr int kRowStages = D == 128 ? 4 : 8;
-    static constexpr int kRowsOff = 2 * kTileBytes;
+    static constexpr int kRowStages = D == 128 ? 2 : 8;
+    static constexpr int kRowsOff = 2 * kKeySets * kTileBytes;
     static constexpr int kOffOff = kRowsOff + kRowStages * kTileBytes;  // [kOffStages][kOffChunks][kRows] floats
     static constexpr int kOddOff = kOffOff + kOffStages * kOffChunks * kRows * 4;    // [2][kM]: sums over the odd chunks
     static constexpr int kBarOff = kOddOff + 2 * kM * 4;
-    // k_full[tile], k_empty[tile], q_full, q_empty, off_full, off_empty, s_full[tile][parity], s_free[tile][parity],
+    // k_full[set][tile], k_empty[set][tile], q_full, q_empty, off_full, off_empty, s_full[tile][parity], s_free[tile][parity],
     // sum_full[tile], sum_free[tile], drain[tile]
-    static constexpr int kNumBars = 4 + 2 * kRowStages + 2 * kOffStages + 8 + 4 + 2;
+    static constexpr int kNumBars = 4 * kKeySets + 2 * kRowStages + 2 * kOffStages + 8 + 4 + 2;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kStartOff = kMiscOff + 8;
     static constexpr int kSumOff = kStartOff + (int)sizeof(WeighStart);
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     weigh_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const WeighParams p) {
     using L = WeighLayout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBarOff), *k_empty = k_full + 2, *q_full = k_empty + 2,
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBarOff), *k_empty = k_full + 2 * kKeySets, *q_full = k_empty + 2 * kKeySets,
              *q_empty = q_full + L::kRowStages, *off_full = q_empty + L::kRowStages, *off_empty = off_full + kOffStages,
              *s_full = off_empty + kOffStages, *s_free = s_full + 4, *sum_full = s_free + 4, *sum_free = sum_full + 2,
              *drain = sum_free + 2;
@@ -109,11 +114,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile_rows = p.tile_tokens * p.G;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2 * kKeySets; ++i) {
             mbar_init(k_full + i, 1);
             mbar_init(k_empty + i, 1);
-            mbar_init(drain + i, 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(drain + i, 1);
         for (int i = 0; i < L::kRowStages; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(q_empty + i, 2);  // both tiles' products
@@ -135,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&map_k);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0) p.open[blockIdx.x] = make_int4(-1, 0, 0, 0);  // (the plan's barriers are between this and another)
     if (warp == kMmaWarp) {
         // behind the wait and before followers start, as in paged_tiles_kernel
         tmem_alloc(tmem_slot, kTmemCols);
@@ -146,7 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                          [&](const WeighSeq &s) { return weigh_head_steps(p, s); });
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    uint32_t kc = 0;  // pieces with rows so far
+    uint32_t kc = 0;  // pieces with rows so far (the producer: their key tiles, two each)
+    auto key_set = [](uint32_t piece, int t) { return static_cast<int>(piece % kKeySets * 2 + t); };
     uint32_t ch = 0;  // chunks so far
     bool ok = true;
     WeighCursor cur;
@@ -166,22 +173,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = my_tile < 2 && key < u.s.len;
             int id = live ? __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + (key >> p.page_shift)) : 0;
             for (int t = 0; t < 2 && ok; ++t) {
-                if (kc > 0 && !lanes_wait(k_empty + t, (kc - 1) & 1, abort_flag)) { ok = false; break; }
+                const uint32_t piece = kc / 2;
+                const int set = key_set(piece, t);
+                if (piece >= kKeySets && !lanes_wait(k_empty + set, (piece / kKeySets - 1) & 1, abort_flag)) { ok = false; break; }
                 const bool mine = live && my_tile == t;
                 const int copies = __popc(__ballot_sync(0xffffffffu, mine));
-                if (lane == 0) mbar_arrive_expect_tx(k_full + t, copies * box * 128);  // (a tile without keys: none)
+                if (lane == 0) mbar_arrive_expect_tx(k_full + set, copies * box * 128);  // (a tile without keys: none)
                 __syncwarp();
                 if (mine) {
                     if (id < 0 || id >= p.num_pages) {
                         record_status(&g_weigh_tiles_status, FA_ERR_PAGE);
                         id = p.num_pages;  // outside the tensor: the copy writes zeros
                     }
-                    tma_load_4d(smem + t * L::kTileBytes + my_slab * L::kSlab + my_box * box * 128, &map_k, k_full + t, my_slab * 64,
+                    tma_load_4d(smem + set * L::kTileBytes + my_slab * L::kSlab + my_box * box * 128, &map_k, k_full + set, my_slab * 64,
                                 key & (page - 1), u.h, id, pol_k);
                 }
+                ++kc;
             }
             if (!ok) break;
-            ++kc;
             for (int c = u.c0; c < u.c1; ++c) {
                 const uint32_t qs = ch % L::kRowStages;
                 if (ch >= L::kRowStages && !lanes_wait(q_empty + qs, (ch / L::kRowStages - 1) & 1, abort_flag)) { ok = false; break; }
@@ -201,12 +210,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = idesc_f16(BF16, kM, kRows, false, false);
         const int t = warp - kMmaWarp;  // the key tile
         const uint32_t rows = smem_u32(smem) + L::kRowsOff, acc = tmem + t * 2 * kRows;
-        const uint64_t k_desc = sdesc_sw128(smem_u32(smem) + t * L::kTileBytes, 16, 1024);
         while (ok && cur.next(p, u)) {
             if (u.s.nq == 0) continue;
             if (lane == 0) {
                 const bool has_keys = u.u * kWeighKeys + t * kM < u.s.len;
-                ok = mbar_wait(k_full + t, kc & 1, abort_flag, kWatchdogNs);
+                const int set = key_set(kc, t);
+                const uint64_t k_desc = sdesc_sw128(smem_u32(smem) + set * L::kTileBytes, 16, 1024);
+                ok = mbar_wait(k_full + set, (kc / kKeySets) & 1, abort_flag, kWatchdogNs);
                 for (int c = u.c0; ok && c < u.c1; ++c) {  // (a tile without keys goes through the same steps)
                     const uint32_t qs = ch % L::kRowStages, buf = ch & 1;
                     // polled: the product should start the moment the accumulator is free
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit(q_empty + qs);
                     ++ch;
                 }
-                if (ok) umma_commit(k_empty + t);
+                if (ok) umma_commit(k_empty + set);
             }
             ++kc;
             ok = __all_sync(0xffffffffu, ok);
@@ -266,16 +276,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp >> 3;
         const uint32_t odd = warp >> 2 & 1;
         float *odd_sum = reinterpret_cast<float *>(smem + L::kOddOff) + t * kM + (warp & 3) * 32 + lane;
-        uint32_t pieces = 0, lots = 0;  // pieces with rows, lots of log-sum-exps
+        uint32_t pieces = 0, lots = 0;  // pieces of several chunks, lots of log-sum-exps
         const int in_unit = t * kM + (warp & 3) * 32 + lane;
         const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (t * 2 + odd) * kRows;
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
-        if (threadIdx.x == 0) p.open[blockIdx.x] = make_int4(-1, 0, 0, 0);
         while (ok && cur.next(p, u)) {
             const int key = u.u * kWeighKeys + in_unit;
             const bool tile_live = u.u * kWeighKeys + t * kM < u.s.len;
             float sum = 0.f;
+            bool mine = !odd;  // whose sums are written
             if (u.s.nq > 0) {
+                const uint32_t ch0 = ch;
                 const int see = weigh_first_token(p, u.s, key) * p.G;  // the first row that sees the key
                 uint64_t acc[2] = {};  // two pairs of sums
                 const int c1 = u.c1, rows = u.s.nq * p.G;
@@ -328,8 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const uint64_t both = fadd2(acc[0], acc[1]);
                 sum = f2_lo(both) + f2_hi(both);
-                // the odd chunks' sums go to the even ones' warps
-                if (odd) {
+                // the odd chunks' sums go to the even ones' warps (of a single chunk to nobody: neither waits for the other)
+                if (c1 - u.c0 == 1) {
+                    mine = (ch0 & 1) == odd;
+                } else if (odd) {
                     if (pieces > 0 && !lanes_wait(sum_free + t, (pieces - 1) & 1, abort_flag)) { ok = false; break; }
                     *odd_sum = sum;
                     __syncwarp();
@@ -340,14 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sum_free + t);
                 }
-                ++pieces;
+                pieces += c1 - u.c0 > 1;
             }
-            if (odd) continue;
+            if (!mine) continue;
             if (u.opens && u.closes) {
                 if (key < u.s.len) weigh_store(p, u.b, u.h, u.s.nq, key, sum);
             } else {
                 p.part[(static_cast<long long>(blockIdx.x) * 2 + (u.opens ? 1 : 0)) * kWeighKeys + in_unit] = sum;
-                if (u.opens && threadIdx.x == 0)
+                if (u.opens && in_unit == 0)
                     p.open[blockIdx.x] = make_int4(weigh_cta_of(start->end + u.to_last, start->W, start->G), u.b, u.h, u.u * kWeighKeys);
             }
         }
@@ -361,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // let every copy already issued land before the CTA goes away
         constexpr uint64_t kDrainNs = 200ull * 1000ull * 1000ull;
         int dummy = 0;
-        for (int t = 0; t < 2 && kc > 0; ++t) mbar_wait(k_full + t, (kc - 1) & 1, &dummy, kDrainNs);
+        for (uint32_t i = kc > 2 * kKeySets ? kc - 2 * kKeySets : 0; i < kc; ++i)
+            mbar_wait(k_full + key_set(i / 2, i & 1), (i / 2 / kKeySets) & 1, &dummy, kDrainNs);
         for (uint32_t i = ch > L::kRowStages ? ch - L::kRowStages : 0; i < ch; ++i)
             mbar_wait(q_full + i % L::kRowStages, (i / L::kRowStages) & 1, &dummy, kDrainNs);
         record_status(&g_weigh_tiles_status, FA_ERR_WATCHDOG);
@@ -418,18 +432,18 @@ size_t part_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * kWeig
 
 }  // namespace
 
-// Which kernel: the tiles' takes as long for one row of a kv head as for 128, the warp products' some more with each.
-// In us, theirs against the tiles':
-//   16 sequences of 4096, 32 heads over 8, d = 128:   8 rows 28 : 40, 16 rows 46 : 40, 32 rows 64 : 40, 128 rows 183 : 42
-//   4 of 16384, 12 heads, d = 64:                     8 rows 24 : 47, 16 rows 44 : 47, 24 rows 56 : 47, 128 rows 215 : 48
-//   32 of 1000, 64 over 8, d = 128:                   8 rows 13 : 25, 16 rows 22 : 25, 32 rows 32 : 26, 128 rows 92 : 27
-//   1 of 4096, 32 over 8, d = 128 (its start counts): 8 rows  6 : 11, 32 rows  9 : 11, 48 rows 10 : 12, 64 rows 12 : 12
+// Which kernel: the tiles' takes about as long for one row of a kv head as for 128, the warp products' some more with
+// every eight.  In us, theirs against the tiles':
+//   16 sequences of 4096, 32 heads over 8, d = 128:   8 rows 28 : 35, 16 rows 45 : 35, 32 rows 64 : 35, 128 rows 183 : 38
+//   4 of 16384, 12 heads, d = 64:                     8 rows 24 : 40, 12 rows 45 : 40, 24 rows 56 : 40, 128 rows 215 : 41
+//   32 of 1000, 64 over 8, d = 128:                   8 rows 13 : 21, 16 rows 22 : 21, 32 rows 32 : 22, 128 rows 92 : 26
+//   1 of 4096, 32 over 8, d = 128 (its start counts): 8 rows  6 : 11, 32 rows  9 : 11, 48 rows 10 : 11, 64 rows 12 : 11
 bool weigh_in_tiles(const WeighLaunch &a, int num_sms) {
     const int group = a.Hq / a.c.num_heads;
     const long long rows = static_cast<long long>(a.max_q) * group;
     const int max_len = std::min(a.max_pages * a.c.page_size, a.weights_len);
     const long long units = static_cast<long long>(a.B) * a.c.num_heads * ((max_len + kWeighKeys - 1) / kWeighKeys);
-    return rows > (units >= 2LL * num_sms ? 16 : 48) && group <= kRows && a.total_q > 0;
+    return rows > (units >= 2LL * num_sms ? 8 : 48) && group <= kRows && a.total_q > 0;
 }
 
 size_t weigh_scratch_bytes(int num_sms) { return part_bytes(num_sms) + static_cast<size_t>(num_sms) * sizeof(int4); }
