@@ -223,7 +223,8 @@ def check_select(w, lens, budget, sink, recent):
 @pytest.mark.parametrize("B,heads,width,budget,sink,recent", [
     (1, 1, 1, 1, 0, 0), (1, 1, 40, 1, 0, 0), (2, 3, 31, 7, 1, 1), (3, 2, 1000, 256, 4, 32), (2, 2, 513, 512, 512, 0),
     (2, 2, 700, 600, 0, 600), (1, 8, 4097, 100, 50, 50), (4, 2, 9000, 4096, 3, 64), (70, 5, 600, 64, 2, 8),
-    (2, 1, 20000, 19999, 7, 9), (1, 2, 33000, 1000, 0, 0), (1, 1, 131071, 16384, 16, 1024), (200, 2, 5000, 300, 0, 20)])
+    (2, 1, 20000, 19999, 7, 9), (1, 2, 33000, 1000, 0, 0), (1, 1, 131071, 16384, 16, 1024), (200, 2, 5000, 300, 0, 20),
+    (1, 2, 150000, 20000, 9, 100), (160, 1, 19000, 5000, 3, 7), (3, 1, 2049, 2048, 0, 0), (2, 8, 70000, 69000, 33000, 33000)])
 @pytest.mark.parametrize("kind", ["spread", "ties", "zeros"])
 def test_select(B, heads, width, budget, sink, recent, kind):
     g = generator(width + budget)
