@@ -51,6 +51,9 @@ FORMS = [
     ([70, 33] * 40, [2, 1] * 40, 64, 8, 128, 32, torch.bfloat16, False),
     ([1000, 40, 513] * 10, [5, 8, 1] * 10, 32, 8, 128, 64, torch.bfloat16, False),   # few rows, many keys
     ([2000, 1, 600] * 12, [6, 1, 3] * 12, 14, 2, 64, 16, torch.float16, True),
+    ([900, 640], [500, 640], 50, 2, 128, 64, torch.bfloat16, False),   # 125 rows of a chunk
+    ([700, 129], [300, 20], 70, 2, 64, 32, torch.float16, False),      # 105
+    ([400], [130], 66, 1, 128, 128, torch.bfloat16, False),            # 66
 ]
 
 
