@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
 #pragma unroll
             for (int r = 1; r < kMaxCluster; ++r)
                 if (r < size) sum4 = add4(sum4, sent[r * part + at]);
+            __syncthreads();  // whoever gets sums from here may send its next counts over the ones that are read above
             if (ok) cluster_send(sums + rank * part + at, to, &sums_bar, sum4);  // (else nobody goes on)
             ok = ok && cluster_receive(&sums_bar, pass & 1);
             if (tid == 0 && ok) mbar_arrive_expect_tx(&sums_bar, sizeof(sums));
