@@ -22,7 +22,7 @@ struct WeighParams {
     const int *page_table, *seq_lens, *cu_q;
     int B, Hq, Hkv, G, total_q, max_q, nq_each;
     int max_pages, max_len, num_pages, page_shift, len;  // len: of a row of weights
-    int causal;
+    int causal, in_place;  // in_place: in is out
     float scale_log2, decay;
     // weigh_tiles_kernel
     int tile_tokens;
@@ -56,6 +56,13 @@ __device__ __forceinline__ bool weigh_seq_bad(const WeighParams &p, int b) {
     return bad;
 }
 
+// Without query tokens a sequence's keys and pages are not asked for, and in place there is nothing to do:
+// no steps.  (32 sequences of 200 to 8192 tokens, one of them with a token, 32 heads over 8, d = 128: 5 us in place, 21
+// into other weights, 41 with all keys loaded.)
+__device__ __forceinline__ bool weigh_stays(const WeighParams &p, const WeighSeq &s) {
+    return s.nq == 0 && p.in_place;
+}
+
 constexpr int kWeighKeys = 256;  // of a unit
 constexpr int kWeighRows = 128;  // of a chunk, at most
 constexpr int kWeighUnit = 2;
@@ -64,7 +71,9 @@ constexpr int kWeighUnit = 2;
 __device__ __forceinline__ int weigh_first_token(const WeighParams &p, const WeighSeq &s, int k) {
     return p.causal ? min(max(k - (s.len - s.nq), 0), s.nq) : 0;
 }
-__device__ __forceinline__ int weigh_units(const WeighSeq &s) { return (s.len + kWeighKeys - 1) / kWeighKeys; }
+__device__ __forceinline__ int weigh_units(const WeighParams &p, const WeighSeq &s) {
+    return weigh_stays(p, s) ? 0 : (s.len + kWeighKeys - 1) / kWeighKeys;
+}
 // Chunks of a sequence, at least one: a unit without rows still writes its keys' weights.
 __device__ __forceinline__ int weigh_chunks(const WeighParams &p, const WeighSeq &s) {
     return max(1, (s.nq + p.tile_tokens - 1) / p.tile_tokens);
@@ -75,12 +84,12 @@ __device__ __forceinline__ int weigh_first_chunk(const WeighParams &p, const Wei
 }
 // Units of a sequence whose first key all of its tokens see.
 __device__ __forceinline__ int weigh_whole(const WeighParams &p, const WeighSeq &s) {
-    const int units = weigh_units(s), past = s.len - s.nq;
+    const int units = weigh_units(p, s), past = s.len - s.nq;
     return !p.causal ? units : (past < 0 ? 0 : min(units, past / kWeighKeys + 1));
 }
 // Steps of one kv head of a sequence.
 __device__ __forceinline__ long long weigh_head_steps(const WeighParams &p, const WeighSeq &s) {
-    const int units = weigh_units(s), chunks = weigh_chunks(p, s), whole = weigh_whole(p, s);
+    const int units = weigh_units(p, s), chunks = weigh_chunks(p, s), whole = weigh_whole(p, s);
     long long sum = static_cast<long long>(units) * (kWeighUnit + chunks);
     for (int u = whole; u < units; ++u) sum -= weigh_first_chunk(p, s, chunks, u);
     return sum;
@@ -118,7 +127,7 @@ struct WeighCursor {
     __device__ __forceinline__ void sequence(const WeighParams &p, int at) {
         b = at;
         s = weigh_seq(p, b);
-        units = weigh_units(s);
+        units = weigh_units(p, s);
         chunks = weigh_chunks(p, s);
     }
     __device__ __forceinline__ void begin(const WeighParams &p, const WeighStart &st) {

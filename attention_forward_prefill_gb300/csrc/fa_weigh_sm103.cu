@@ -30,7 +30,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16;
 constexpr int kStepKeys = kWarps * kWarpKeys;  // keys of a CTA's step
 
-__device__ __forceinline__ int weigh_steps(const WeighSeq &s) { return (s.len + kStepKeys - 1) / kStepKeys; }
+__device__ __forceinline__ int weigh_steps(const WeighParams &p, const WeighSeq &s) {
+    return weigh_stays(p, s) ? 0 : (s.len + kStepKeys - 1) / kStepKeys;
+}
 
 // A warp's 16 keys of a step: where they are, and what they bring.
 template <int D>
@@ -52,7 +54,7 @@ struct WeighWalk {
         if (left <= 0) return;
         b = st.b;
         s = weigh_seq(p, b);
-        steps = weigh_steps(s);  // (at least one)
+        steps = weigh_steps(p, s);  // (at least one)
         h = static_cast<int>(st.rem / steps);
         j = static_cast<int>(st.rem % steps);
     }
@@ -63,7 +65,7 @@ struct WeighWalk {
         h = 0;
         do {
             s = weigh_seq(p, ++b);  // steps are left, so a later sequence has some
-            steps = weigh_steps(s);
+            steps = weigh_steps(p, s);
         } while (steps == 0 && b + 1 < p.B);
         if (steps == 0) left = 0;
     }
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
     __shared__ WeighStart st;
     __shared__ long long warp_sum[kWarps];
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
-    weigh_plan<kThreads>(p, st, warp_sum, 1, &g_weigh_status, [&](const WeighSeq &s) { return static_cast<long long>(weigh_steps(s)); });
+    weigh_plan<kThreads>(p, st, warp_sum, 1, &g_weigh_status, [&](const WeighSeq &s) { return static_cast<long long>(weigh_steps(p, s)); });
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
     WeighWalk walk;
     walk.begin(p, st);
@@ -92,15 +94,15 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
         x.h = w.h;
         x.s = w.s;
         x.k0 = w.left > 0 ? w.j * kStepKeys + warp * kWarpKeys : INT_MAX / 2;
-        const bool there = page >= 0 && page < p.num_pages;
-        if (x.k0 < x.s.len && !there) record_status(&g_weigh_status, FA_ERR_PAGE);  // zeros
+        const bool asked = x.k0 < x.s.len && x.s.nq > 0, there = page >= 0 && page < p.num_pages;
+        if (asked && !there) record_status(&g_weigh_status, FA_ERR_PAGE);  // zeros
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int key = x.k0 + g + 8 * r;
             // the eight channels take places 2 quad, 2 quad + 1, 2 quad + 8 and 2 quad + 9 of two products
             const uint16_t *row = p.k_pages + page * p.page_stride + w.h * p.head_stride +
                                   (key & ((1 << p.page_shift) - 1)) * p.slot_stride + quad * 8;
-            const bool live = there && key < x.s.len;
+            const bool live = asked && there && key < x.s.len;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c)
                 x.k[r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(row + c * 32)) : make_uint4(0, 0, 0, 0);
@@ -232,6 +234,7 @@ int launch_weigh(const WeighLaunch &a, const DeviceInfo &dev, cudaStream_t strea
     p.causal = a.causal;
     p.scale_log2 = a.scale * kLog2e;
     p.decay = a.decay;
+    p.in_place = a.weights == a.out ? 1 : 0;
     if (weigh_in_tiles(a, dev.num_sms)) return launch_weigh_tiles(a, p, dev, stream);
     const bool bf16 = a.c.dtype == FA_BF16;
     if (a.c.head_dim == 64) return bf16 ? launch_rows<64, true>(p, dev, stream) : launch_rows<64, false>(p, dev, stream);

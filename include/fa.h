@@ -617,8 +617,9 @@ int fa_prefill_tree(const fa_paged_cache *cache, const void *q, void *out,
  *     total_q == B * max_seqlen_q
  *   weights : fp32 [B][num_heads][weights_len], or NULL (nothing so far)
  *   out : the same sizes; may be weights itself
- * A sequence without query tokens keeps its weights as they are (out gets them).  Places at
- * and behind seq_lens[b] are neither read nor written: zero them before their tokens come.
+ * A sequence without query tokens keeps its weights as they are (out gets them), and its
+ * pages are not asked for.  Places at and behind seq_lens[b] are neither read nor written:
+ * zero them before their tokens come.
  * Lengths are clamped to [0, min(max_pages * page_size, weights_len)] and recorded as
  * FA_ERR_SEQ_LEN when they were outside.  Products, exponentials and sums are fp32, in a
  * fixed order without atomics.  The cache's values are not read.
