@@ -61,10 +61,10 @@ __device__ __forceinline__ void weigh_plan(const WeighParams &p, WeighStart &st,
     __syncthreads();
 }
 
-// Key j's weight from the sum over its rows.
+// Key j's weight from the sum over its rows; without rows it keeps its bits (-0 + 0 would be 0).
 __device__ __forceinline__ void weigh_store(const WeighParams &p, int b, int h, int nq, int key, float sum) {
     const long long at = (static_cast<long long>(b) * p.Hkv + h) * p.len + key;
-    p.out[at] = p.in ? fmaf(nq > 0 ? p.decay : 1.f, p.in[at], sum) : sum;
+    p.out[at] = !p.in ? sum : nq > 0 ? fmaf(p.decay, p.in[at], sum) : p.in[at];
 }
 // -lse in log2 units; a row that saw no key adds nothing.
 __device__ __forceinline__ float weigh_off(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }

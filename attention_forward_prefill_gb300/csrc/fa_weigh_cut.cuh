@@ -57,7 +57,7 @@ __device__ __forceinline__ bool weigh_seq_bad(const WeighParams &p, int b) {
 }
 
 // Without query tokens a sequence's keys and pages are not asked for, and in place there is nothing to do:
-// no steps.  (32 sequences of 200 to 8192 tokens, one of them with a token, 32 heads over 8, d = 128: 5 us in place, 21
+// no steps.  (32 sequences of 200 to 8192 tokens, one of them with a token, 32 heads over 8, d = 128: 5 us in place, 20
 // into other weights, 41 with all keys loaded.)
 __device__ __forceinline__ bool weigh_stays(const WeighParams &p, const WeighSeq &s) {
     return s.nq == 0 && p.in_place;

@@ -135,6 +135,12 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
     auto compute = [&](const WeighKeys<D> &x) {
         if (x.k0 >= x.s.len) return;
         const int rows = x.s.nq * p.G, key[2] = {x.k0 + g, x.k0 + g + 8};
+        if (rows == 0) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (quad == 0 && key[r] < x.s.len) p.out[(static_cast<long long>(x.b) * p.Hkv + x.h) * p.len + key[r]] = x.old[r];
+            return;
+        }
         // rows from `see` on see the key
         const int see[2] = {weigh_first_token(p, x.s, key[0]) * p.G, weigh_first_token(p, x.s, key[1]) * p.G};
         float sum[2] = {0.f, 0.f}, c[4];
@@ -148,16 +154,14 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
             }
         };
         if constexpr (FEW) {
-            if (rows > 0) {
-                if (z_of != x.b * p.Hkv + x.h) {
-                    z_of = x.b * p.Hkv + x.h;
-                    rows_of(x, 0, z);
-                    lse[0] = off_of(x, quad * 2);
-                    lse[1] = off_of(x, quad * 2 + 1);
-                }
-                products(x, z, c);
-                add(0, lse[0], lse[1]);
+            if (z_of != x.b * p.Hkv + x.h) {
+                z_of = x.b * p.Hkv + x.h;
+                rows_of(x, 0, z);
+                lse[0] = off_of(x, quad * 2);
+                lse[1] = off_of(x, quad * 2 + 1);
             }
+            products(x, z, c);
+            add(0, lse[0], lse[1]);
         } else {
             for (int r0 = weigh_first_token(p, x.s, x.k0) * p.G & ~7; r0 < rows; r0 += 8) {
                 uint4 q[D / 32];
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
             sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
             if (quad == 0 && key[r] < x.s.len)
                 p.out[(static_cast<long long>(x.b) * p.Hkv + x.h) * p.len + key[r]] =
-                    p.in ? fmaf(x.s.nq > 0 ? p.decay : 1.f, x.old[r], sum[r]) : sum[r];
+                    p.in ? fmaf(p.decay, x.old[r], sum[r]) : sum[r];
         }
     };
     WeighKeys<D> one, two;

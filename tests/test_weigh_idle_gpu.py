@@ -83,3 +83,18 @@ def test_pages_of_sequences_with_tokens_are_checked(counts, Hq, Hkv, d):
     table[1, 2] = -1
     binding.cache_weigh(q, lse, cache.k, cache.v, table, cache.seq_lens, cu, max(counts), weights=w, out=w)
     assert binding.fa_device_status(True) == binding.FA_ERR_PAGE
+
+
+@pytest.mark.parametrize("counts,Hq,Hkv,d", KERNELS)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_weights_of_idle_sequences_keep_their_bits(counts, Hq, Hkv, d, in_place):
+    """-0, NaN of any bits, infinities and subnormals too."""
+    cache, q, lse, w, cu = step(counts, Hq, Hkv, d)
+    some = ints([-(1 << 31), 0, 0x7fc12345, 0x7f800000, -0x800000, 1, -0x7fffffff, 0x3f800000])
+    pick = torch.randint(0, 8, w.shape, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    w.copy_(some[pick].view(torch.float32))
+    old = w.clone().view(torch.int32)
+    out = w if in_place else torch.full_like(w, 7.0)
+    binding.cache_weigh(q, lse, cache.k, cache.v, cache.table, cache.seq_lens, cu, max(counts), weights=w, decay=0.5, out=out)
+    for b in (0, 2):
+        assert torch.equal(out[b, :, :LENS[b]].contiguous().view(torch.int32), old[b, :, :LENS[b]])
