@@ -998,7 +998,8 @@ def cache_weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q=Non
     cache; cu_seqlens_q None: one token per sequence.  weights fp32 [B, Hkv, width] or None (nothing
     so far); out: the same sizes, weights itself for in place, or None for a new array of the width
     of weights or of the page table.  Places behind a sequence's last token are neither read nor
-    written (zeros in a new array).  A sequence without query tokens keeps its weights.
+    written (zeros in a new array).  A sequence without query tokens keeps its weights.  A row whose lse
+    is infinite adds nothing, whatever its query holds.
     """
     if workspace is None:
         done = (_calls or _fast()).weigh(q, lse, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal,

@@ -66,7 +66,7 @@ __device__ __forceinline__ void weigh_store(const WeighParams &p, int b, int h, 
     const long long at = (static_cast<long long>(b) * p.Hkv + h) * p.len + key;
     p.out[at] = !p.in ? sum : nq > 0 ? fmaf(p.decay, p.in[at], sum) : p.in[at];
 }
-// -lse in log2 units; a row that saw no key adds nothing.
+// -lse in log2 units.  -inf: the row adds nothing, whatever its products are.
 __device__ __forceinline__ float weigh_off(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
 
 int launch_weigh_tiles(const WeighLaunch &a, WeighParams p, const DeviceInfo &dev, cudaStream_t stream);

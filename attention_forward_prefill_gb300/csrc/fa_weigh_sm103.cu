@@ -146,11 +146,12 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_rows_kernel(const WeighPara
         float sum[2] = {0.f, 0.f}, c[4];
         auto add = [&](int r0, float off0, float off1) {
             const float off[2] = {off0, off1};
+            const bool counts[2] = {off0 != -INFINITY, off1 != -INFINITY};  // (rows that there are not have it too)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = r0 + quad * 2 + e;
-                if (r < rows && r >= see[0]) sum[0] += ex2_approx(fmaf(c[e], p.scale_log2, off[e]));
-                if (r < rows && r >= see[1]) sum[1] += ex2_approx(fmaf(c[2 + e], p.scale_log2, off[e]));
+                if (counts[e] && r >= see[0]) sum[0] += ex2_approx(fmaf(c[e], p.scale_log2, off[e]));
+                if (counts[e] && r >= see[1]) sum[1] += ex2_approx(fmaf(c[2 + e], p.scale_log2, off[e]));
             }
         };
         if constexpr (FEW) {

@@ -23,6 +23,10 @@
 // time 145, a product thread for each tile 138 (products alone 98, sums alone 120), hidden quarters
 // passed over 124, a whole chunk without a loop 118, two units' keys and two chunks of rows held instead
 // of one and four 116.
+// Rows whose log-sum-exp is infinite add nothing, whatever their products are: bits for the rows that count come with the
+// log-sum-exps, and chunks in which some do not are summed under them (4 chunks of 1024 tokens on 5000, 32 heads over 8,
+// d = 128, 116 us, with one row in a hundred left out 183).  To look for them costs 16 sequences of 4096 tokens, 128
+// rows, 0.8 us.
 // One chunk a unit (up to 128 rows), 16 sequences of 4096 tokens: 35 to 38 us for 134 MB (40 with one
 // unit's keys, 37 where the warps of both parities still met at every unit).
 #include <algorithm>
@@ -56,7 +60,9 @@ struct WeighLayout {
     static constexpr int kRowsOff = 2 * kKeySets * kTileBytes;
     static constexpr int kOffOff = kRowsOff + kRowStages * kTileBytes;  // [kOffStages][kOffChunks][kRows] floats
     static constexpr int kOddOff = kOffOff + kOffStages * kOffChunks * kRows * 4;    // [2][kM]: sums over the odd chunks
-    static constexpr int kBarOff = kOddOff + 2 * kM * 4;
+    static constexpr int kCountOff = kOddOff + 2 * kM * 4;  // [kOffStages][kOffChunks]: which of a chunk's rows count
+    static constexpr int kLiveOff = kCountOff + kOffStages * kOffChunks * 16;  // and how many it has; below 0: not all of them count
+    static constexpr int kBarOff = kLiveOff + kOffStages * kOffChunks * 4;
     // k_full[set][tile], k_empty[set][tile], q_full, q_empty, off_full, off_empty, s_full[tile][parity], s_free[tile][parity],
     // sum_full[tile], sum_free[tile], drain[tile]
     static constexpr int kNumBars = 4 * kKeySets + 2 * kRowStages + 2 * kOffStages + 8 + 4 + 2;
@@ -67,11 +73,11 @@ struct WeighLayout {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-// The weights of 8 rows' columns s, added to two pairs of sums; MASKED: of columns [lo, hi) alone.
+// The weights of 8 rows' columns s, added to two pairs of sums; MASKED: of the columns whose bits are set.
 // (Written stage by stage, so that eight exponentials are in flight: column by column, each waited for its
 // own chain of a load, a product and an exponential.)
 template <bool MASKED>
-__device__ __forceinline__ void add_weights(const uint32_t *s, const ulonglong2 *off, uint64_t scale2, int lo, int hi,
+__device__ __forceinline__ void add_weights(const uint32_t *s, const ulonglong2 *off, uint64_t scale2, uint32_t bits,
                                             uint64_t (&acc)[2]) {
     uint64_t x[4];
 #pragma unroll
@@ -91,7 +97,7 @@ __device__ __forceinline__ void add_weights(const uint32_t *s, const ulonglong2 
     }
     if constexpr (MASKED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = i >= lo && i < hi ? e[i] : 0.f;
+        for (int i = 0; i < 8; ++i) e[i] = bits >> i & 1 ? e[i] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i & 1] = fadd2(acc[i & 1], f2_pack(e[2 * i], e[2 * i + 1]));
@@ -113,6 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     WeighStart *start = reinterpret_cast<WeighStart *>(smem + L::kStartOff);
     long long *warp_sum = reinterpret_cast<long long *>(smem + L::kSumOff);
     float *offs = reinterpret_cast<float *>(smem + L::kOffOff);
+    uint32_t *counts = reinterpret_cast<uint32_t *>(smem + L::kCountOff);
+    int *live_rows = reinterpret_cast<int *>(smem + L::kLiveOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile_rows = p.tile_tokens * p.G;
 
@@ -270,6 +278,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kOffChunks; ++k)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) offs[(os * kOffChunks + k) * kRows + i * 32 + lane] = v[k][i];
+#pragma unroll
+                for (int k = 0; k < kOffChunks; ++k) {
+                    if (c0 + k >= u.c1) break;
+                    uint32_t is[4];  // the rows that count, as bits
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) is[i] = __ballot_sync(0xffffffffu, v[k][i] != -INFINITY);
+                    const int live = min(rows - (c0 + k) * tile_rows, tile_rows);
+                    const bool all = __popc(is[0]) + __popc(is[1]) + __popc(is[2]) + __popc(is[3]) == live;
+                    if (lane == 0) {
+                        reinterpret_cast<uint4 *>(counts)[os * kOffChunks + k] = make_uint4(is[0], is[1], is[2], is[3]);
+                        live_rows[os * kOffChunks + k] = all ? live : -live;
+                    }
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(off_full + os);
             }
@@ -292,12 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t ch0 = ch;
                 const int see = weigh_first_token(p, u.s, key) * p.G;  // the first row that sees the key
                 uint64_t acc[2] = {};  // two pairs of sums
-                const int c1 = u.c1, rows = u.s.nq * p.G;
+                const int c1 = u.c1;
                 for (int c0 = u.c0; ok && c0 < c1; c0 += kOffChunks, ++lots) {
                     const uint32_t os = lots % kOffStages;
                     if (!lanes_wait(off_full + os, (lots / kOffStages) & 1, abort_flag)) { ok = false; break; }
                     for (int c = c0; c < min(c1, c0 + kOffChunks); ++c, ++ch) {
                         if ((ch & 1) != odd) continue;
+                        const int live = live_rows[os * kOffChunks + c - c0];
                         if (!warp_wait(s_full + t * 2 + odd, (ch / 2) & 1, abort_flag)) { ok = false; break; }
                         tc_fence_after();
                         auto load = [&](int q, uint32_t (&s)[32]) {
@@ -310,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                             if (lane == 0) mbar_arrive(s_free + t * 2 + odd);
                         };
-                        // Columns [first, end) of the chunk are rows that see the key; what lies outside may be anything.
-                        const int first = see - c * tile_rows, end = tile_live ? min(rows - c * tile_rows, tile_rows) : 0;
+                        // Columns [first, live) of the chunk are rows that see the key; what lies outside may be anything.
+                        const int first = see - c * tile_rows;
                         const ulonglong2 *off = reinterpret_cast<const ulonglong2 *>(offs + (os * kOffChunks + c - c0) * kRows);
-                        if (__all_sync(0xffffffffu, first <= 0) && end >= (RAGGED ? max(tile_rows, kRows - 32) : kRows)) {
+                        if (__all_sync(0xffffffffu, first <= 0) && tile_live && live >= (RAGGED ? max(tile_rows, kRows - 32) : kRows)) {
 #pragma unroll
                             for (int q = 0; q < kRows / 32; ++q) {
                                 uint32_t s[32];
@@ -322,21 +344,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     if (RAGGED && q == kRows / 32 - 1)
-                                        add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, 0, end - q * 32 - i * 8, acc);
+                                        add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, ~(~0u << max(0, min(live - q * 32 - i * 8, 8))), acc);
                                     else
-                                        add_weights<false>(&s[i * 8], off + q * 8 + i * 2, scale2, 0, 8, acc);
+                                        add_weights<false>(&s[i * 8], off + q * 8 + i * 2, scale2, ~0u, acc);
                                 }
                             }
                         } else {
-                            // the quarters that any of the warp's keys are seen from
-                            const int q0 = max(0, __reduce_min_sync(0xffffffffu, first)) / 32, q1 = (end + 31) / 32;
+                            // the quarters that any of the warp's keys are seen from; of the rows those that count
+                            const uint32_t *is = counts + (os * kOffChunks + c - c0) * 4;
+                            const int q0 = max(0, __reduce_min_sync(0xffffffffu, first)) / 32, q1 = tile_live ? (abs(live) + 31) / 32 : 0;
 #pragma unroll 1
                             for (int q = q0; q < q1; ++q) {
                                 uint32_t s[32];
                                 load(q, s);
+                                const int hidden = first - q * 32;
+                                const uint32_t bits = hidden >= 32 ? 0u : is[q] & (~0u << max(hidden, 0));
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, first - q * 32 - i * 8, end - q * 32 - i * 8, acc);
+                                    add_weights<true>(&s[i * 8], off + q * 8 + i * 2, scale2, bits >> i * 8, acc);
                             }
                             release();
                         }

@@ -612,7 +612,8 @@ int fa_prefill_tree(const fa_paged_cache *cache, const void *q, void *out,
  * over the query rows of the sequence's tokens and the head's group that see the key.
  *   q : [total_q][Hq][d] in the cache's type, lse : fp32 [total_q][Hq], both as in the
  *     attention call over the same cache (fa_prefill_paged with the same causal and scale;
- *     a row with lse = -inf adds nothing); both may be NULL when total_q is 0
+ *     a row whose lse is infinite, as one without keys has it, adds nothing, whatever its
+ *     query holds); both may be NULL when total_q is 0
  *   cu_seqlens_q : device int32 [B + 1], or NULL: max_seqlen_q tokens for each sequence,
  *     total_q == B * max_seqlen_q
  *   weights : fp32 [B][num_heads][weights_len], or NULL (nothing so far)
