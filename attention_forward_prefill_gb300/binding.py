@@ -90,6 +90,9 @@ _SIGNATURES = {
     "fa_read_probe": (_i, [_vp, _sz, _vp, _vp]),
     "fa_version": (_i, []),
 }
+# where a call's arguments are whole numbers of 32 bits, and the first size that none of them takes
+_INTS = {name: tuple(i for i, t in enumerate(types) if t is _i) for name, (_, types) in _SIGNATURES.items()}
+_TOO_MANY = 1 << 30
 
 
 class PagedCacheArg(ctypes.Structure):
@@ -708,6 +711,9 @@ def _tables(device, page_table, seq_lens):
 
 def _run(name, device, *args):
     """The library's call `name` with `device` current, on its current stream."""
+    for i in _INTS[name]:  # (ctypes would cut them off)
+        if not -0x80000000 <= args[i] <= 0x7fffffff:
+            raise FaError(FA_ERR_SHAPE, name)
     torch = _torch()
     fn = getattr(_lib or load(), name)
     index = device.index
@@ -929,6 +935,8 @@ def tree_mask(parents, cu_seqlens_q, max_seqlen_q: int, seq_lens=None):
     if seq_lens is not None:
         _check_ints(device, "seq_lens", seq_lens, (B,))
         lens_ptr = seq_lens.data_ptr()
+    if max_seqlen_q >= _TOO_MANY:
+        raise FaError(FA_ERR_SHAPE, "fa_tree_mask")
     words = max(1, -(-int(max_seqlen_q) // 32))
     mask = torch.empty((total, words), dtype=torch.int32, device=device)
     positions = None if seq_lens is None else torch.empty_like(parents)
@@ -1060,7 +1068,7 @@ def cache_select(weights, seq_lens, budget: int, sink: int = 0, recent: int = 0)
     _check_weights("weights", weights, device, (None, None, None))
     B, heads, width = weights.shape
     _check_ints(device, "seq_lens", seq_lens, (B,))
-    if budget < 1:
+    if not 1 <= budget < _TOO_MANY:
         raise FaError(FA_ERR_SHAPE, "fa_cache_select")
     keep = torch.empty((B, heads, int(budget)), dtype=torch.int32, device=device)
     counts = torch.empty_like(seq_lens)

@@ -414,7 +414,7 @@ static PyObject *py_mask(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int most;
     void *stream, *words_at, *positions_at = NULL;
     if (n != 4 || !read_tensor(a[0], &parents) || !ints(a[0], &parents, 1, parents.device) || parents.size[0] < 1 ||
-        !ints(a[1], &cu, 1, parents.device) || cu.size[0] < 2 || !whole(a[2], &most) || most < 1)
+        !ints(a[1], &cu, 1, parents.device) || cu.size[0] < 2 || !whole(a[2], &most) || most < 1 || most > INT32_MAX / 2)
         GIVE_UP;
     lens.ptr = NULL;
     if (a[3] != Py_None && (!ints(a[3], &lens, 1, parents.device) || lens.size[0] != cu.size[0] - 1)) GIVE_UP;
@@ -478,7 +478,7 @@ static PyObject *py_select(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int budget, sink, recent;
     void *stream, *keep_at, *counts_at, *kept_at;
     if (n != 5 || !read_tensor(a[0], &w) || !floats(a[0], &w, 3, w.device) || !ints(a[1], &lens, 1, w.device) ||
-        lens.size[0] != w.size[0] || !whole(a[2], &budget) || budget < 1 || !whole(a[3], &sink) || !whole(a[4], &recent) ||
+        lens.size[0] != w.size[0] || !whole(a[2], &budget) || budget < 1 || budget > INT32_MAX / 2 || !whole(a[3], &sink) || !whole(a[4], &recent) ||
         !stream_of(w.device, &stream))
         GIVE_UP;
     PyObject *keep = of_sizes(a[1], Py_BuildValue("(LLi)", w.size[0], w.size[1], budget), &keep_at);
