@@ -953,7 +953,9 @@ def prefill_tree(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_se
     sequence's query tokens, and of the query tokens those whose bits are set in its row of the mask
     (int32 [T, words], as tree_mask makes them; any bits will do).
 
-    The rest as prefill_paged; the keys and values of the query tokens are in the cache already.
+    Keys that a token does not see may hold anything; a NaN or an infinity among the values of one query
+    token may reach the others of its sequence, other branches of a tree too.  The rest as
+    prefill_paged; the keys and values of the query tokens are in the cache already.
     """
     if out_dtype is None and workspace is None:
         done = (_calls or _fast()).tree(q, k_pages, v_pages, page_table, seq_lens, cu_seqlens_q, max_seqlen_q, mask, scale,

@@ -443,8 +443,8 @@ size_t fa_decode_noalloc_max_bytes(void);
  * A row with a score of NaN or +inf comes out NaN, its log-sum-exp too, as the
  * softmax of such scores is; one whose scores are all -inf counts as a row
  * without keys.  A NaN or an infinity among the values of a token reaches the rows
- * that see the token, and may reach rows of its sequence that a causal mask keeps
- * from it.
+ * that see the token, and may reach rows of its sequence that a causal mask, or a
+ * drafted tree's, keeps from it (a weight of 0 times infinity).
  * Scores, sums and joins are fp32.  The weights are rounded to the cache's type for
  * the product with the values, and the sum adds the rounded weights.
  */
@@ -589,6 +589,9 @@ int fa_tree_mask(const int32_t *parents, uint32_t *mask, int mask_words,
  * in its row of the mask (any bits, not only trees'; those of tokens behind the n-th count
  * for nothing).  With more query tokens than seq_lens[b] the first tokens have no key.
  * A row that sees no key gives zeros (lse -inf).
+ * Keys that a row does not see may hold anything.  Values have to be finite: a NaN or an
+ * infinity among the values of a drafted node may reach the other nodes of its sequence,
+ * those of other branches too, as the note on the cache says.
  *   mask : device [total_q][mask_words], 4-byte aligned, 32 * mask_words >= max_seqlen_q
  * The rest as fa_prefill_paged, the workspace too.
  */
