@@ -15,14 +15,9 @@ template <int NT, typename StepsOf>
 __device__ __forceinline__ void weigh_plan(const WeighParams &p, WeighStart &st, long long *warp_sum, int least, int *status,
                                            StepsOf steps_of) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.B + NT - 1) / NT;
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mine = 0;
+    const WeighShare share = weigh_share(p, tid, NT);
     bool bad = false;
-    for (int b = b0; b < b1; ++b) {
-        mine += steps_of(weigh_seq(p, b)) * p.Hkv;
-        bad |= weigh_seq_bad(p, b);
-    }
+    const long long mine = weigh_sum(p, share, steps_of, bad);
     if (bad && blockIdx.x == 0) record_status(status, FA_ERR_SEQ_LEN);
     long long incl = mine;
 #pragma unroll
@@ -39,25 +34,14 @@ __device__ __forceinline__ void weigh_plan(const WeighParams &p, WeighStart &st,
         if (w < warp) before += v;
         W += v;
     }
-    const int c = blockIdx.x, G = static_cast<int>(min(static_cast<long long>(gridDim.x), max(W / least, 1LL)));
-    const long long first = c < G ? c * W / G : W, end = c < G ? (c + 1) * W / G : W;
+    const WeighStart range = weigh_range(W, blockIdx.x, gridDim.x, least);
     if (tid == 0) {
-        st.W = W;
-        st.G = G;
-        st.first = first;
-        st.end = end;
+        st.W = range.W;
+        st.G = range.G;
+        st.first = range.first;
+        st.end = range.end;
     }
-    if (first < end && before <= first && first < before + mine) {
-        long long rem = first - before;
-        int b = b0;
-        for (; b < b1 - 1; ++b) {
-            const long long n = steps_of(weigh_seq(p, b)) * p.Hkv;
-            if (rem < n) break;
-            rem -= n;
-        }
-        st.b = b;
-        st.rem = rem;
-    }
+    weigh_find(p, range, share, before, mine, steps_of, st);
     __syncthreads();
 }
 

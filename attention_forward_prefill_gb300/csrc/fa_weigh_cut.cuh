@@ -1,5 +1,5 @@
 // fa_weigh_cut.cuh -- how the weighing of cached tokens is cut into equal ranges of work.
-// Plain arithmetic: tests/test_weigh_cut_host.py compiles this file for the host.
+// Plain arithmetic: tests/test_weigh_cut_host.py and tests/test_weigh_plan_host.py compile this file for the host.
 //
 // weigh_tiles_kernel.  A sequence's n query tokens give each kv head n * G query rows, in
 // chunks of tile_tokens whole tokens (kWeighRows rows at most).  A unit = (sequence, kv head, 256
@@ -100,6 +100,48 @@ struct WeighStart {
     long long W, first, end, rem;
     int b, G;  // G: CTAs with work
 };
+
+// Thread `tid` of NT adds up the steps of sequences [b0, b1).
+struct WeighShare {
+    int b0, b1;
+};
+__device__ __forceinline__ WeighShare weigh_share(const WeighParams &p, int tid, int NT) {
+    const int per = (p.B + NT - 1) / NT, b0 = min(tid * per, p.B);
+    return {b0, min(b0 + per, p.B)};
+}
+template <typename StepsOf>
+__device__ __forceinline__ long long weigh_sum(const WeighParams &p, const WeighShare &x, StepsOf steps_of, bool &bad) {
+    long long sum = 0;
+    for (int b = x.b0; b < x.b1; ++b) {
+        sum += steps_of(weigh_seq(p, b)) * p.Hkv;
+        bad |= weigh_seq_bad(p, b);
+    }
+    return sum;
+}
+// What CTA c of `ctas` gets of W steps; no more CTAs get any than there are lots of `least` steps.
+__device__ __forceinline__ WeighStart weigh_range(long long W, int c, int ctas, int least) {
+    WeighStart st;
+    st.W = W;
+    st.G = static_cast<int>(min(static_cast<long long>(ctas), max(W / least, 1LL)));
+    st.first = c < st.G ? c * W / st.G : W;
+    st.end = c < st.G ? (c + 1) * W / st.G : W;
+    return st;
+}
+// Where the range starts, if it is in this thread's share: `mine` steps behind `before` others.
+template <typename StepsOf>
+__device__ __forceinline__ void weigh_find(const WeighParams &p, const WeighStart &range, const WeighShare &x, long long before,
+                                           long long mine, StepsOf steps_of, WeighStart &st) {
+    if (range.first >= range.end || range.first < before || range.first >= before + mine) return;
+    long long rem = range.first - before;
+    int b = x.b0;
+    for (; b < x.b1 - 1; ++b) {
+        const long long n = steps_of(weigh_seq(p, b)) * p.Hkv;
+        if (rem < n) break;
+        rem -= n;
+    }
+    st.b = b;
+    st.rem = rem;
+}
 
 // The CTA whose range holds `step`.
 __device__ __forceinline__ int weigh_cta_of(long long step, long long W, int G) {
