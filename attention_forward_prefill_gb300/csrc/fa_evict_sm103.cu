@@ -81,7 +81,7 @@ __device__ __forceinline__ bool cluster_received(uint64_t *bar, uint32_t parity)
                  : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return done;
 }
-constexpr uint64_t kReceiveNs = 1500ull * 1000ull * 1000ull;
+constexpr uint64_t kReceiveNs = 1500ull * 1000ull * 1000ull, kLandNs = 1000ull * 1000ull;
 // False: it has not come within the limit.
 __device__ __forceinline__ bool cluster_receive(uint64_t *bar, uint32_t parity) {
     if (cluster_received(bar, parity)) return true;
@@ -233,11 +233,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
                 }
             }
     };
-    // Nobody leaves while others may still send to it.
+    // Nobody leaves while others may still send to it, or while what they have sent is on its way: whoever has waited
+    // in vain does not know what that is, so it stays for far longer than a store takes.
     auto give_up = [&] {
         if (lane == 0) record_status(&g_evict_status, FA_ERR_WATCHDOG);
         cluster_arrive();
         cluster_wait();
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kLandNs;) {}
     };
     int shift = 32;
 #pragma unroll 1
