@@ -17,18 +17,19 @@
 // each tile's products, and log-sum-exps in lots.  Every warp walks through the CTA's pieces
 // (fa_weigh_cut.cuh) by itself.  TMEM: S of (tile, parity).
 //
-// 4 chunks of 700 to 2048 tokens on up to 11048, 32 heads over 8, d = 128: 116 us (1226 TFLOP/s; tensor pipe
-// 56% active, exponential unit 55%, issue 57%), of which the start takes 8 and the join 5.  Before: eight
+// 4 chunks of 700 to 2048 tokens on up to 11048, 32 heads over 8, d = 128: 115 us (1234 TFLOP/s; tensor pipe
+// 56% active, exponential unit 55%, issue 57%) again and again on the same inputs, whose keys stay in L2, and 131 among
+// calls on others; the start takes 8 of them and the join 5.  Before: eight
 // summing warps 230, a branch for every quarter of a chunk 159, sixteen warps and eight columns at a
-// time 145, a product thread for each tile 138 (products alone 98, sums alone 120), hidden quarters
+// time 145, a product thread for each tile 138, hidden quarters
 // passed over 124, a whole chunk without a loop 118, two units' keys and two chunks of rows held instead
 // of one and four 116.
 // Rows whose log-sum-exp is infinite add nothing, whatever their products are: bits for the rows that count come with the
 // log-sum-exps, and chunks in which some do not are summed under them (4 chunks of 1024 tokens on 5000, 32 heads over 8,
-// d = 128, 116 us, with one row in a hundred left out 183).  To look for them costs 16 sequences of 4096 tokens, 128
-// rows, 0.8 us.
-// One chunk a unit (up to 128 rows), 16 sequences of 4096 tokens: 35 to 38 us for 134 MB (40 with one
-// unit's keys, 37 where the warps of both parities still met at every unit).
+// d = 128, 115 us, with one row in a hundred left out 183).
+// One chunk a unit (up to 128 rows), 16 sequences of 4096 tokens: 34 to 36 us for 134 MB (40 with one
+// unit's keys, 37 where the warps of both parities still met at every unit, 36 to 39 where the log-sum-exps' warp went
+// through four chunks whether they were there or not: it is in the way of short units).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -267,23 +268,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kOffChunks; ++k) {
                     const int c = c0 + k;
+                    if (c >= u.c1) break;
                     const float *lse = p.lse + (static_cast<long long>(u.s.t0) + c * p.tile_tokens) * p.Hq + u.h * p.G;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        v[k][i] = c < u.c1 && at[i] >= 0 && c * tile_rows + i * 32 + lane < rows ? weigh_off(__ldg(lse + at[i])) : -INFINITY;
+                        v[k][i] = at[i] >= 0 && c * tile_rows + i * 32 + lane < rows ? __ldg(lse + at[i]) : -INFINITY;
                 }
                 const uint32_t os = ch % kOffStages;
                 if (ch >= kOffStages && !lanes_wait(off_empty + os, (ch / kOffStages - 1) & 1, abort_flag)) { ok = false; break; }
-#pragma unroll
-                for (int k = 0; k < kOffChunks; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) offs[(os * kOffChunks + k) * kRows + i * 32 + lane] = v[k][i];
 #pragma unroll
                 for (int k = 0; k < kOffChunks; ++k) {
                     if (c0 + k >= u.c1) break;
                     uint32_t is[4];  // the rows that count, as bits
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) is[i] = __ballot_sync(0xffffffffu, v[k][i] != -INFINITY);
+                    for (int i = 0; i < 4; ++i) {
+                        const float off = weigh_off(v[k][i]);
+                        offs[(os * kOffChunks + k) * kRows + i * 32 + lane] = off;
+                        is[i] = __ballot_sync(0xffffffffu, off != -INFINITY);
+                    }
                     const int live = min(rows - (c0 + k) * tile_rows, tile_rows);
                     const bool all = __popc(is[0]) + __popc(is[1]) + __popc(is[2]) + __popc(is[3]) == live;
                     if (lane == 0) {
@@ -467,10 +469,10 @@ size_t part_bytes(int num_sms) { return static_cast<size_t>(num_sms) * 2 * kWeig
 
 // Which kernel: the tiles' takes about as long for one row of a kv head as for 128, the warp products' some more with
 // every eight.  In us, theirs against the tiles':
-//   16 sequences of 4096, 32 heads over 8, d = 128:   8 rows 28 : 35, 16 rows 45 : 35, 32 rows 64 : 35, 128 rows 183 : 38
-//   4 of 16384, 12 heads, d = 64:                     8 rows 24 : 40, 12 rows 45 : 40, 24 rows 56 : 40, 128 rows 215 : 41
-//   32 of 1000, 64 over 8, d = 128:                   8 rows 13 : 21, 16 rows 22 : 21, 32 rows 32 : 22, 128 rows 92 : 26
-//   1 of 4096, 32 over 8, d = 128 (its start counts): 8 rows  6 : 11, 32 rows  9 : 11, 48 rows 10 : 11, 64 rows 12 : 11
+//   16 sequences of 4096, 32 heads over 8, d = 128:   8 rows 28 : 34, 16 rows 46 : 34, 32 rows 66 : 34, 128 rows 189 : 36
+//   4 of 16384, 12 heads, d = 64:                     8 rows 24 : 37, 12 rows 45 : 37, 24 rows 57 : 37, 128 rows 217 : 38
+//   32 of 1000, 64 over 8, d = 128:                   8 rows 13 : 22, 16 rows 22 : 21, 32 rows 33 : 21, 128 rows 96 : 25
+//   1 of 4096, 32 over 8, d = 128 (its start counts): 8 rows  6 : 11, 32 rows  9 : 11, 48 rows 11 : 11, 64 rows 13 : 11
 bool weigh_in_tiles(const WeighLaunch &a, int num_sms) {
     const int group = a.Hq / a.c.num_heads;
     const long long rows = static_cast<long long>(a.max_q) * group;
