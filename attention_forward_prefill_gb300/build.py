@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["fa_api.cu", "fa_prefill_sm103.cu", "fa_decode_sm103.cu", "fa_backward_sm103.cu",
            "fa_paged_api.cu", "fa_paged_sm103.cu", "fa_paged_tiles_sm103.cu",
            "fa_paged_cluster_sm103.cu", "fa_cache_sm103.cu", "fa_tree_sm103.cu", "fa_weigh_sm103.cu",
-           "fa_weigh_tiles_sm103.cu",            "fa_evict_sm103.cu"]
+           "fa_weigh_tiles_sm103.cu", "fa_evict_sm103.cu"]
 # The CPython module in front of the paged-cache calls (host code only).
 CALLS_SOURCE = "paged_calls.c"
 CALLS_PATH = os.path.join(HERE, "_paged_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))

@@ -148,7 +148,7 @@ int fa_device_status(int reset) {
     if (cudaDeviceSynchronize() != cudaSuccess) return -1;
     const int words[11] = {read_prefill_status(reset), read_decode_status(reset), read_backward_status(reset),
                           read_paged_status(reset), read_tiles_status(reset), read_cluster_status(reset), read_append_status(reset),
-                           read_tree_status(reset), read_weigh_status(reset), read_weigh_tiles_status(reset), read_evict_status(reset)};
+                          read_tree_status(reset), read_weigh_status(reset), read_weigh_tiles_status(reset), read_evict_status(reset)};
     int first = 0;
     for (int v : words) {
         if (v < 0) return -1;
