@@ -1,7 +1,7 @@
 """Whole numbers that do not fit the library's 32 bits are refused, not cut off (no GPU)."""
 import pytest
 
-from attention_forward_prefill_gb300 import binding
+from attention_forward_prefill_gb300 import binding, build
 
 BIG = [1 << 31, (1 << 32) + 9, -(1 << 31) - 1, -(1 << 32) + 9, 1 << 70]
 
@@ -9,6 +9,7 @@ BIG = [1 << 31, (1 << 32) + 9, -(1 << 31) - 1, -(1 << 32) + 9, 1 << 70]
 @pytest.fixture(scope="module", autouse=True)
 def lib():
     pytest.importorskip("torch")
+    build.build()
     binding.load()
 
 
